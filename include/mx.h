@@ -521,6 +521,173 @@ typedef struct {
 
 int mx_grouped_gemm(const mx_grouped_args* args, void* stream);
 
+/* ---------------------------------------------------------------- linear operators */
+/*
+ * A linear layer at any number of tokens, trained with its activations kept
+ * in 8 bits: the GEMM with bias, activation and residual in its epilogue
+ * (mx_gemm_act), activation checkpoints (mx_checkpoint_save / _load), the
+ * packs of the backward GEMMs straight from checkpoints (mx_quantize_saved)
+ * and the whole backward pass (mx_linear_bwd_saved).  Where the calls above
+ * need multiples of 256 (or 32 rows), these take any row count, widths in
+ * multiples of 32 (one MX block) and row pitches.
+ */
+
+/* Activations of the linear operators:
+ *  GELU_TANH  x s(z), z = 2 sqrt(2/pi) (x + 0.044715 x^3);  SILU  x s(x);
+ *  s(z) = 1/(1+exp(-z)).  Evaluated in binary32 with the hardware's exp2 and
+ *  reciprocal: within a few ulps, not the bit-exact contract of mx_prologue. */
+typedef enum { MX_ACT_NONE = 0, MX_ACT_GELU_TANH = 1, MX_ACT_SILU = 2 } mx_act;
+
+/*
+ * mx_gemm_act -- with P[m][n] = sum_k A[m][k] * B[n][k] + bias[n] in
+ * binary32:
+ *   C = act(P) + residual, rounded once to c_dtype, and
+ *   saved = the 8-bit checkpoint of the unrounded P (what
+ *           mx_checkpoint_save makes of it), for the backward pass.
+ *
+ *  M            rows, any number >= 0 (one token included).
+ *  N, K         multiples of 32.  K is the operands' packed length (for a
+ *               columnwise pack of R rows, R rounded up to 32); the pad codes
+ *               and scales of their last K group must be zero, as every pack
+ *               writes them.  K = 0 gives P = bias.
+ *  fmt, act     element format of A and B; an mx_act.
+ *  bias         [N] of bias_dtype, or NULL.
+ *  residual     [M][ldr] of c_dtype, or NULL.  It may be C itself (with
+ *               ldr = ldc): C is then accumulated into, e.g. a weight gradient
+ *               into its main_grad.  No other overlap of C or saved with an
+ *               input is allowed.
+ *  C            [M][ldc] of c_dtype, or NULL where only the checkpoint is
+ *               wanted (then no residual).
+ *  ldr, ldc     row pitches in elements, >= N, multiples of 8; elements
+ *               between N and the pitch are left as they are.
+ *  saved        E4M3 operand [M] x K=N, or {NULL, NULL}.
+ * Errors: MX_ERR_NULL, MX_ERR_SHAPE, MX_ERR_ALIGN, MX_ERR_FORMAT,
+ * MX_ERR_INDEX_OVERFLOW, MX_ERR_DEVICE, MX_ERR_LAUNCH.  M = 0 or N = 0
+ * enqueues nothing (pointers may then be NULL, and A and B may be where
+ * K = 0).  The accumulation order depends on M, N and whether a checkpoint
+ * is asked for, never on timing.
+ */
+typedef struct {
+  int64_t M, N, K;
+  int32_t fmt;
+  int32_t act;
+  mx_packed A, B;
+  const void* bias;
+  const void* residual;
+  void* C;
+  int64_t ldr, ldc;
+  int32_t bias_dtype, c_dtype;
+  mx_packed saved;
+} mx_gemm_act_args;
+
+int mx_gemm_act(const mx_gemm_act_args* args, void* stream);
+
+/*
+ * mx_checkpoint_save -- x [R][ldx] (x_dtype) to its 8-bit checkpoint, the
+ * rowwise MXFP8 operand [R] x K=C (E4M3, RCEIL scales; for bf16 the bytes
+ * mx_quantize writes).  8.25 bits a value; also the A operand of an MXFP8
+ * mx_gemm_act at any row count.  A value is off by at most 2^-4 of itself,
+ * or 2^-18 of its block's largest value where that is more; a block
+ * holding a NaN or Inf reads back as NaN throughout.
+ *
+ * mx_checkpoint_load -- the values that a checkpoint stands for, into
+ * y [R][ldy] (y_dtype); exact but for bf16 subnormals.  Reads any E4M3
+ * operand.
+ *
+ *  R            any number >= 0; R = 0 or C = 0 enqueues nothing.
+ *  C            a multiple of 32.
+ *  ldx, ldy     row pitches in elements, >= C, multiples of 8.
+ * Errors: MX_ERR_NULL, MX_ERR_SHAPE, MX_ERR_ALIGN, MX_ERR_FORMAT (dtype),
+ * MX_ERR_INDEX_OVERFLOW (more than 2^31 workgroups), MX_ERR_DEVICE,
+ * MX_ERR_LAUNCH.
+ */
+int mx_checkpoint_save(const void* x, int x_dtype, int64_t R, int64_t C, int64_t ldx, void* codes, void* scales,
+                       void* stream);
+int mx_checkpoint_load(const void* codes, const void* scales, int64_t R, int64_t C, void* y, int y_dtype,
+                       int64_t ldy, void* stream);
+
+/*
+ * mx_quantize_saved -- pack v [R][C] into GEMM operands, where
+ *   x == NULL:  v = act(s)          (an activation recomputed),
+ *   x != NULL:  v = x * act'(s)     (the gradient before the activation),
+ *               or x itself with MX_ACT_NONE,
+ * s being the checkpoint `saved`; formed in binary32 and rounded to bf16.
+ *
+ *  x            bf16 [R][ldx] or NULL.  ldx >= C, a multiple of 8.
+ *  saved        E4M3 operand [R] x K=C; {NULL, NULL} exactly where x is given
+ *               and act is MX_ACT_NONE.
+ *  R            any number >= 0.  C: a multiple of 32.
+ *  fmt, scale_mode, hadamard   as mx_quantize.
+ *  row          rowwise operand [R] x K=C, or {NULL, NULL}.
+ *  col          columnwise operand [C] x K = R rounded up to 32, or {NULL,
+ *               NULL}; rows past R are packed as zeros.
+ *  colsum_partials  binary32 [ceil(R/128)][C]: sums of v over 128-row blocks,
+ *               of the binary32 values before their rounding to bf16.
+ *  colsum       binary32 [C]: the partials summed in order (zeros if R = 0).
+ *               Requires colsum_partials.
+ * At least one of row, col and colsum_partials.  Errors as mx_quantize.
+ */
+typedef struct {
+  int64_t R, C;
+  int32_t fmt, scale_mode, hadamard;
+  int32_t act;
+  const void* x;
+  int64_t ldx;
+  mx_packed saved;
+  mx_packed row, col;
+  float* colsum_partials;
+  float* colsum;
+} mx_quantize_saved_args;
+
+int mx_quantize_saved(const mx_quantize_saved_args* args, void* stream);
+
+/*
+ * mx_linear_bwd_saved -- the backward pass of Y = act(X W^T + b) (+ residual,
+ * whose gradient is dY itself) from 8-bit checkpoints of the pre-activation
+ * (mx_gemm_act's `saved`) and of the input, where X = x_act(saved_x):
+ *   G  = dY * act'(saved_pre)         bf16, packed as it is formed
+ *   db = sum of G over the tokens     binary32, before G's rounding
+ *   dX = Q(G) . Q(W)                  [M][K], W's columns packed by the caller
+ *   dW = Q(G^T) . Q(X^T)^T            [N][K]
+ * Q packs to fmt along the product's inner dimension.  Composed of
+ * mx_quantize_saved and mx_gemm_act, with their results.
+ *
+ *  M            tokens, any number >= 0.  N (out), K (in): multiples of 32.
+ *  act, x_act   mx_act of the layer and of its input.
+ *  dY           bf16 [M][lddy].
+ *  saved_pre    E4M3 [M] x K=N; {NULL, NULL} exactly where act is NONE.
+ *  saved_x      E4M3 [M] x K=K; needed for dW.
+ *  Wc           fmt operand [K] x K=N (columns of W); needed for dX.
+ *  dX           bf16 [M][lddx], or NULL to skip it.
+ *  dW           dw_dtype [N][lddw], or NULL to skip it; accumulate = 1 adds
+ *               the gradient into it, 0 overwrites it.
+ *  db           binary32 [N] with db_partials [ceil(M/128)][N], or NULL.
+ *  dPr, dPc, Xc work operands of fmt: [M] x K=N (for dX); [N] and [K] x K = M
+ *               rounded up to 32 (for dW).
+ * M = 0 sets dW (unless accumulating) and db to zero.  Errors: as the
+ * calls it is made of; nothing is enqueued on an error.
+ */
+typedef struct {
+  int64_t M, N, K;
+  int32_t fmt, scale_mode, hadamard;
+  int32_t act, x_act;
+  int32_t accumulate;
+  const void* dY;
+  int64_t lddy;
+  mx_packed saved_pre, saved_x, Wc;
+  void* dX;
+  int64_t lddx;
+  void* dW;
+  int64_t lddw;
+  int32_t dw_dtype;
+  int32_t reserved;       /* 0 */
+  float* db;
+  float* db_partials;
+  mx_packed dPr, dPc, Xc;
+} mx_linear_bwd_args;
+
+int mx_linear_bwd_saved(const mx_linear_bwd_args* args, void* stream);
+
 /* ---------------------------------------------------------------- misc */
 /* Human-readable name of a status code (static string). */
 const char* mx_status_str(int status);

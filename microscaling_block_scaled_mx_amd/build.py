@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmx.so")
-SOURCES = ["mx_api.hip", "mx_pack.hip", "mx_gemm.hip"]
+SOURCES = ["mx_api.hip", "mx_pack.hip", "mx_gemm.hip", "mx_gemm_act.hip", "mx_saved.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off",

@@ -1,0 +1,136 @@
+// Activations and the 8-bit checkpoint format of the linear operators
+// (mx_gemm_act, mx_checkpoint_*, mx_quantize_saved): binary32 device
+// functions.
+//
+// With z = 2u = 2 sqrt(2/pi) (x + 0.044715 x^3) for the tanh form of GELU and
+// z = x for SiLU, and s = 1 / (1 + exp(-z)), (1 + tanh u) / 2 = s, so
+//   act(x)  = x s,
+//   act'(x) = s + x z'(x) s (1 - s).
+// exp2 and the reciprocal are the hardware's (each within 1 ulp): 6 vector
+// instructions and two quarter-rate ones per value where the packers'
+// bit-exact contract (mx_device.h) takes about 45.  Results differ from
+// that contract's by a few binary32 ulps before their one rounding to bf16.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "mx_device.h"
+
+namespace mx {
+
+enum Act { kActNone = 0, kActGelu = 1, kActSilu = 2 };
+
+// 1 / (1 + 2^(-t))
+__device__ __forceinline__ float sigmoid2(float t) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-t));
+#else
+  return t;
+#endif
+}
+
+// z(x) log2(e): the exponent of sigmoid2
+template <int ACT>
+__device__ __forceinline__ float act_exponent(float x) {
+  if constexpr (ACT == kActGelu) {
+    const float A = 0x1.26aec2p+1f;   // 2 sqrt(2/pi) log2(e)
+    const float B = 0x1.a5a7d0p-4f;   // 0.044715 A
+    return x * __builtin_fmaf(x * x, B, A);
+  } else {
+    return x * 0x1.715476p+0f;  // log2(e)
+  }
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_value(float x) {
+  if constexpr (ACT == kActNone) return x;
+  return x * sigmoid2(act_exponent<ACT>(x));
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_slope(float x) {
+  if constexpr (ACT == kActNone) return 1.0f;
+  const float s = sigmoid2(act_exponent<ACT>(x));
+  const float w = s * (1.0f - s);  // 0 once |z| passes 25: the slope's second term is then below its rounding
+  if constexpr (ACT == kActGelu) {
+    const float C = 0x1.988454p+0f, D = 0x1.b6676cp-3f;  // z' = C + D x^2
+    const float xz = x * __builtin_fmaf(x * x, D, C);
+    return __builtin_fmaf(w == 0.0f ? 0.0f : xz, w, s);  // (0 inf is no NaN here)
+  } else {
+    return __builtin_fmaf(w == 0.0f ? 0.0f : x, w, s);
+  }
+}
+
+// 2^(byte - 127) of an E8M0 scale; 0 gives 2^-127 (a subnormal), 0xff gives
+// +inf, so that the zero codes of a NaN block decode to NaN.
+__device__ __forceinline__ float e8m0_value(uint32_t byte) {
+  return __uint_as_float(byte == 0u ? 0x00400000u : byte << 23);
+}
+
+// Four E4M3 codes (one dword) times a scale.
+__device__ __forceinline__ void e4m3_decode4(uint32_t w, float scale, float (&v)[4]) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  const f2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
+  const f2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+  v[0] = lo.x * scale;
+  v[1] = lo.y * scale;
+  v[2] = hi.x * scale;
+  v[3] = hi.y * scale;
+#endif
+}
+
+// Four values to E4M3 codes under scale byte `s` (RCEIL: |v| <= 448 2^X, so
+// nothing saturates).  The conversion divides by 2^X exactly; a block with
+// X = -127 is converted as (v 2^64) / 2^-63, and a NaN block's codes are 0.
+__device__ __forceinline__ uint32_t e4m3_encode4(const float (&v)[4], uint32_t s) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef short s2 __attribute__((ext_vector_type(2)));
+  const bool tiny = s == 0u;
+  const float up = tiny ? 0x1p64f : 1.0f;
+  const float sc = __uint_as_float((tiny ? 64u : (s == 0xffu ? 127u : s)) << 23);
+  s2 q = {0, 0};
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(q, v[0] * up, v[1] * up, sc, false);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(q, v[2] * up, v[3] * up, sc, true);
+  return s == 0xffu ? 0u : __builtin_bit_cast(uint32_t, q);
+#else
+  return 0u;
+#endif
+}
+
+// Largest |v| of four values as a bit pattern (a NaN sorts above infinity).
+__device__ __forceinline__ uint32_t abs_max4(const float (&v)[4], uint32_t m = 0u) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t b = __float_as_uint(v[i]) & 0x7fffffffu;
+    m = m > b ? m : b;
+  }
+  return m;
+}
+
+// One step of a reduction within a row of 16 lanes: the value of the lane
+// that DPP control `CTRL` names.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_move(uint32_t v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
+#else
+  return v;
+#endif
+}
+constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppHalfMirror = 0x141, kDppRor4 = 0x124, kDppRor8 = 0x128;
+
+__device__ __forceinline__ uint32_t max_u32(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// Maximum over the 4 (8) lanes of an aligned group.
+__device__ __forceinline__ uint32_t max_over4(uint32_t v) {
+  v = max_u32(v, dpp_move<kDppXor1>(v));
+  return max_u32(v, dpp_move<kDppXor2>(v));
+}
+__device__ __forceinline__ uint32_t max_over8(uint32_t v) {
+  v = max_over4(v);
+  return max_u32(v, dpp_move<kDppHalfMirror>(v));  // lane i of 8 takes lane 7 - i's: the other four
+}
+
+}  // namespace mx

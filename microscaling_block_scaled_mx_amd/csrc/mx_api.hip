@@ -8,6 +8,7 @@
 
 #include "mx.h"
 #include "mx_kernels.h"
+#include "mx_linear.h"
 
 namespace {
 
@@ -207,6 +208,125 @@ __global__ __launch_bounds__(64) void clock_sample_kernel(uint64_t wall_ticks, u
 
 bool packed_ok(const mx_packed& q) { return q.codes && q.scales; }
 bool packed_aligned(const mx_packed& q) { return aligned16(q.codes) && aligned16(q.scales); }
+
+// ---------------------------------------------------------------- linear operators
+bool packed_none(const mx_packed& q) { return !q.codes && !q.scales; }
+uint8_t* bytes(void* p) { return static_cast<uint8_t*>(p); }
+bool act_ok(int act) { return act >= MX_ACT_NONE && act <= MX_ACT_SILU; }
+bool dtype_ok(int d) { return d == MX_BF16 || d == MX_F32; }
+int64_t up32(int64_t n) { return (n + 31) / 32 * 32; }
+// sizes past this are refused before they are multiplied
+constexpr int64_t kMaxExtent = 1ll << 40;
+// row pitch of an [R][C] tensor: in 8-element steps, the last row's end addressable
+bool pitch_ok(int64_t ld, int64_t C) { return ld >= C && ld % 8 == 0 && ld <= kMaxExtent; }
+
+int validate_gemm_act(const mx_gemm_act_args& a) {
+  if (bits_of(a.fmt) == 0 || !act_ok(a.act) || !dtype_ok(a.c_dtype) || !dtype_ok(a.bias_dtype)) return MX_ERR_FORMAT;
+  if (a.M < 0 || a.N < 0 || a.K < 0 || a.N % 32 || a.K % 32) return MX_ERR_SHAPE;
+  if (a.M > kMaxExtent || a.N > kMaxExtent || a.K > kMaxExtent) return MX_ERR_INDEX_OVERFLOW;
+  if (packed_ok(a.saved) == packed_none(a.saved)) return MX_ERR_NULL;  // half a pair
+  if (a.C && !pitch_ok(a.ldc, a.N)) return MX_ERR_SHAPE;
+  if (a.residual && !pitch_ok(a.ldr, a.N)) return MX_ERR_SHAPE;
+  if (a.residual && a.residual == a.C && a.ldr != a.ldc) return MX_ERR_SHAPE;
+  const void* ptrs[] = {a.A.codes, a.A.scales, a.B.codes, a.B.scales, a.bias,
+                        a.residual, a.C, a.saved.codes, a.saved.scales};
+  for (const void* q : ptrs)
+    if (q && !aligned16(q)) return MX_ERR_ALIGN;
+  // 32-bit byte offsets into an operand; output tiles of 16 x 16 at least
+  const int64_t kp = (a.K + 127) / 128 * 128;
+  for (int64_t rows : {a.M, a.N}) {
+    if (rows > kMaxOperandBytes) return MX_ERR_INDEX_OVERFLOW;
+    if (rows > 0 && kp * bits_of(a.fmt) / 8 > kMaxOperandBytes / rows) return MX_ERR_INDEX_OVERFLOW;
+  }
+  if (!grid_fits(((a.M + 15) / 16) * ((a.N + 15) / 16), 1, 1)) return MX_ERR_INDEX_OVERFLOW;
+  if (a.M == 0 || a.N == 0) return MX_OK;
+  if (!a.C && packed_none(a.saved)) return MX_ERR_NULL;
+  if (a.residual && !a.C) return MX_ERR_NULL;
+  if (a.K > 0 && (!packed_ok(a.A) || !packed_ok(a.B))) return MX_ERR_NULL;
+  return MX_OK;
+}
+
+int gemm_act_launch(const mx_gemm_act_args& a, hipStream_t s) {
+  if (a.M == 0 || a.N == 0) return MX_OK;
+  mx::GemmActParams p;
+  memset(&p, 0, sizeof p);
+  p.a_codes = bytes(a.A.codes);
+  p.a_scales = bytes(a.A.scales);
+  p.b_codes = bytes(a.B.codes);
+  p.b_scales = bytes(a.B.scales);
+  p.M = a.M;
+  p.N = a.N;
+  p.K = p.ktot = a.K;
+  p.bias = a.bias;
+  p.bias_f32 = a.bias_dtype == MX_F32;
+  p.c = a.C;
+  p.ldc = a.ldc;
+  p.c_f32 = a.c_dtype == MX_F32;
+  p.residual = a.residual;
+  p.ldr = a.ldr;
+  p.act = a.act;
+  p.saved_codes = bytes(a.saved.codes);
+  p.saved_scales = bytes(a.saved.scales);
+  return launched(mx::launch_gemm_act(p, a.fmt, s));
+}
+
+int validate_checkpoint(const void* x, int dtype, int64_t R, int64_t C, int64_t ld, const void* codes,
+                        const void* scales) {
+  if (!dtype_ok(dtype)) return MX_ERR_FORMAT;
+  if (R < 0 || C < 0 || C % 32 || !pitch_ok(ld, C)) return MX_ERR_SHAPE;
+  if (R > kMaxExtent || C > kMaxExtent) return MX_ERR_INDEX_OVERFLOW;
+  const void* ptrs[] = {x, codes, scales};
+  for (const void* q : ptrs)
+    if (q && !aligned16(q)) return MX_ERR_ALIGN;
+  const int64_t gx = (C + 127) / 128, gy = (R + 63) / 64;
+  if (gx > 0 && gy >= ((1ll << 31) + gx - 1) / gx) return MX_ERR_INDEX_OVERFLOW;
+  if (R > 0 && C > 0 && (!x || !codes || !scales)) return MX_ERR_NULL;
+  return MX_OK;
+}
+
+int validate_quantize_saved(const mx_quantize_saved_args& a) {
+  if (!combo_ok(a.fmt, a.scale_mode, a.hadamard) || !act_ok(a.act)) return MX_ERR_FORMAT;
+  if (a.R < 0 || a.C < 0 || a.C % 32) return MX_ERR_SHAPE;
+  if (a.R > kMaxExtent || a.C > kMaxExtent) return MX_ERR_INDEX_OVERFLOW;
+  for (const mx_packed* q : {&a.saved, &a.row, &a.col})
+    if (packed_ok(*q) == packed_none(*q)) return MX_ERR_NULL;
+  if (a.colsum && !a.colsum_partials && a.R > 0) return MX_ERR_NULL;
+  if (a.x && !pitch_ok(a.ldx, a.C)) return MX_ERR_SHAPE;
+  const void* ptrs[] = {a.x, a.saved.codes, a.saved.scales, a.row.codes, a.row.scales,
+                        a.col.codes, a.col.scales, a.colsum_partials, a.colsum};
+  for (const void* q : ptrs)
+    if (q && !aligned16(q)) return MX_ERR_ALIGN;
+  const int64_t gx = (a.C + 127) / 128, gy = (a.R + 127) / 128;
+  if (gx > 0 && gy >= ((1ll << 31) + gx - 1) / gx) return MX_ERR_INDEX_OVERFLOW;
+  if (a.R == 0 || a.C == 0) return MX_OK;
+  if (a.x && a.act == MX_ACT_NONE && packed_ok(a.saved)) return MX_ERR_FORMAT;
+  if ((!a.x || a.act != MX_ACT_NONE) && packed_none(a.saved)) return MX_ERR_NULL;
+  if (packed_none(a.row) && packed_none(a.col) && !a.colsum_partials) return MX_ERR_NULL;
+  return MX_OK;
+}
+
+int quantize_saved_launch(const mx_quantize_saved_args& a, hipStream_t s) {
+  if (a.C == 0) return MX_OK;
+  int st = MX_OK;
+  if (a.R > 0) {
+    mx::SavedPackParams p;
+    p.x = static_cast<const uint16_t*>(a.x);
+    p.ldx = a.ldx;
+    p.saved_codes = bytes(a.saved.codes);
+    p.saved_scales = bytes(a.saved.scales);
+    p.R = a.R;
+    p.C = a.C;
+    p.row_codes = bytes(a.row.codes);
+    p.row_scales = bytes(a.row.scales);
+    p.col_codes = bytes(a.col.codes);
+    p.col_scales = bytes(a.col.scales);
+    p.partials = a.colsum_partials;
+    st = launched(mx::launch_quantize_saved(p, a.fmt, a.scale_mode, a.hadamard, a.act, s));
+  }
+  if (st == MX_OK && a.colsum)  // no rows: no partials, zeros
+    st = launched(mx::launch_colsum_finish(a.colsum_partials, (a.R + 127) / 128, a.C, a.colsum, 1, s));
+  return st;
+}
 
 }  // namespace
 
@@ -674,6 +794,119 @@ int mx_grouped_gemm(const mx_grouped_args* a, void* stream) {
   p.ktot = a->R;
   p.ldc = a->N;
   return launched(mx::launch_gemm(p, a->fmt, mx::kRaggedK, mx::kEpiStore, s));
+}
+
+int mx_gemm_act(const mx_gemm_act_args* args, void* stream) {
+  if (!args) return MX_ERR_NULL;
+  int st = validate_gemm_act(*args);
+  if (st != MX_OK) return st;
+  if ((st = check_device()) != MX_OK) return st;
+  return gemm_act_launch(*args, static_cast<hipStream_t>(stream));
+}
+
+int mx_checkpoint_save(const void* x, int x_dtype, int64_t R, int64_t C, int64_t ldx, void* codes, void* scales,
+                       void* stream) {
+  int st = validate_checkpoint(x, x_dtype, R, C, ldx, codes, scales);
+  if (st != MX_OK) return st;
+  if ((st = check_device()) != MX_OK) return st;
+  return launched(mx::launch_checkpoint_save(x, x_dtype == MX_F32, R, C, ldx, bytes(codes), bytes(scales),
+                                             static_cast<hipStream_t>(stream)));
+}
+
+int mx_checkpoint_load(const void* codes, const void* scales, int64_t R, int64_t C, void* y, int y_dtype, int64_t ldy,
+                       void* stream) {
+  int st = validate_checkpoint(y, y_dtype, R, C, ldy, codes, scales);
+  if (st != MX_OK) return st;
+  if ((st = check_device()) != MX_OK) return st;
+  return launched(mx::launch_checkpoint_load(static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales),
+                                             R, C, y, y_dtype == MX_F32, ldy, static_cast<hipStream_t>(stream)));
+}
+
+int mx_quantize_saved(const mx_quantize_saved_args* args, void* stream) {
+  if (!args) return MX_ERR_NULL;
+  int st = validate_quantize_saved(*args);
+  if (st != MX_OK) return st;
+  if ((st = check_device()) != MX_OK) return st;
+  return quantize_saved_launch(*args, static_cast<hipStream_t>(stream));
+}
+
+int mx_linear_bwd_saved(const mx_linear_bwd_args* args, void* stream) {
+  if (!args) return MX_ERR_NULL;
+  const mx_linear_bwd_args& a = *args;
+  if (a.accumulate != 0 && a.accumulate != 1) return MX_ERR_FORMAT;
+  if (!act_ok(a.act) || !act_ok(a.x_act)) return MX_ERR_FORMAT;
+  if (a.M < 0 || a.N < 0 || a.K < 0 || a.N % 32 || a.K % 32) return MX_ERR_SHAPE;
+  if (a.M > kMaxExtent) return MX_ERR_INDEX_OVERFLOW;
+  if (!a.dX && !a.dW && !a.db && a.M > 0 && a.N > 0 && a.K > 0) return MX_ERR_NULL;
+  const int64_t Mp = up32(a.M);
+  const bool want_dx = a.dX && a.M > 0 && a.K > 0, want_dw = a.dW && a.N > 0 && a.K > 0;
+  // G = dY act'(saved_pre): rows for dX, columns for dW, column sums for db
+  mx_quantize_saved_args g;
+  memset(&g, 0, sizeof g);
+  g.R = a.M;
+  g.C = a.N;
+  g.fmt = a.fmt;
+  g.scale_mode = a.scale_mode;
+  g.hadamard = a.hadamard;
+  g.act = a.act;
+  g.x = a.dY;
+  g.ldx = a.lddy;
+  g.saved = a.saved_pre;
+  if (want_dx) g.row = a.dPr;
+  if (want_dw) g.col = a.dPc;
+  g.colsum = a.db;
+  g.colsum_partials = a.db ? a.db_partials : nullptr;
+  // X^T = x_act(saved_x)^T
+  mx_quantize_saved_args x = g;
+  x.C = a.K;
+  x.act = a.x_act;
+  x.x = nullptr;
+  x.ldx = 0;
+  x.saved = a.saved_x;
+  x.row = mx_packed{nullptr, nullptr};
+  x.col = a.Xc;
+  x.colsum = x.colsum_partials = nullptr;
+  mx_gemm_act_args d;
+  memset(&d, 0, sizeof d);
+  d.M = a.M;
+  d.N = a.K;
+  d.K = a.N;
+  d.fmt = a.fmt;
+  d.act = MX_ACT_NONE;
+  d.A = a.dPr;
+  d.B = a.Wc;
+  d.C = a.dX;
+  d.ldc = a.lddx;
+  mx_gemm_act_args w = d;
+  w.M = a.N;
+  w.N = a.K;
+  w.K = Mp;
+  w.A = a.dPc;
+  w.B = a.Xc;
+  w.C = a.dW;
+  w.ldc = a.lddw;
+  w.c_dtype = a.dw_dtype;
+  w.residual = a.accumulate ? a.dW : nullptr;
+  w.ldr = a.lddw;
+  // the work operands and inputs that the products asked for need
+  const bool want_g = want_dx || want_dw || a.db;
+  if (want_g && a.M > 0 && a.N > 0) {
+    if (!a.dY) return MX_ERR_NULL;
+    if (want_dx && !packed_ok(a.dPr)) return MX_ERR_NULL;
+    if (want_dw && !packed_ok(a.dPc)) return MX_ERR_NULL;
+  }
+  int st;
+  if (want_g && (st = validate_quantize_saved(g)) != MX_OK) return st;
+  if (want_dw && (st = validate_quantize_saved(x)) != MX_OK) return st;
+  if (want_dx && (st = validate_gemm_act(d)) != MX_OK) return st;
+  if (want_dw && (st = validate_gemm_act(w)) != MX_OK) return st;
+  if ((st = check_device()) != MX_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (want_g && (st = quantize_saved_launch(g, s)) != MX_OK) return st;
+  if (want_dw && (st = quantize_saved_launch(x, s)) != MX_OK) return st;
+  if (want_dx && (st = gemm_act_launch(d, s)) != MX_OK) return st;
+  if (want_dw && (st = gemm_act_launch(w, s)) != MX_OK) return st;
+  return MX_OK;
 }
 
 const char* mx_status_str(int status) {

@@ -1,0 +1,341 @@
+// Activation checkpoints in 8 bits and the packs that read them.
+//
+// A checkpoint of x [R][C] is its rowwise MXFP8 operand: E4M3 codes with one
+// E8M0 exponent per 32 columns (RCEIL, so nothing saturates), in the packed
+// layout of [R] x K=C -- 8.25 bits a value, and itself an operand of an MXFP8
+// GEMM.  Three kernels, each one pass over its data and bound by HBM:
+//   checkpoint_save_kernel   bf16 / binary32 -> checkpoint,
+//   checkpoint_load_kernel   checkpoint -> bf16 / binary32,
+//   quantize_saved_kernel    checkpoint (and a gradient) -> the operands of
+//                            the backward GEMMs, rowwise and columnwise, with
+//                            the activation or its slope in between.
+#include "mx_act.h"
+#include "mx_device.h"
+#include "mx_kernels.h"
+#include "mx_linear.h"
+
+namespace mx {
+
+namespace {
+
+// Eight values of a row at column c: one 16-byte load of bf16, two of binary32.
+template <int F32>
+struct Eight {
+  uint4 w[F32 ? 2 : 1];
+};
+template <int F32>
+__device__ __forceinline__ Eight<F32> load8(const void* base, int64_t at) {
+  Eight<F32> q;
+  if constexpr (F32) {
+    const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(base) + at);
+    q.w[0] = src[0];
+    q.w[1] = src[1];
+  } else {
+    q.w[0] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(base) + at);
+  }
+  return q;
+}
+template <int F32>
+__device__ __forceinline__ void values8(const Eight<F32>& q, float (&lo)[4], float (&hi)[4]) {
+  if constexpr (F32) {
+    const uint32_t a[4] = {q.w[0].x, q.w[0].y, q.w[0].z, q.w[0].w}, b[4] = {q.w[1].x, q.w[1].y, q.w[1].z, q.w[1].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      lo[i] = __uint_as_float(a[i]);
+      hi[i] = __uint_as_float(b[i]);
+    }
+  } else {
+    lo[0] = bf16_lo(q.w[0].x);
+    lo[1] = bf16_hi(q.w[0].x);
+    lo[2] = bf16_lo(q.w[0].y);
+    lo[3] = bf16_hi(q.w[0].y);
+    hi[0] = bf16_lo(q.w[0].z);
+    hi[1] = bf16_hi(q.w[0].z);
+    hi[2] = bf16_lo(q.w[0].w);
+    hi[3] = bf16_hi(q.w[0].w);
+  }
+}
+
+// ------------------------------------------------------------------ save and load
+// A workgroup takes 64 rows of one 128-column K group: 16 lanes a row, eight
+// values a lane, four rows a thread.  Reads are 256-byte (bf16) row segments,
+// writes one contiguous run (the layout puts a K group's rows back to back).
+constexpr int kCkptRows = 64, kCkptSteps = 4;
+
+template <int F32>
+__global__ __launch_bounds__(256) void checkpoint_save_kernel(const void* __restrict__ x, int64_t R, int64_t C,
+                                                              int64_t ldx, uint8_t* __restrict__ codes,
+                                                              uint8_t* __restrict__ scales, int groups) {
+  const int t = threadIdx.x, ch = t & 15, row = t >> 4;
+  const int64_t q = blockIdx.x % groups, r0 = (int64_t)(blockIdx.x / groups) * kCkptRows + row;
+  const int64_t c = q * 128 + ch * 8;
+  Eight<F32> in[kCkptSteps];
+#pragma unroll
+  for (int i = 0; i < kCkptSteps; ++i) {
+    const int64_t r = r0 + 16 * i;
+    if (r < R && c < C) in[i] = load8<F32>(x, r * ldx + c);
+    else in[i] = Eight<F32>{};  // pad blocks: zero codes
+  }
+#pragma unroll
+  for (int i = 0; i < kCkptSteps; ++i) {
+    const int64_t r = r0 + 16 * i;
+    float lo[4], hi[4];
+    values8<F32>(in[i], lo, hi);
+    // an all-zero block gets scale byte 0, and so does a pad block
+    const uint32_t s = scale_byte<kE4M3, kRceil>(max_over4(abs_max4(hi, abs_max4(lo))));
+    const uint2 w = make_uint2(e4m3_encode4(lo, s), e4m3_encode4(hi, s));
+    // the row's scale dword: byte b from the lanes of block b = ch / 4
+    uint32_t d = s << (8 * (ch >> 2));
+    d |= dpp_move<kDppRor8>(d);
+    d |= dpp_move<kDppRor4>(d);
+    if (r < R) {
+      *reinterpret_cast<uint2*>(codes + (q * R + r) * 128 + ch * 8) = w;
+      if (ch == 0) *reinterpret_cast<uint32_t*>(scales + (q * R + r) * 4) = d;
+    }
+  }
+}
+
+template <int F32>
+__global__ __launch_bounds__(256) void checkpoint_load_kernel(const uint8_t* __restrict__ codes,
+                                                              const uint8_t* __restrict__ scales, int64_t R,
+                                                              int64_t C, void* __restrict__ y, int64_t ldy,
+                                                              int groups) {
+  const int t = threadIdx.x, ch = t & 15, row = t >> 4;
+  const int64_t q = blockIdx.x % groups, r0 = (int64_t)(blockIdx.x / groups) * kCkptRows + row;
+  const int64_t c = q * 128 + ch * 8;
+  uint2 w[kCkptSteps];
+  uint32_t s[kCkptSteps];
+#pragma unroll
+  for (int i = 0; i < kCkptSteps; ++i) {
+    const int64_t r = r0 + 16 * i;
+    if (r < R && c < C) {
+      w[i] = *reinterpret_cast<const uint2*>(codes + (q * R + r) * 128 + ch * 8);
+      s[i] = *reinterpret_cast<const uint32_t*>(scales + (q * R + r) * 4);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kCkptSteps; ++i) {
+    const int64_t r = r0 + 16 * i;
+    if (r < R && c < C) {
+      const float sc = e8m0_value((s[i] >> (8 * (ch >> 2))) & 255u);
+      float lo[4], hi[4];
+      e4m3_decode4(w[i].x, sc, lo);
+      e4m3_decode4(w[i].y, sc, hi);
+      if constexpr (F32) {
+        float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(y) + r * ldy + c);
+        dst[0] = make_float4(lo[0], lo[1], lo[2], lo[3]);
+        dst[1] = make_float4(hi[0], hi[1], hi[2], hi[3]);
+      } else {
+        *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(y) + r * ldy + c) =
+            make_uint4(pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]), pack_bf16x2(hi[0], hi[1]),
+                       pack_bf16x2(hi[2], hi[3]));
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ packs from a checkpoint
+// One 256-thread workgroup turns a 128 x 128 tile of v into rows' and columns'
+// blocks: inputs -> v in registers (its column sums are taken there, in
+// binary32) -> bf16 in LDS -> one quantization pass per axis.  Tile geometry
+// as in the bf16 packer: row pitch 272 bytes, every 32-row block shifted by a
+// further 32 so that a column pass's four blocks fall in different banks.
+constexpr int kTile = 128, kPitch = kTile * 2 + 16, kBlockSkew = 32;
+constexpr int kTileBytes = kTile * kPitch + 3 * kBlockSkew;
+constexpr int kSteps = 8;  // 16-row steps of a tile
+__device__ __forceinline__ int lds_row_at(int row) { return row * kPitch + (row >> 5) * kBlockSkew; }
+
+// Sum over the four lanes l, l ^ 16, l ^ 32, l ^ 48 (a fixed order).
+__device__ __forceinline__ float sum_over_rows4(float v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const uint32_t b = __float_as_uint(v);
+  const auto x = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+  const uint32_t h = __float_as_uint(__uint_as_float(x[0]) + __uint_as_float(x[1]));
+  const auto y = __builtin_amdgcn_permlane32_swap(h, h, false, false);
+  return __uint_as_float(y[0]) + __uint_as_float(y[1]);
+#else
+  return v;
+#endif
+}
+
+// HASX: v = x act'(saved) (ACT none: v = x, no checkpoint), else v = act(saved).
+template <int FMT, int MODE, int HAD, int ACT, int HASX>
+__global__ __launch_bounds__(256) void quantize_saved_kernel(SavedPackParams p) {
+  constexpr int B = FmtTraits<FMT>::kBits;
+  constexpr bool kSaved = !HASX || ACT != kActNone;
+  __shared__ __attribute__((aligned(16))) uint8_t tile[kTileBytes];
+  __shared__ float part[4][kTile];
+  const int t = threadIdx.x, ch = t & 15, row_t = t >> 4;
+  const int tx = (int)((p.C + kTile - 1) / kTile);
+  const int64_t by = blockIdx.x / tx, bx = blockIdx.x - by * tx;
+  const int64_t r0 = by * kTile, c0 = bx * kTile, c = c0 + ch * 8;
+
+  // 1. every load of the tile in flight, then v, its sums, and bf16 in LDS
+  uint4 x[kSteps];
+  uint2 w[kSteps];
+  uint32_t s[kSteps];
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int64_t r = r0 + row_t + 16 * i;
+    x[i] = make_uint4(0u, 0u, 0u, 0u);
+    w[i] = make_uint2(0u, 0u);
+    s[i] = 0u;
+    if (r < p.R && c < p.C) {
+      if constexpr (HASX) x[i] = *reinterpret_cast<const uint4*>(p.x + r * p.ldx + c);
+      if constexpr (kSaved) {
+        w[i] = *reinterpret_cast<const uint2*>(p.saved_codes + (bx * p.R + r) * 128 + ch * 8);
+        s[i] = *reinterpret_cast<const uint32_t*>(p.saved_scales + (bx * p.R + r) * 4);
+      }
+    }
+  }
+  float sum[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    float v[8];
+    if constexpr (kSaved) {
+      const float sc = e8m0_value((s[i] >> (8 * (ch >> 2))) & 255u);
+      float lo[4], hi[4];
+      e4m3_decode4(w[i].x, sc, lo);
+      e4m3_decode4(w[i].y, sc, hi);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = HASX ? act_slope<ACT>(lo[e]) : act_value<ACT>(lo[e]);
+        v[4 + e] = HASX ? act_slope<ACT>(hi[e]) : act_value<ACT>(hi[e]);
+      }
+    }
+    if constexpr (HASX) {
+      const uint32_t d[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[2 * e] = kSaved ? bf16_lo(d[e]) * v[2 * e] : bf16_lo(d[e]);
+        v[2 * e + 1] = kSaved ? bf16_hi(d[e]) * v[2 * e + 1] : bf16_hi(d[e]);
+      }
+    }
+    // (rows and columns past the end hold zeros: act(0) = 0, 0 act'(0) = 0)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] = sum[e] + v[e];
+    *reinterpret_cast<uint4*>(tile + row_t * kPitch + ch * 16 + i * 16 * kPitch + (i >> 1) * kBlockSkew) =
+        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                   pack_bf16x2(v[6], v[7]));
+  }
+  if (p.partials != nullptr) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] = sum_over_rows4(sum[e]);
+    if ((t & 63) < 16) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) part[t >> 6][ch * 8 + e] = sum[e];
+    }
+  }
+  __syncthreads();
+  if (p.partials != nullptr && t < kTile && c0 + t < p.C)
+    p.partials[by * p.C + c0 + t] = ((part[0][t] + part[1][t]) + part[2][t]) + part[3][t];
+
+  // 2. rowwise blocks: the four of a row come from four adjacent lanes
+  if (p.row_codes != nullptr) {
+    uint8_t* const codes = p.row_codes + (bx * p.R + r0) * (16 * B);
+    uint8_t* const scales = p.row_scales + (bx * p.R + r0) * 4;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int q = t + 256 * h, row = q >> 2, blk = q & 3;
+      const int64_t r = r0 + row;
+      if (r < p.R) {
+        if (c0 + blk * 32 < p.C) {
+          float v[32];
+          lds_row_block(tile + lds_row_at(row), 0, 0, blk * 32, v);
+          quant_store<FMT, MODE, HAD>(v, codes + row * (16 * B), blk, r, scales + (row * 4 + blk));
+        } else {
+          scales[row * 4 + blk] = 0;
+          zero_block<FMT>(codes + row * (16 * B), blk, r);
+        }
+      }
+    }
+  }
+
+  // 3. columnwise blocks, written as a K-major operand; a block that ends
+  //    past R is filled with zero rows, one past R is a pad block
+  if (p.col_codes != nullptr) {
+    uint8_t* const codes = p.col_codes + (by * p.C + c0) * (16 * B);
+    uint8_t* const scales = p.col_scales + (by * p.C + c0) * 4;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int q = t + 256 * h, col = q >> 2, blk = q & 3;
+      if (c0 + col < p.C) {
+        if (r0 + blk * 32 < p.R) {
+          float v[32];
+          const uint16_t* src = reinterpret_cast<const uint16_t*>(tile + lds_row_at(32 * blk)) + col;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = bf16_to_f32(src[i * (kPitch / 2)]);
+          quant_store<FMT, MODE, HAD>(v, codes + col * (16 * B), blk, c0 + col, scales + (col * 4 + blk));
+        } else {
+          scales[col * 4 + blk] = 0;
+          zero_block<FMT>(codes + col * (16 * B), blk, c0 + col);
+        }
+      }
+    }
+  }
+}
+
+using SavedFn = void (*)(SavedPackParams);
+
+template <int FMT, int MODE, int HAD>
+SavedFn pick_act(int act, bool has_x) {
+  switch (act) {
+    case kActNone: return has_x ? quantize_saved_kernel<FMT, MODE, HAD, kActNone, 1> : quantize_saved_kernel<FMT, MODE, HAD, kActNone, 0>;
+    case kActGelu: return has_x ? quantize_saved_kernel<FMT, MODE, HAD, kActGelu, 1> : quantize_saved_kernel<FMT, MODE, HAD, kActGelu, 0>;
+    case kActSilu: return has_x ? quantize_saved_kernel<FMT, MODE, HAD, kActSilu, 1> : quantize_saved_kernel<FMT, MODE, HAD, kActSilu, 0>;
+    default: return nullptr;
+  }
+}
+
+SavedFn pick_saved(int fmt, int mode, int had, int act, bool has_x) {
+  if (fmt == kE2M1 && mode == kFloor && !had) return pick_act<kE2M1, kFloor, 0>(act, has_x);
+  if (fmt == kE2M3 && mode == kFloor && !had) return pick_act<kE2M3, kFloor, 0>(act, has_x);
+  if (fmt == kE2M3 && mode == kFloor && had) return pick_act<kE2M3, kFloor, 1>(act, has_x);
+  if (fmt == kE4M3 && mode == kRceil && !had) return pick_act<kE4M3, kRceil, 0>(act, has_x);
+  if (fmt == kE4M3 && mode == kFloor && !had) return pick_act<kE4M3, kFloor, 0>(act, has_x);
+  return nullptr;
+}
+
+// Workgroups of a save / load launch, or -1 if they do not fit a grid.
+int64_t checkpoint_grid(int64_t R, int64_t C, int* groups) {
+  const int64_t g = (C + 127) / 128, n = g * ((R + kCkptRows - 1) / kCkptRows);
+  *groups = (int)g;
+  return g < (1ll << 31) && n < (1ll << 31) ? n : -1;
+}
+
+}  // namespace
+
+hipError_t launch_checkpoint_save(const void* x, int x_f32, int64_t R, int64_t C, int64_t ldx, uint8_t* codes,
+                                  uint8_t* scales, hipStream_t stream) {
+  int groups = 0;
+  const int64_t n = checkpoint_grid(R, C, &groups);
+  if (n < 0) return hipErrorInvalidValue;
+  if (n == 0) return hipSuccess;
+  hipLaunchKernelGGL((x_f32 ? checkpoint_save_kernel<1> : checkpoint_save_kernel<0>), dim3((unsigned)n), dim3(256), 0,
+                     stream, x, R, C, ldx, codes, scales, groups);
+  return hipGetLastError();
+}
+
+hipError_t launch_checkpoint_load(const uint8_t* codes, const uint8_t* scales, int64_t R, int64_t C, void* y,
+                                  int y_f32, int64_t ldy, hipStream_t stream) {
+  int groups = 0;
+  const int64_t n = checkpoint_grid(R, C, &groups);
+  if (n < 0) return hipErrorInvalidValue;
+  if (n == 0) return hipSuccess;
+  hipLaunchKernelGGL((y_f32 ? checkpoint_load_kernel<1> : checkpoint_load_kernel<0>), dim3((unsigned)n), dim3(256), 0,
+                     stream, codes, scales, R, C, y, ldy, groups);
+  return hipGetLastError();
+}
+
+hipError_t launch_quantize_saved(const SavedPackParams& p, int fmt, int mode, int had, int act, hipStream_t stream) {
+  SavedFn fn = pick_saved(fmt, mode, had, act, p.x != nullptr);
+  const int64_t tiles = ((p.C + kTile - 1) / kTile) * ((p.R + kTile - 1) / kTile);
+  if (!fn || tiles >= (1ll << 31)) return hipErrorInvalidValue;
+  if (tiles == 0) return hipSuccess;
+  hipLaunchKernelGGL(fn, dim3((unsigned)tiles), dim3(256), 0, stream, p);
+  return hipGetLastError();
+}
+
+}  // namespace mx

@@ -19,6 +19,7 @@ PRO_IDENTITY, PRO_GELU_TANH, PRO_DGELU_TANH, PRO_SWIGLU, PRO_DSWIGLU = 0, 1, 2, 
 BF16, F32 = 0, 1
 RAGGED_M, RAGGED_K = 0, 1
 EPI_NONE, EPI_SWIGLU, EPI_DSWIGLU = 0, 1, 2
+ACT_NONE, ACT_GELU_TANH, ACT_SILU = 0, 1, 2
 BITS = {E2M1: 4, E2M3: 6, E4M3: 8}
 
 STATUS = {0: "MX_OK", 1: "MX_ERR_NULL", 2: "MX_ERR_SHAPE", 3: "MX_ERR_ALIGN", 4: "MX_ERR_FORMAT",
@@ -84,6 +85,31 @@ class GemmItem(ctypes.Structure):
 
 GEMM_MANY_MAX = 4
 
+
+class GemmActArgs(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("fmt", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("A", Packed), ("B", Packed), ("bias", ctypes.c_void_p),
+                ("residual", ctypes.c_void_p), ("C", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+                ("ldc", ctypes.c_int64), ("bias_dtype", ctypes.c_int32), ("c_dtype", ctypes.c_int32),
+                ("saved", Packed)]
+
+
+class QuantizeSavedArgs(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int64), ("C", ctypes.c_int64), ("fmt", ctypes.c_int32), ("scale_mode", ctypes.c_int32),
+                ("hadamard", ctypes.c_int32), ("act", ctypes.c_int32), ("x", ctypes.c_void_p),
+                ("ldx", ctypes.c_int64), ("saved", Packed), ("row", Packed), ("col", Packed),
+                ("colsum_partials", ctypes.c_void_p), ("colsum", ctypes.c_void_p)]
+
+
+class LinearBwdArgs(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("fmt", ctypes.c_int32),
+                ("scale_mode", ctypes.c_int32), ("hadamard", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("x_act", ctypes.c_int32), ("accumulate", ctypes.c_int32), ("dY", ctypes.c_void_p),
+                ("lddy", ctypes.c_int64), ("saved_pre", Packed), ("saved_x", Packed), ("Wc", Packed),
+                ("dX", ctypes.c_void_p), ("lddx", ctypes.c_int64), ("dW", ctypes.c_void_p), ("lddw", ctypes.c_int64),
+                ("dw_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32), ("db", ctypes.c_void_p),
+                ("db_partials", ctypes.c_void_p), ("dPr", Packed), ("dPc", Packed), ("Xc", Packed)]
+
 _lib = None
 
 
@@ -123,6 +149,16 @@ def lib():
         L.mx_fused_mlp_bwd.argtypes = [ctypes.POINTER(MlpBwdArgs), vp]
         L.mx_grouped_gemm.restype = ci
         L.mx_grouped_gemm.argtypes = [ctypes.POINTER(GroupedArgs), vp]
+        L.mx_gemm_act.restype = ci
+        L.mx_gemm_act.argtypes = [ctypes.POINTER(GemmActArgs), vp]
+        L.mx_checkpoint_save.restype = ci
+        L.mx_checkpoint_save.argtypes = [vp, ci, i64, i64, i64, vp, vp, vp]
+        L.mx_checkpoint_load.restype = ci
+        L.mx_checkpoint_load.argtypes = [vp, vp, i64, i64, vp, ci, i64, vp]
+        L.mx_quantize_saved.restype = ci
+        L.mx_quantize_saved.argtypes = [ctypes.POINTER(QuantizeSavedArgs), vp]
+        L.mx_linear_bwd_saved.restype = ci
+        L.mx_linear_bwd_saved.argtypes = [ctypes.POINTER(LinearBwdArgs), vp]
         L.mx_status_str.restype = ctypes.c_char_p
         L.mx_status_str.argtypes = [ci]
         L.mx_device_supported.restype = ci
@@ -447,6 +483,138 @@ def grouped_gemm(mode, G, R, offsets, A, B, C, fmt=E4M3, epilogue=EPI_NONE, scal
 
 def device_supported(device: int = 0) -> bool:
     return bool(lib().mx_device_supported(device))
+
+
+# ---------------------------------------------------------------- linear operators
+def _matrix(t, R: int, C: int, what: str, dtypes=(BF16, F32)):
+    """(address, row pitch, dtype) of an [R][C] operand: a tensor of that
+    shape whose rows are dense (a column slice of a wider one included), or
+    a contiguous one of R * C elements.  float32 is MX_F32; bfloat16 and the
+    16-bit integers that carry bf16 patterns are MX_BF16."""
+    if t is None:
+        return None, max(C, 0), dtypes[0]
+    if t.dtype == torch.float32:
+        dtype = F32
+    elif t.dtype in (torch.bfloat16, torch.int16, torch.uint16):
+        dtype = BF16
+    else:
+        raise MXError(4, f"{what}: {t.dtype} is neither float32 nor bf16")
+    if dtype not in dtypes:
+        raise MXError(4, f"{what}: {t.dtype} is not served here")
+    if not t.is_contiguous():
+        if tuple(t.shape) != (R, C) or (C > 1 and t.stride(1) != 1) or (R > 1 and t.stride(0) < C):
+            raise MXError(2, f"{what}: not an [{R}][{C}] tensor with dense rows")
+        ld = t.stride(0) if R > 1 else C
+    elif t.numel() != R * C:
+        raise MXError(2, f"{what}: {tuple(t.shape)} does not hold [{R}][{C}]")
+    else:
+        ld = C
+    return _device_ptr(t, what), ld, dtype
+
+
+def _device_ptr(t, what: str):
+    if not t.is_cuda:
+        raise MXError(7, f"{what}: tensor is not on a GPU (the kernels take device memory)")
+    if t.device.index != torch.cuda.current_device():
+        raise MXError(7, f"{what}: tensor is on cuda:{t.device.index}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return t.data_ptr()
+
+
+def _operand(p, rows: int, K: int, fmt: int, what: str):
+    """Packed struct of an operand (codes, scales) of [rows] x K, or of None."""
+    if p is None:
+        return Packed(None, None)
+    groups = (K + 127) // 128
+    for t, per_row, part in ((p[0], 16 * BITS.get(fmt, 0), "codes"), (p[1], 4, "scales")):
+        if not t.is_contiguous():
+            raise MXError(2, f"{what} {part}: tensor argument is a strided view; pass a contiguous tensor")
+        _need(t, groups * rows * per_row, f"{what} {part}")
+    return Packed(_device_ptr(p[0], what), _device_ptr(p[1], what))
+
+
+def _vector(t, n: int, what: str, dtypes):
+    if t is None:
+        return None, dtypes[0]
+    ptr, _, dtype = _matrix(t, 1, n, what, dtypes)
+    return ptr, dtype
+
+
+def gemm_act(a, b, M: int, N: int, K: int, fmt: int, c=None, act: int = ACT_NONE, bias=None, residual=None,
+             saved=None, stream=None):
+    """mx_gemm_act: c = act(A . B^T + bias) + residual for any M (N, K
+    multiples of 32), and / or saved = (codes, scales), the 8-bit checkpoint
+    of A . B^T + bias.  c and residual are [M][N] of one type (bf16 or
+    float32), rows dense; residual may be c."""
+    cp, ldc, c_dtype = _matrix(c, M, N, "gemm_act C")
+    rp, ldr, r_dtype = _matrix(residual, M, N, "gemm_act residual")
+    if residual is not None and c is not None and r_dtype != c_dtype:
+        raise MXError(4, "gemm_act: residual and C are of different types")
+    bp, bias_dtype = _vector(bias, N, "gemm_act bias", (BF16, F32))
+    g = GemmActArgs(M, N, K, fmt, act, _operand(a, M, K, fmt, "gemm_act A"), _operand(b, N, K, fmt, "gemm_act B"),
+                    bp, rp, cp, ldr, ldc, bias_dtype, c_dtype, _operand(saved, M, N, E4M3, "gemm_act saved"))
+    _check(lib().mx_gemm_act(ctypes.byref(g), _stream(stream)), "mx_gemm_act")
+
+
+def checkpoint_save(x, saved, stream=None):
+    """mx_checkpoint_save: x [R][C] (bf16 or float32, rows dense) into saved =
+    (codes, scales) of alloc_packed(R, C, E4M3)."""
+    R, C = x.shape
+    xp, ldx, dtype = _matrix(x, R, C, "checkpoint_save x")
+    p = _operand(saved, R, C, E4M3, "checkpoint_save")
+    _check(lib().mx_checkpoint_save(xp, dtype, R, C, ldx, p.codes, p.scales, _stream(stream)), "mx_checkpoint_save")
+
+
+def checkpoint_load(saved, y, stream=None):
+    """mx_checkpoint_load: the values of saved = (codes, scales) into y [R][C]
+    (bf16 or float32, rows dense)."""
+    R, C = y.shape
+    yp, ldy, dtype = _matrix(y, R, C, "checkpoint_load y")
+    p = _operand(saved, R, C, E4M3, "checkpoint_load")
+    _check(lib().mx_checkpoint_load(p.codes, p.scales, R, C, yp, dtype, ldy, _stream(stream)), "mx_checkpoint_load")
+
+
+def _rows32(R: int):
+    return (R + 31) // 32 * 32
+
+
+def quantize_saved(R: int, C: int, fmt: int, scale_mode: int, hadamard: bool = False, act: int = ACT_NONE, x=None,
+                   saved=None, row=None, col=None, colsum_partials=None, colsum=None, stream=None):
+    """mx_quantize_saved: pack act(saved), or x * act'(saved) where x [R][C]
+    (bf16) is given (x itself with ACT_NONE and no checkpoint), for any R:
+    row [R] x K=C, col [C] x K = R rounded up to 32, and the column sums
+    (partials float32 [ceil(R/128)][C])."""
+    xp, ldx, _ = _matrix(x, R, C, "quantize_saved x", (BF16,))
+    part, _ = _vector(colsum_partials, (R + 127) // 128 * C, "quantize_saved colsum partials", (F32,))
+    total, _ = _vector(colsum, C, "quantize_saved colsum", (F32,))
+    q = QuantizeSavedArgs(R, C, fmt, scale_mode, int(hadamard), act, xp, ldx,
+                          _operand(saved, R, C, E4M3, "quantize_saved checkpoint"),
+                          _operand(row, R, C, fmt, "quantize_saved row"),
+                          _operand(col, C, _rows32(R), fmt, "quantize_saved col"), part, total)
+    _check(lib().mx_quantize_saved(ctypes.byref(q), _stream(stream)), "mx_quantize_saved")
+
+
+def linear_bwd_saved(M: int, N: int, K: int, dY, saved_x, Wc, fmt: int, scale_mode: int, hadamard: bool = False,
+                     act: int = ACT_NONE, saved_pre=None, x_act: int = ACT_NONE, dX=None, dW=None, db=None,
+                     dPr=None, dPc=None, Xc=None, db_partials=None, accumulate: bool = False, stream=None):
+    """mx_linear_bwd_saved: dX [M][K], dW [N][K] (bf16 or float32) and db [N]
+    (float32), each optional, of Y = act(X W^T + b), X = x_act(saved_x).
+    Work operands: dPr [M] x K=N, and dPc [N], Xc [K] x K = M rounded up to
+    32; db_partials float32 [ceil(M/128)][N]."""
+    yp, lddy, _ = _matrix(dY, M, N, "linear_bwd_saved dY", (BF16,))
+    xp, lddx, _ = _matrix(dX, M, K, "linear_bwd_saved dX", (BF16,))
+    wp, lddw, dw_dtype = _matrix(dW, N, K, "linear_bwd_saved dW")
+    bp, _ = _vector(db, N, "linear_bwd_saved db", (F32,))
+    part, _ = _vector(db_partials, (M + 127) // 128 * N, "linear_bwd_saved db partials", (F32,))
+    Mp = _rows32(M)
+    b = LinearBwdArgs(M, N, K, fmt, scale_mode, int(hadamard), act, x_act, int(accumulate), yp, lddy,
+                      _operand(saved_pre, M, N, E4M3, "linear_bwd_saved saved_pre"),
+                      _operand(saved_x, M, K, E4M3, "linear_bwd_saved saved_x"),
+                      _operand(Wc, K, N, fmt, "linear_bwd_saved Wc"), xp, lddx, wp, lddw, dw_dtype, 0, bp, part,
+                      _operand(dPr, M, N, fmt, "linear_bwd_saved dPr"),
+                      _operand(dPc, N, Mp, fmt, "linear_bwd_saved dPc"),
+                      _operand(Xc, K, Mp, fmt, "linear_bwd_saved Xc"))
+    _check(lib().mx_linear_bwd_saved(ctypes.byref(b), _stream(stream)), "mx_linear_bwd_saved")
 
 
 def status_str(st: int) -> str:
