@@ -35,62 +35,122 @@ __global__ __launch_bounds__(tile_threads(BM, BN, kEpiAct), OCC) void gemm_act_k
 // of block g, E4M3 [16g, 16g+16) and [64+16g, 64+16g+16); its scale operand is
 // the byte of block g (layouts measured).  With B as the first operand, a lane
 // ends with C row l % 16 and the four columns 4g .. 4g+3.
+//
+// W wavefronts compute a 16 MI x 16 NJ tile of C, wavefront w from the K groups
+// w, w + W, ...; each stages its groups in a ring of D buffers of its own in
+// LDS, filled by direct global -> LDS loads that need no registers and no
+// barrier.  The loads take a panel's rows back to back, lane after lane, so a
+// wavefront's load is whole cache lines (loaded straight into the layout
+// above, 16 bytes of each of 16 rows at a time, 32 x 4096 x 12288 in E4M3
+// took 19.3 us); the 16-byte chunks of a row are permuted on the way so that
+// the reads of 16 rows spread over the LDS banks.  The partial tiles meet in
+// LDS and are summed in wavefront order: the result does not depend on
+// timing.  Rows past the operands' ends are loaded as the last row and never
+// stored.
+template <int FMT, int MI, int NJ, int W, int D>
+struct RowsCfg {
+  static constexpr int kTR = 16 * MI, kTC = 16 * NJ;
+  static constexpr int kGB = 16 * FmtTraits<FMT>::kBits;  // code bytes of a row in one K group
+  static constexpr int kChunks = kGB / 16;
+  // 16-byte loads per lane and stage; the last one may cover 32 lanes only
+  static constexpr int kALoads = (kTR * kChunks + 63) / 64, kBLoads = (kTC * kChunks + 63) / 64;
+  static constexpr int kLoads = kALoads + kBLoads + 2;  // + the scale dwords of A and of B
+  static constexpr int kAOff = 0, kBOff = kTR * kGB, kSOff = kBOff + kTC * kGB;
+  static constexpr int kStage = kSOff + 2 * 256;  // (64 scale dwords each)
+  static constexpr int kRing = W * D * kStage;
+  static constexpr int kPitch = kTC + 4;  // floats: the 16 rows of a write start in different banks
+  static constexpr int kRed = W * kTR * kPitch * 4;
+  static constexpr int kSmem = kRing > kRed ? kRing : kRed;
+  static_assert(D >= 2 && kLoads * (D - 1) < 64, "outstanding loads are counted in six bits");
+  static_assert(kSmem <= 163840 && MI <= 4 && NJ >= 2 && NJ <= 4, "LDS budget; scale slots; whole checkpoint blocks");
+};
+
+// Place of 16-byte chunk c of row x (of 16) in its staged row.
 template <int FMT>
-__device__ __forceinline__ v8i rows_operand(const uint8_t* at, int row, int g) {
+__device__ __forceinline__ int rows_place(int x, int c) {
+  if constexpr (FMT == kE4M3) return c ^ ((x >> 1) & 7);
+  else if constexpr (FMT == kE2M1) return c ^ ((x >> 2) & 3);
+  else return (c + (x >> 3)) % 6;
+}
+template <int FMT>
+__device__ __forceinline__ int rows_chunk(int x, int place) {
+  if constexpr (FMT == kE2M3) return (place + 6 - (x >> 3)) % 6;
+  else return rows_place<FMT>(x, place);
+}
+
+// This lane's operand from a staged panel of 16 rows; `row` is the operand's
+// row (its bit 4 orders the tails of an E2M3 group).
+template <int FMT>
+__device__ __forceinline__ v8i rows_fragment(const uint8_t* panel, int x, int g, uint32_t row) {
+  constexpr int kGB = 16 * FmtTraits<FMT>::kBits;
+  const uint8_t* at = panel + x * kGB;
+  const v4i a = *reinterpret_cast<const v4i*>(at + 16 * rows_place<FMT>(x, g));
   if constexpr (FMT == kE2M1) {
-    const v4i a = *reinterpret_cast<const v4i*>(at + 16 * g);
-    return __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
+    return v8i{a.x, a.y, a.z, a.w, 0, 0, 0, 0};
   } else if constexpr (FMT == kE2M3) {
-    const v4i a = *reinterpret_cast<const v4i*>(at + 16 * g);
-    const v2i h = *reinterpret_cast<const v2i*>(at + 64 + 8 * (g ^ ((row >> 4) & 1)));
-    const v4i h4 = __builtin_shufflevector(h, h, 0, 1, -1, -1);
-    return __builtin_shufflevector(a, h4, 0, 1, 2, 3, 4, 5, -1, -1);
+    const int tail = g ^ (int)((row >> 4) & 1u);  // which 8 of the last 32 bytes
+    const v2i h = *reinterpret_cast<const v2i*>(at + 16 * rows_place<FMT>(x, 4 + (tail >> 1)) + 8 * (tail & 1));
+    return v8i{a.x, a.y, a.z, a.w, h.x, h.y, 0, 0};
   } else {
-    const v4i a = *reinterpret_cast<const v4i*>(at + 16 * g);
-    const v4i b = *reinterpret_cast<const v4i*>(at + 64 + 16 * g);
+    const v4i b = *reinterpret_cast<const v4i*>(at + 16 * rows_place<FMT>(x, 4 + g));
     return v8i{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   }
 }
 
-// W wavefronts compute a 16 MI x 16 NJ tile of C: wavefront w the K groups
-// w, w + W, ..., U of them in flight.  The partial tiles meet in LDS and are
-// summed in wavefront order, so the result does not depend on timing.  Rows
-// past the operands' ends are loaded as the last row and never stored.
-template <int FMT, int MI, int NJ, int W>
-struct RowsCfg {
-  static constexpr int kTR = 16 * MI, kTC = 16 * NJ;
-  static constexpr int kPitch = kTC + 4;  // floats: the 16 rows of a write start in different banks
-  static constexpr int kRegs = (FMT == kE4M3 ? 8 : FMT == kE2M3 ? 6 : 4) + 1;
-  // K groups in flight per wavefront: as many as about 96 registers hold
-  static constexpr int kFit = 96 / (kRegs * (MI + NJ));
-  static constexpr int kU = kFit >= 8 ? 8 : kFit >= 4 ? 4 : kFit >= 2 ? 2 : 1;
-};
+// A point that no memory access is moved across.
+__device__ __forceinline__ void memory_fence() {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("" ::: "memory");
+#endif
+}
 
-template <int FMT, int MI, int NJ, int W>
+template <int FMT, int MI, int NJ, int W, int D>
 __global__ __launch_bounds__(64 * W) void gemm_rows_kernel(GemmActParams p) {
-  using CF = RowsCfg<FMT, MI, NJ, W>;
-  constexpr int kGB = 16 * FmtTraits<FMT>::kBits;  // code bytes of a row in one K group
-  constexpr int U = CF::kU;
-  __shared__ __attribute__((aligned(16))) float red[W][CF::kTR][CF::kPitch];
+  using CF = RowsCfg<FMT, MI, NJ, W, D>;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[CF::kSmem];
   const int t = threadIdx.x, lane = t & 63, wave = wave_uniform(t >> 6);
-  const int r16 = lane & 15, g = lane >> 4;
+  const int x = lane & 15, g = lane >> 4;
   const int tiles_m = (int)((p.M + CF::kTR - 1) / CF::kTR);
   const int tn = blockIdx.x / tiles_m, tm = blockIdx.x - tn * tiles_m;
   const int64_t m0 = (int64_t)tm * CF::kTR, n0 = (int64_t)tn * CF::kTC;
   const int nq = (int)((p.K + 127) / 128);
+  const int n_own = wave < nq ? (nq - wave + W - 1) / W : 0;  // this wavefront's K groups
 
-  // operand rows of this lane (32-bit byte offsets: operands are under 2 GiB)
-  uint32_t a_row[MI], b_row[NJ];
+  // byte offsets of this lane's loads within a K group (32-bit: operands are
+  // under 2 GiB)
+  const auto row_of = [](int64_t first, int r, int64_t rows) {
+    return (uint32_t)(first + r < rows ? first + r : rows - 1);
+  };
+  uint32_t a_off[CF::kALoads], b_off[CF::kBLoads];
 #pragma unroll
-  for (int i = 0; i < MI; ++i) {
-    const int64_t m = m0 + 16 * i + r16;
-    a_row[i] = (uint32_t)(m < p.M ? m : p.M - 1);
+  for (int i = 0; i < CF::kALoads; ++i) {
+    const int s = 64 * i + lane, r = s / CF::kChunks;
+    a_off[i] = row_of(m0, r, p.M) * CF::kGB + 16 * rows_chunk<FMT>(r & 15, s % CF::kChunks);
   }
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    const int64_t n = n0 + 16 * j + r16;
-    b_row[j] = (uint32_t)(n < p.N ? n : p.N - 1);
+  for (int i = 0; i < CF::kBLoads; ++i) {
+    const int s = 64 * i + lane, r = s / CF::kChunks;
+    b_off[i] = row_of(n0, r, p.N) * CF::kGB + 16 * rows_chunk<FMT>(r & 15, s % CF::kChunks);
   }
+  const uint32_t sa_off = row_of(m0, lane < CF::kTR ? lane : 0, p.M) * 4;
+  const uint32_t sb_off = row_of(n0, lane < CF::kTC ? lane : 0, p.N) * 4;
+
+  uint8_t* const ring = smem + wave * (D * CF::kStage);
+  const uint32_t ring_lds = (uint32_t)wave_uniform((int)lds_addr(ring));
+  const auto issue = [&](int it, int buf) __attribute__((always_inline)) {
+    const uint64_t q = (uint64_t)(wave + it * W);
+    const uint32_t at = ring_lds + (uint32_t)(buf * CF::kStage);
+    const uint8_t* ac = p.a_codes + q * (uint64_t)p.M * CF::kGB;
+    const uint8_t* bc = p.b_codes + q * (uint64_t)p.N * CF::kGB;
+#pragma unroll
+    for (int i = 0; i < CF::kBLoads; ++i)
+      if (64 * (i + 1) <= CF::kTC * CF::kChunks || lane < 32) lds_dma16_s(bc, b_off[i], at + CF::kBOff + 1024 * i);
+#pragma unroll
+    for (int i = 0; i < CF::kALoads; ++i)
+      if (64 * (i + 1) <= CF::kTR * CF::kChunks || lane < 32) lds_dma16_s(ac, a_off[i], at + CF::kAOff + 1024 * i);
+    lds_dma4_s(p.a_scales + q * (uint64_t)p.M * 4, sa_off, at + CF::kSOff);
+    lds_dma4_s(p.b_scales + q * (uint64_t)p.N * 4, sb_off, at + CF::kSOff + 256);
+  };
 
   v4f acc[MI][NJ];
 #pragma unroll
@@ -98,42 +158,48 @@ __global__ __launch_bounds__(64 * W) void gemm_rows_kernel(GemmActParams p) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
-  const uint32_t a_rows = (uint32_t)p.M, b_rows = (uint32_t)p.N;
-  for (int q0 = wave; q0 < nq; q0 += W * U) {
-    v8i a[U][MI], b[U][NJ];
-    uint32_t sa[U][MI], sb[U][NJ];
+  // (every branch here is uniform; the wait that ends a group lets the loads
+  // of the D - 1 groups after it stay in flight)
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      // a group past the end loads the last one again and is not multiplied
-      const uint32_t q = (uint32_t)(q0 + W * u < nq ? q0 + W * u : nq - 1);
+  for (int it = 0; it < D - 1; ++it)
+    if (it < n_own) issue(it, it);
+  int buf = 0;
+  for (int it = 0; it < n_own; ++it) {
+    if (it + D - 1 < n_own) {
+      issue(it + D - 1, buf == 0 ? D - 1 : buf - 1);
+      wait_vmcnt<CF::kLoads * (D - 1)>();
+    } else {
+      wait_vmcnt<0>();
+    }
+    memory_fence();
+    const uint8_t* stage = ring + buf * CF::kStage;
+    v8i b[NJ];
+    int sb[NJ];
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        b[u][j] = rows_operand<FMT>(p.b_codes + (uint64_t)q * b_rows * kGB + b_row[j] * (uint32_t)kGB, b_row[j], g);
-        sb[u][j] = *reinterpret_cast<const uint32_t*>(p.b_scales + (uint64_t)q * b_rows * 4 + b_row[j] * 4u);
-      }
-#pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        a[u][i] = rows_operand<FMT>(p.a_codes + (uint64_t)q * a_rows * kGB + a_row[i] * (uint32_t)kGB, a_row[i], g);
-        sa[u][i] = *reinterpret_cast<const uint32_t*>(p.a_scales + (uint64_t)q * a_rows * 4 + a_row[i] * 4u);
-      }
+    for (int j = 0; j < NJ; ++j) {
+      b[j] = rows_fragment<FMT>(stage + CF::kBOff + 16 * j * CF::kGB, x, g, row_of(n0, 16 * j + x, p.N));
+      sb[j] = (int)(*reinterpret_cast<const uint32_t*>(stage + CF::kSOff + 256 + 4 * (16 * j + x)) >> (8 * g));
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (q0 + W * u < nq) {  // uniform
+    for (int i = 0; i < MI; ++i) {
+      const v8i a = rows_fragment<FMT>(stage + CF::kAOff + 16 * i * CF::kGB, x, g, row_of(m0, 16 * i + x, p.M));
+      const int sa = (int)(*reinterpret_cast<const uint32_t*>(stage + CF::kSOff + 4 * (16 * i + x)) >> (8 * g));
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
-#pragma unroll
-          for (int j = 0; j < NJ; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                b[u][j], a[u][i], acc[i][j], MfmaFmt<FMT>::kCode, MfmaFmt<FMT>::kCode, 0, (int)(sb[u][j] >> (8 * g)),
-                0, (int)(sa[u][i] >> (8 * g)));
-      }
+      for (int j = 0; j < NJ; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j], a, acc[i][j], MfmaFmt<FMT>::kCode,
+                                                                    MfmaFmt<FMT>::kCode, 0, sb[j], 0, sa);
     }
+    wait_lgkmcnt0();  // every read of this buffer done before the next group is loaded into it
+    memory_fence();
+    buf = buf + 1 == D ? 0 : buf + 1;
   }
+  __syncthreads();  // all wavefronts are done with their rings before the partial tiles take the LDS
+  float* const red = reinterpret_cast<float*>(smem);
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) *reinterpret_cast<v4f*>(&red[wave][16 * i + r16][16 * j + 4 * g]) = acc[i][j];
+    for (int j = 0; j < NJ; ++j)
+      *reinterpret_cast<v4f*>(red + (wave * CF::kTR + 16 * i + x) * CF::kPitch + 16 * j + 4 * g) = acc[i][j];
   __syncthreads();
 
   // Epilogue: four columns of a row per thread and step, rows in order; the
@@ -145,9 +211,9 @@ __global__ __launch_bounds__(64 * W) void gemm_rows_kernel(GemmActParams p) {
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      const v4f x = *reinterpret_cast<const v4f*>(&red[w][r][c]);
+      const v4f part = *reinterpret_cast<const v4f*>(red + (w * CF::kTR + r) * CF::kPitch + c);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = v[e] + x[e];
+      for (int e = 0; e < 4; ++e) v[e] = v[e] + part[e];
     }
     const int64_t m = m0 + r, n = n0 + c;
     const bool in = m < p.M && n < p.N;
@@ -166,14 +232,12 @@ __global__ __launch_bounds__(64 * W) void gemm_rows_kernel(GemmActParams p) {
         v[3] = v[3] + bf16_hi(x.y);
       }
     }
-    if constexpr (NJ >= 2) {
-      if (p.saved_codes != nullptr) {
-        const uint32_t s = scale_byte<kE4M3, kRceil>(max_over8(abs_max4(v)));
-        const uint32_t w = e4m3_encode4(v, s);
-        if (in) {
-          *reinterpret_cast<uint32_t*>(p.saved_codes + code_group(m, n, p.M, 8) + (n & 127)) = w;
-          if ((lane & 7) == 0) p.saved_scales[scale_offset(m, n >> 5, p.M)] = (uint8_t)s;
-        }
+    if (p.saved_codes != nullptr) {
+      const uint32_t s = scale_byte<kE4M3, kRceil>(max_over8(abs_max4(v)));
+      const uint32_t w = e4m3_encode4(v, s);
+      if (in) {
+        *reinterpret_cast<uint32_t*>(p.saved_codes + code_group(m, n, p.M, 8) + (n & 127)) = w;
+        if ((lane & 7) == 0) p.saved_scales[scale_offset(m, n >> 5, p.M)] = (uint8_t)s;
       }
     }
     if (!in || p.c == nullptr) continue;
@@ -206,17 +270,15 @@ __global__ __launch_bounds__(64 * W) void gemm_rows_kernel(GemmActParams p) {
           make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
     }
   }
-  if constexpr (NJ >= 2) {
-    // the pad blocks of the checkpoint's last K group
-    if (p.saved_codes != nullptr && n0 + CF::kTC >= p.N) {
-      const int pad = (int)(((p.N + 127) & ~(int64_t)127) - p.N);  // 0, 32, 64 or 96 columns
-      for (int q = t; q < CF::kTR * pad / 4; q += 64 * W) {
-        const int r = q / (pad / 4);
-        const int64_t m = m0 + r, n = p.N + 4 * (q - r * (pad / 4));
-        if (m < p.M) {
-          *reinterpret_cast<uint32_t*>(p.saved_codes + code_group(m, n, p.M, 8) + (n & 127)) = 0u;
-          if ((n & 31) == 0) p.saved_scales[scale_offset(m, n >> 5, p.M)] = 0;
-        }
+  // the pad blocks of the checkpoint's last K group
+  if (p.saved_codes != nullptr && n0 + CF::kTC >= p.N) {
+    const int pad = (int)(((p.N + 127) & ~(int64_t)127) - p.N);  // 0, 32, 64 or 96 columns
+    for (int q = t; q < CF::kTR * pad / 4; q += 64 * W) {
+      const int r = q / (pad / 4);
+      const int64_t m = m0 + r, n = p.N + 4 * (q - r * (pad / 4));
+      if (m < p.M) {
+        *reinterpret_cast<uint32_t*>(p.saved_codes + code_group(m, n, p.M, 8) + (n & 127)) = 0u;
+        if ((n & 31) == 0) p.saved_scales[scale_offset(m, n >> 5, p.M)] = 0;
       }
     }
   }
@@ -232,60 +294,79 @@ hipError_t launch_tiles(const GemmActParams& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int FMT, int MI, int NJ, int W>
+template <int FMT, int MI, int NJ, int W, int D>
 hipError_t launch_rows(const GemmActParams& p, hipStream_t stream) {
-  using CF = RowsCfg<FMT, MI, NJ, W>;
+  using CF = RowsCfg<FMT, MI, NJ, W, D>;
   const int64_t tiles = ((p.M + CF::kTR - 1) / CF::kTR) * ((p.N + CF::kTC - 1) / CF::kTC);
   if (tiles >= (1ll << 31)) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((gemm_rows_kernel<FMT, MI, NJ, W>), dim3((unsigned)tiles), dim3(64 * W), 0, stream, p);
+  hipLaunchKernelGGL((gemm_rows_kernel<FMT, MI, NJ, W, D>), dim3((unsigned)tiles), dim3(64 * W), 0, stream, p);
   return hipGetLastError();
 }
 
-// Kernel variants.
-enum Shape { kRows1x1, kRows1x2, kRows2x2, kRows4x2, kRows4x4, kTile128x256, kTile256x128, kTile256x256, kNumShapes };
+// The kernel variants: rows_<tile>, the few-rows kernel, and tile_<size>.
+enum Shape { kRows16x32, kRows16x32Deep, kRows32x32, kRows32x32Deep, kRows64x32, kRows64x64, kTile128, kTile256 };
 
+// Which one (times in us, measured with one variant after the other on the
+// same operands; E2M1 / E2M3 / E4M3):
+//  - M <= 32: one row of tiles, so the weights are read once.  Four
+//    wavefronts where the column panels fill the chip (1 x 12288 x 4096:
+//    6.6 / 8.5 / 9.8, eight 6.8 / 8.5 / 11.1), else eight over K
+//    (8 x 4096 x 12288: 7.2 / 8.6 / 10.2, four 8.3 / 9.8 / 9.9).
+//  - up to 320 tiles of 64 x 64 (or M <= 64, whose 128-row tiles would be half
+//    empty) the few-rows kernel with the largest tile that still gives most
+//    compute units one: 512 x 2048 x 2048 64x64 6.8 / 8.4 / 9.8, 128x128
+//    8.2 / 9.5 / 14.9; 128 x 4096 x 4096 64x32 7.0 / 8.2 / 9.7, 64x64
+//    8.1 / 8.9 / 10.3; 64 x 2048 x 12288 32x32 8.0 / 10.3 / 12.6, 64x32
+//    11.4 / 12.8 / 14.7.  With fewer K groups than wavefronts the 128x128
+//    tiles are faster (768 x 2048 x 224: 5.6 / 5.8 / 6.2, 64x64 4.9 / 7.5 / 7.5).
+//  - beyond, 256x256 tiles or, where those would leave compute units idle,
+//    128x128 at two per unit: 8191 x 2048 x 8192 256x256 66 / 79 / 112, 128x128
+//    75 / 102 / 140; 1500 x 4096 x 4096 27 / 28 / 45 against 21 / 26 / 29.
+//    Their cost per round of the chip goes by area, 128x128 15% more.
 int pick_shape(const GemmActParams& p) {
-  if (p.M <= 16) return p.saved_codes == nullptr ? kRows1x1 : kRows1x2;
-  if (p.M <= 32) return kRows2x2;
-  if (p.M <= 64) return kRows4x2;
+  const auto tiles = [&](int64_t m, int64_t n) { return ((p.M + m - 1) / m) * ((p.N + n - 1) / n); };
   const int64_t cus = cu_count();
-  const int64_t t256 = ((p.M + 255) / 256) * ((p.N + 255) / 256);
-  if (t256 >= cus) return kTile256x256;
-  const int64_t t128 = ((p.M + 127) / 128) * ((p.N + 255) / 256);
-  if (t128 >= cus) return kTile128x256;
-  return kRows4x4;
+  if (p.M <= 16) return tiles(16, 32) >= cus ? kRows16x32 : kRows16x32Deep;
+  if (p.M <= 32) return tiles(32, 32) >= cus ? kRows32x32 : kRows32x32Deep;
+  const int64_t t64 = tiles(64, 64);
+  if (p.M <= 64 || t64 <= cus + cus / 4) {
+    if (t64 < cus * 5 / 8) return tiles(64, 32) >= cus / 2 ? kRows64x32 : kRows32x32Deep;
+    if (p.M <= 64 || p.K > 3 * 128) return kRows64x64;
+    return kTile128;
+  }
+  const int64_t t256 = tiles(256, 256), t128 = tiles(128, 128);
+  const int64_t rest = t128 % (2 * cus);  // a last round of at most one tile per unit takes 2/3 of a full one
+  const int64_t cost256 = (t256 + cus - 1) / cus * 65536;
+  const int64_t cost128 = (t128 / (2 * cus) * 32768 + (rest == 0 ? 0 : rest <= cus ? 22000 : 32768)) * 115 / 100;
+  return cost256 <= cost128 ? kTile256 : kTile128;
 }
 
 template <int FMT>
 hipError_t launch_shape(const GemmActParams& p, int shape, hipStream_t stream) {
   switch (shape) {
-    case kRows1x1: return launch_rows<FMT, 1, 1, 8>(p, stream);
-    case kRows1x2: return launch_rows<FMT, 1, 2, 8>(p, stream);
-    case kRows2x2: return launch_rows<FMT, 2, 2, 8>(p, stream);
-    case kRows4x2: return launch_rows<FMT, 4, 2, 8>(p, stream);
-    case kRows4x4: return launch_rows<FMT, 4, 4, 4>(p, stream);
-    case kTile128x256: return launch_tiles<FMT, 128, 256, 2>(p, stream);
-    case kTile256x128: return launch_tiles<FMT, 256, 128, 2>(p, stream);
-    case kTile256x256: return launch_tiles<FMT, 256, 256, 1>(p, stream);
+    case kRows16x32: return launch_rows<FMT, 1, 2, 4, 3>(p, stream);
+    case kRows16x32Deep: return launch_rows<FMT, 1, 2, 8, 2>(p, stream);
+    case kRows32x32: return launch_rows<FMT, 2, 2, 4, 2>(p, stream);
+    case kRows32x32Deep: return launch_rows<FMT, 2, 2, 8, 2>(p, stream);
+    case kRows64x32: return launch_rows<FMT, 4, 2, 4, 2>(p, stream);
+    case kRows64x64: return launch_rows<FMT, 4, 4, 4, 2>(p, stream);
+    case kTile128: return launch_tiles<FMT, 128, 128, 2>(p, stream);
+    case kTile256: return launch_tiles<FMT, 256, 256, 1>(p, stream);
     default: return hipErrorInvalidValue;
   }
 }
 
 }  // namespace
 
-hipError_t launch_gemm_act_shape(const GemmActParams& p, int fmt, int shape, hipStream_t stream) {
+hipError_t launch_gemm_act(const GemmActParams& p, int fmt, hipStream_t stream) {
   if (p.M == 0 || p.N == 0) return hipSuccess;
-  if (shape < 0) shape = pick_shape(p);
+  const int shape = pick_shape(p);
   switch (fmt) {
     case kE2M1: return launch_shape<kE2M1>(p, shape, stream);
     case kE2M3: return launch_shape<kE2M3>(p, shape, stream);
     case kE4M3: return launch_shape<kE4M3>(p, shape, stream);
     default: return hipErrorInvalidValue;
   }
-}
-
-hipError_t launch_gemm_act(const GemmActParams& p, int fmt, hipStream_t stream) {
-  return launch_gemm_act_shape(p, fmt, -1, stream);
 }
 
 }  // namespace mx

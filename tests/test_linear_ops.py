@@ -321,7 +321,8 @@ def test_checkpoint_of_a_column_slice_leaves_its_neighbours():
 
 # ---------------------------------------------------------------- GEMM
 SIZES = [(1, 32, 32), (1, 2080, 160), (5, 96, 128), (16, 64, 2048), (17, 64, 96), (32, 160, 384), (33, 32, 1056),
-         (64, 288, 256), (65, 64, 32), (100, 352, 800), (257, 4096, 96), (300, 8224, 64), (2050, 8224, 96), (4100, 4128, 160)]
+         (3, 8224, 160), (29, 8224, 416), (64, 288, 256), (65, 64, 32), (100, 352, 800), (130, 2080, 416), (257, 4096, 96),
+         (200, 4128, 640), (300, 8224, 64), (2039, 8160, 96), (4100, 4128, 160)]
 
 
 @gpu
