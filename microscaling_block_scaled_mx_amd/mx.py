@@ -6,6 +6,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -150,15 +151,15 @@ def lib():
         L.mx_grouped_gemm.restype = ci
         L.mx_grouped_gemm.argtypes = [ctypes.POINTER(GroupedArgs), vp]
         L.mx_gemm_act.restype = ci
-        L.mx_gemm_act.argtypes = [ctypes.POINTER(GemmActArgs), vp]
+        L.mx_gemm_act.argtypes = [vp, vp]
         L.mx_checkpoint_save.restype = ci
         L.mx_checkpoint_save.argtypes = [vp, ci, i64, i64, i64, vp, vp, vp]
         L.mx_checkpoint_load.restype = ci
         L.mx_checkpoint_load.argtypes = [vp, vp, i64, i64, vp, ci, i64, vp]
         L.mx_quantize_saved.restype = ci
-        L.mx_quantize_saved.argtypes = [ctypes.POINTER(QuantizeSavedArgs), vp]
+        L.mx_quantize_saved.argtypes = [vp, vp]
         L.mx_linear_bwd_saved.restype = ci
-        L.mx_linear_bwd_saved.argtypes = [ctypes.POINTER(LinearBwdArgs), vp]
+        L.mx_linear_bwd_saved.argtypes = [vp, vp]
         L.mx_status_str.restype = ctypes.c_char_p
         L.mx_status_str.argtypes = [ci]
         L.mx_device_supported.restype = ci
@@ -486,58 +487,79 @@ def device_supported(device: int = 0) -> bool:
 
 
 # ---------------------------------------------------------------- linear operators
-def _matrix(t, R: int, C: int, what: str, dtypes=(BF16, F32)):
+# These calls are also made for single tokens, where the kernels take a few
+# microseconds, so their marshalling is kept short: one device query a call
+# and each argument struct packed in one step.
+def _packer(cls):
+    """struct.pack of the fields of an argument struct (Packed as two
+    addresses), with the C layout."""
+    code = {ctypes.c_int64: "q", ctypes.c_int32: "i", ctypes.c_void_p: "P", Packed: "PP"}
+    s = struct.Struct("@" + "".join(code[t] for _, t in cls._fields_) + "0q")
+    assert s.size == ctypes.sizeof(cls)
+    return s.pack
+
+
+_pack_gemm_act = _packer(GemmActArgs)
+_pack_quantize_saved = _packer(QuantizeSavedArgs)
+_pack_linear_bwd = _packer(LinearBwdArgs)
+
+
+def _current():
+    """The current device and its current stream's handle."""
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    return dev, torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else 0
+
+
+def _on_device(t, dev: int, what: str):
+    """Address of a tensor, refused where the kernels could not reach it."""
+    at = t.get_device()
+    if at != dev or at < 0:
+        raise MXError(7, f"{what}: tensor is not on a GPU (the kernels take device memory)" if at < 0 else
+                      f"{what}: tensor is on cuda:{at}, the current device is cuda:{dev}")
+    return t.data_ptr()
+
+
+_DTYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.int16: BF16, torch.uint16: BF16}
+
+
+def _matrix(t, R: int, C: int, dev: int, what: str, dtypes=(BF16, F32)):
     """(address, row pitch, dtype) of an [R][C] operand: a tensor of that
     shape whose rows are dense (a column slice of a wider one included), or
     a contiguous one of R * C elements.  float32 is MX_F32; bfloat16 and the
     16-bit integers that carry bf16 patterns are MX_BF16."""
     if t is None:
-        return None, max(C, 0), dtypes[0]
-    if t.dtype == torch.float32:
-        dtype = F32
-    elif t.dtype in (torch.bfloat16, torch.int16, torch.uint16):
-        dtype = BF16
-    else:
-        raise MXError(4, f"{what}: {t.dtype} is neither float32 nor bf16")
+        return 0, max(C, 0), dtypes[0]
+    dtype = _DTYPES.get(t.dtype, -1)
     if dtype not in dtypes:
-        raise MXError(4, f"{what}: {t.dtype} is not served here")
+        raise MXError(4, f"{what}: {t.dtype} is not served here" if dtype >= 0 else
+                      f"{what}: {t.dtype} is neither float32 nor bf16")
+    ld = C
     if not t.is_contiguous():
         if tuple(t.shape) != (R, C) or (C > 1 and t.stride(1) != 1) or (R > 1 and t.stride(0) < C):
             raise MXError(2, f"{what}: not an [{R}][{C}] tensor with dense rows")
-        ld = t.stride(0) if R > 1 else C
+        if R > 1:
+            ld = t.stride(0)
     elif t.numel() != R * C:
         raise MXError(2, f"{what}: {tuple(t.shape)} does not hold [{R}][{C}]")
-    else:
-        ld = C
-    return _device_ptr(t, what), ld, dtype
+    return _on_device(t, dev, what), ld, dtype
 
 
-def _device_ptr(t, what: str):
-    if not t.is_cuda:
-        raise MXError(7, f"{what}: tensor is not on a GPU (the kernels take device memory)")
-    if t.device.index != torch.cuda.current_device():
-        raise MXError(7, f"{what}: tensor is on cuda:{t.device.index}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    return t.data_ptr()
-
-
-def _operand(p, rows: int, K: int, fmt: int, what: str):
-    """Packed struct of an operand (codes, scales) of [rows] x K, or of None."""
+def _operand(p, rows: int, K: int, fmt: int, dev: int, what: str):
+    """Addresses of an operand's codes and scales, [rows] x K, or (0, 0)."""
     if p is None:
-        return Packed(None, None)
-    groups = (K + 127) // 128
-    for t, per_row, part in ((p[0], 16 * BITS.get(fmt, 0), "codes"), (p[1], 4, "scales")):
-        if not t.is_contiguous():
-            raise MXError(2, f"{what} {part}: tensor argument is a strided view; pass a contiguous tensor")
-        _need(t, groups * rows * per_row, f"{what} {part}")
-    return Packed(_device_ptr(p[0], what), _device_ptr(p[1], what))
+        return 0, 0
+    codes, scales = p
+    if not (codes.is_contiguous() and scales.is_contiguous()):
+        raise MXError(2, f"{what}: tensor argument is a strided view; pass a contiguous tensor")
+    n = (K + 127) // 128 * rows * 4
+    if codes.nbytes < n * BITS.get(fmt, 0) * 4 or scales.nbytes < n:
+        raise MXError(2, f"{what}: codes and scales hold {codes.nbytes} and {scales.nbytes} bytes, "
+                         f"the call touches {n * BITS.get(fmt, 0) * 4} and {n}")
+    return _on_device(codes, dev, what), _on_device(scales, dev, what)
 
 
-def _vector(t, n: int, what: str, dtypes):
-    if t is None:
-        return None, dtypes[0]
-    ptr, _, dtype = _matrix(t, 1, n, what, dtypes)
-    return ptr, dtype
+def _handle(stream, current: int):
+    return current if stream is None else _stream(stream)
 
 
 def gemm_act(a, b, M: int, N: int, K: int, fmt: int, c=None, act: int = ACT_NONE, bias=None, residual=None,
@@ -546,32 +568,36 @@ def gemm_act(a, b, M: int, N: int, K: int, fmt: int, c=None, act: int = ACT_NONE
     multiples of 32), and / or saved = (codes, scales), the 8-bit checkpoint
     of A . B^T + bias.  c and residual are [M][N] of one type (bf16 or
     float32), rows dense; residual may be c."""
-    cp, ldc, c_dtype = _matrix(c, M, N, "gemm_act C")
-    rp, ldr, r_dtype = _matrix(residual, M, N, "gemm_act residual")
+    dev, here = _current()
+    cp, ldc, c_dtype = _matrix(c, M, N, dev, "gemm_act C")
+    rp, ldr, r_dtype = _matrix(residual, M, N, dev, "gemm_act residual")
     if residual is not None and c is not None and r_dtype != c_dtype:
         raise MXError(4, "gemm_act: residual and C are of different types")
-    bp, bias_dtype = _vector(bias, N, "gemm_act bias", (BF16, F32))
-    g = GemmActArgs(M, N, K, fmt, act, _operand(a, M, K, fmt, "gemm_act A"), _operand(b, N, K, fmt, "gemm_act B"),
-                    bp, rp, cp, ldr, ldc, bias_dtype, c_dtype, _operand(saved, M, N, E4M3, "gemm_act saved"))
-    _check(lib().mx_gemm_act(ctypes.byref(g), _stream(stream)), "mx_gemm_act")
+    bp, _, bias_dtype = _matrix(bias, 1, N, dev, "gemm_act bias")
+    args = _pack_gemm_act(M, N, K, fmt, act, *_operand(a, M, K, fmt, dev, "gemm_act A"),
+                          *_operand(b, N, K, fmt, dev, "gemm_act B"), bp, rp, cp, ldr, ldc, bias_dtype, c_dtype,
+                          *_operand(saved, M, N, E4M3, dev, "gemm_act saved"))
+    _check(lib().mx_gemm_act(args, _handle(stream, here)), "mx_gemm_act")
 
 
 def checkpoint_save(x, saved, stream=None):
     """mx_checkpoint_save: x [R][C] (bf16 or float32, rows dense) into saved =
     (codes, scales) of alloc_packed(R, C, E4M3)."""
     R, C = x.shape
-    xp, ldx, dtype = _matrix(x, R, C, "checkpoint_save x")
-    p = _operand(saved, R, C, E4M3, "checkpoint_save")
-    _check(lib().mx_checkpoint_save(xp, dtype, R, C, ldx, p.codes, p.scales, _stream(stream)), "mx_checkpoint_save")
+    dev, here = _current()
+    xp, ldx, dtype = _matrix(x, R, C, dev, "checkpoint_save x")
+    codes, scales = _operand(saved, R, C, E4M3, dev, "checkpoint_save")
+    _check(lib().mx_checkpoint_save(xp, dtype, R, C, ldx, codes, scales, _handle(stream, here)), "mx_checkpoint_save")
 
 
 def checkpoint_load(saved, y, stream=None):
     """mx_checkpoint_load: the values of saved = (codes, scales) into y [R][C]
     (bf16 or float32, rows dense)."""
     R, C = y.shape
-    yp, ldy, dtype = _matrix(y, R, C, "checkpoint_load y")
-    p = _operand(saved, R, C, E4M3, "checkpoint_load")
-    _check(lib().mx_checkpoint_load(p.codes, p.scales, R, C, yp, dtype, ldy, _stream(stream)), "mx_checkpoint_load")
+    dev, here = _current()
+    yp, ldy, dtype = _matrix(y, R, C, dev, "checkpoint_load y")
+    codes, scales = _operand(saved, R, C, E4M3, dev, "checkpoint_load")
+    _check(lib().mx_checkpoint_load(codes, scales, R, C, yp, dtype, ldy, _handle(stream, here)), "mx_checkpoint_load")
 
 
 def _rows32(R: int):
@@ -584,14 +610,15 @@ def quantize_saved(R: int, C: int, fmt: int, scale_mode: int, hadamard: bool = F
     (bf16) is given (x itself with ACT_NONE and no checkpoint), for any R:
     row [R] x K=C, col [C] x K = R rounded up to 32, and the column sums
     (partials float32 [ceil(R/128)][C])."""
-    xp, ldx, _ = _matrix(x, R, C, "quantize_saved x", (BF16,))
-    part, _ = _vector(colsum_partials, (R + 127) // 128 * C, "quantize_saved colsum partials", (F32,))
-    total, _ = _vector(colsum, C, "quantize_saved colsum", (F32,))
-    q = QuantizeSavedArgs(R, C, fmt, scale_mode, int(hadamard), act, xp, ldx,
-                          _operand(saved, R, C, E4M3, "quantize_saved checkpoint"),
-                          _operand(row, R, C, fmt, "quantize_saved row"),
-                          _operand(col, C, _rows32(R), fmt, "quantize_saved col"), part, total)
-    _check(lib().mx_quantize_saved(ctypes.byref(q), _stream(stream)), "mx_quantize_saved")
+    dev, here = _current()
+    xp, ldx, _ = _matrix(x, R, C, dev, "quantize_saved x", (BF16,))
+    part, _, _ = _matrix(colsum_partials, (R + 127) // 128, C, dev, "quantize_saved colsum partials", (F32,))
+    total, _, _ = _matrix(colsum, 1, C, dev, "quantize_saved colsum", (F32,))
+    args = _pack_quantize_saved(R, C, fmt, scale_mode, int(hadamard), act, xp, ldx,
+                                *_operand(saved, R, C, E4M3, dev, "quantize_saved checkpoint"),
+                                *_operand(row, R, C, fmt, dev, "quantize_saved row"),
+                                *_operand(col, C, _rows32(R), fmt, dev, "quantize_saved col"), part, total)
+    _check(lib().mx_quantize_saved(args, _handle(stream, here)), "mx_quantize_saved")
 
 
 def linear_bwd_saved(M: int, N: int, K: int, dY, saved_x, Wc, fmt: int, scale_mode: int, hadamard: bool = False,
@@ -601,20 +628,21 @@ def linear_bwd_saved(M: int, N: int, K: int, dY, saved_x, Wc, fmt: int, scale_mo
     (float32), each optional, of Y = act(X W^T + b), X = x_act(saved_x).
     Work operands: dPr [M] x K=N, and dPc [N], Xc [K] x K = M rounded up to
     32; db_partials float32 [ceil(M/128)][N]."""
-    yp, lddy, _ = _matrix(dY, M, N, "linear_bwd_saved dY", (BF16,))
-    xp, lddx, _ = _matrix(dX, M, K, "linear_bwd_saved dX", (BF16,))
-    wp, lddw, dw_dtype = _matrix(dW, N, K, "linear_bwd_saved dW")
-    bp, _ = _vector(db, N, "linear_bwd_saved db", (F32,))
-    part, _ = _vector(db_partials, (M + 127) // 128 * N, "linear_bwd_saved db partials", (F32,))
+    dev, here = _current()
+    yp, lddy, _ = _matrix(dY, M, N, dev, "linear_bwd_saved dY", (BF16,))
+    xp, lddx, _ = _matrix(dX, M, K, dev, "linear_bwd_saved dX", (BF16,))
+    wp, lddw, dw_dtype = _matrix(dW, N, K, dev, "linear_bwd_saved dW")
+    bp, _, _ = _matrix(db, 1, N, dev, "linear_bwd_saved db", (F32,))
+    part, _, _ = _matrix(db_partials, (M + 127) // 128, N, dev, "linear_bwd_saved db partials", (F32,))
     Mp = _rows32(M)
-    b = LinearBwdArgs(M, N, K, fmt, scale_mode, int(hadamard), act, x_act, int(accumulate), yp, lddy,
-                      _operand(saved_pre, M, N, E4M3, "linear_bwd_saved saved_pre"),
-                      _operand(saved_x, M, K, E4M3, "linear_bwd_saved saved_x"),
-                      _operand(Wc, K, N, fmt, "linear_bwd_saved Wc"), xp, lddx, wp, lddw, dw_dtype, 0, bp, part,
-                      _operand(dPr, M, N, fmt, "linear_bwd_saved dPr"),
-                      _operand(dPc, N, Mp, fmt, "linear_bwd_saved dPc"),
-                      _operand(Xc, K, Mp, fmt, "linear_bwd_saved Xc"))
-    _check(lib().mx_linear_bwd_saved(ctypes.byref(b), _stream(stream)), "mx_linear_bwd_saved")
+    args = _pack_linear_bwd(M, N, K, fmt, scale_mode, int(hadamard), act, x_act, int(accumulate), yp, lddy,
+                            *_operand(saved_pre, M, N, E4M3, dev, "linear_bwd_saved saved_pre"),
+                            *_operand(saved_x, M, K, E4M3, dev, "linear_bwd_saved saved_x"),
+                            *_operand(Wc, K, N, fmt, dev, "linear_bwd_saved Wc"), xp, lddx, wp, lddw, dw_dtype, 0, bp,
+                            part, *_operand(dPr, M, N, fmt, dev, "linear_bwd_saved dPr"),
+                            *_operand(dPc, N, Mp, fmt, dev, "linear_bwd_saved dPc"),
+                            *_operand(Xc, K, Mp, fmt, dev, "linear_bwd_saved Xc"))
+    _check(lib().mx_linear_bwd_saved(args, _handle(stream, here)), "mx_linear_bwd_saved")
 
 
 def status_str(st: int) -> str:
