@@ -52,13 +52,14 @@ template <int ACT>
 __device__ __forceinline__ float act_slope(float x) {
   if constexpr (ACT == kActNone) return 1.0f;
   const float s = sigmoid2(act_exponent<ACT>(x));
-  const float w = s * (1.0f - s);  // 0 once |z| passes 25: the slope's second term is then below its rounding
+  const float w = __builtin_fmaf(-s, s, s);  // s (1 - s): 0 once |z| passes 25, the term it scales then below s's rounding
+  // the term's other factor, kept finite so that w = 0 ends it
+  const float y = __builtin_fminf(__builtin_fmaxf(x, -0x1p40f), 0x1p40f);
   if constexpr (ACT == kActGelu) {
     const float C = 0x1.988454p+0f, D = 0x1.b6676cp-3f;  // z' = C + D x^2
-    const float xz = x * __builtin_fmaf(x * x, D, C);
-    return __builtin_fmaf(w == 0.0f ? 0.0f : xz, w, s);  // (0 inf is no NaN here)
+    return __builtin_fmaf(y * __builtin_fmaf(y * y, D, C), w, s);
   } else {
-    return __builtin_fmaf(w == 0.0f ? 0.0f : x, w, s);
+    return __builtin_fmaf(y, w, s);
   }
 }
 
@@ -81,32 +82,47 @@ __device__ __forceinline__ void e4m3_decode4(uint32_t w, float scale, float (&v)
 #endif
 }
 
-// Four values to E4M3 codes under scale byte `s` (RCEIL: |v| <= 448 2^X, so
-// nothing saturates).  The conversion divides by 2^X exactly; a block with
-// X = -127 is converted as (v 2^64) / 2^-63, and a NaN block's codes are 0.
-__device__ __forceinline__ uint32_t e4m3_encode4(const float (&v)[4], uint32_t s) {
+// N values to E4M3 codes (four a dword) under scale byte `s` (RCEIL: |v| <=
+// 448 2^X, so nothing saturates); the values may be rescaled in place.  The
+// conversion divides by 2^X exactly; a block with X = -127, whose scale is no
+// normal binary32, is converted as (v 2^64) / 2^-63 (only a wavefront that
+// holds such a block pays), and a NaN block's codes are 0.
+template <int N>
+__device__ __forceinline__ void e4m3_encode(float (&v)[N], uint32_t s, uint32_t (&w)[N / 4]) {
 #if defined(__HIP_DEVICE_COMPILE__)
   typedef short s2 __attribute__((ext_vector_type(2)));
   const bool tiny = s == 0u;
-  const float up = tiny ? 0x1p64f : 1.0f;
   const float sc = __uint_as_float((tiny ? 64u : (s == 0xffu ? 127u : s)) << 23);
-  s2 q = {0, 0};
-  q = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(q, v[0] * up, v[1] * up, sc, false);
-  q = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(q, v[2] * up, v[3] * up, sc, true);
-  return s == 0xffu ? 0u : __builtin_bit_cast(uint32_t, q);
-#else
-  return 0u;
+  if (__builtin_amdgcn_ballot_w64(tiny) != 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = tiny ? v[i] * 0x1p64f : v[i];
+  }
+#pragma unroll
+  for (int d = 0; d < N / 4; ++d) {
+    s2 q = {0, 0};
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(q, v[4 * d + 0], v[4 * d + 1], sc, false);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(q, v[4 * d + 2], v[4 * d + 3], sc, true);
+    w[d] = s == 0xffu ? 0u : __builtin_bit_cast(uint32_t, q);
+  }
 #endif
 }
 
-// Largest |v| of four values as a bit pattern (a NaN sorts above infinity).
-__device__ __forceinline__ uint32_t abs_max4(const float (&v)[4], uint32_t m = 0u) {
+// Largest |v| as a bit pattern (a NaN sorts above infinity).  Positive
+// values order as signed integers, negative ones as unsigned integers above
+// every positive one, so two integer maxima (three operands an instruction)
+// need no absolute values.
+template <int N>
+__device__ __forceinline__ uint32_t abs_max(const float (&v)[N]) {
+  int32_t pos = 0;
+  uint32_t neg = 0u;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t b = __float_as_uint(v[i]) & 0x7fffffffu;
-    m = m > b ? m : b;
+  for (int i = 0; i < N; ++i) {
+    const uint32_t b = __float_as_uint(v[i]);
+    pos = pos > (int32_t)b ? pos : (int32_t)b;
+    neg = neg > b ? neg : b;
   }
-  return m;
+  neg &= 0x7fffffffu;
+  return (uint32_t)pos > neg ? (uint32_t)pos : neg;
 }
 
 // One step of a reduction within a row of 16 lanes: the value of the lane

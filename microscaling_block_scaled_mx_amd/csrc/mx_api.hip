@@ -246,8 +246,7 @@ int validate_gemm_act(const mx_gemm_act_args& a) {
   return MX_OK;
 }
 
-int gemm_act_launch(const mx_gemm_act_args& a, hipStream_t s) {
-  if (a.M == 0 || a.N == 0) return MX_OK;
+mx::GemmActParams gemm_act_params(const mx_gemm_act_args& a) {
   mx::GemmActParams p;
   memset(&p, 0, sizeof p);
   p.a_codes = bytes(a.A.codes);
@@ -267,7 +266,11 @@ int gemm_act_launch(const mx_gemm_act_args& a, hipStream_t s) {
   p.act = a.act;
   p.saved_codes = bytes(a.saved.codes);
   p.saved_scales = bytes(a.saved.scales);
-  return launched(mx::launch_gemm_act(p, a.fmt, s));
+  return p;
+}
+
+int gemm_act_launch(const mx_gemm_act_args& a, hipStream_t s) {
+  return launched(mx::launch_gemm_act(gemm_act_params(a), a.fmt, s));
 }
 
 int validate_checkpoint(const void* x, int dtype, int64_t R, int64_t C, int64_t ld, const void* codes,
@@ -305,11 +308,22 @@ int validate_quantize_saved(const mx_quantize_saved_args& a) {
   return MX_OK;
 }
 
-int quantize_saved_launch(const mx_quantize_saved_args& a, hipStream_t s) {
+// `before`: a pack earlier on the stream whose column sums this launch
+// finishes beside its own work (nullptr: none).  `finish`: whether this
+// pack's own are finished by a launch after it.
+int quantize_saved_launch(const mx_quantize_saved_args& a, hipStream_t s, const mx_quantize_saved_args* before = nullptr,
+                          bool finish = true) {
   if (a.C == 0) return MX_OK;
   int st = MX_OK;
   if (a.R > 0) {
     mx::SavedPackParams p;
+    memset(&p, 0, sizeof p);
+    if (before) {
+      p.sum_partials = before->colsum_partials;
+      p.sum_rows = (before->R + 127) / 128;
+      p.sum_cols = before->C;
+      p.sum_out = before->colsum;
+    }
     p.x = static_cast<const uint16_t*>(a.x);
     p.ldx = a.ldx;
     p.saved_codes = bytes(a.saved.codes);
@@ -323,7 +337,7 @@ int quantize_saved_launch(const mx_quantize_saved_args& a, hipStream_t s) {
     p.partials = a.colsum_partials;
     st = launched(mx::launch_quantize_saved(p, a.fmt, a.scale_mode, a.hadamard, a.act, s));
   }
-  if (st == MX_OK && a.colsum)  // no rows: no partials, zeros
+  if (st == MX_OK && a.colsum && finish)  // no rows: no partials, zeros
     st = launched(mx::launch_colsum_finish(a.colsum_partials, (a.R + 127) / 128, a.C, a.colsum, 1, s));
   return st;
 }
@@ -902,11 +916,14 @@ int mx_linear_bwd_saved(const mx_linear_bwd_args* args, void* stream) {
   if (want_dw && (st = validate_gemm_act(w)) != MX_OK) return st;
   if ((st = check_device()) != MX_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (want_g && (st = quantize_saved_launch(g, s)) != MX_OK) return st;
-  if (want_dw && (st = quantize_saved_launch(x, s)) != MX_OK) return st;
-  if (want_dx && (st = gemm_act_launch(d, s)) != MX_OK) return st;
-  if (want_dw && (st = gemm_act_launch(w, s)) != MX_OK) return st;
-  return MX_OK;
+  // db's partials are finished beside the pack of X, where there is one
+  const bool beside = want_dw && a.db && a.M > 0;
+  if (want_g && (st = quantize_saved_launch(g, s, nullptr, !beside)) != MX_OK) return st;
+  if (want_dw && (st = quantize_saved_launch(x, s, beside ? &g : nullptr)) != MX_OK) return st;
+  if (want_dx && want_dw)
+    return launched(mx::launch_gemm_act_pair(gemm_act_params(d), gemm_act_params(w), a.fmt, s));
+  if (want_dx) return gemm_act_launch(d, s);
+  return want_dw ? gemm_act_launch(w, s) : MX_OK;
 }
 
 const char* mx_status_str(int status) {

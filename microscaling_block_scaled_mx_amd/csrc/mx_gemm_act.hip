@@ -23,10 +23,29 @@ namespace {
 typedef float v4f __attribute__((ext_vector_type(4)));
 
 // ------------------------------------------------------------------ many rows
-template <int FMT, int BM, int BN, int OCC>
-__global__ __launch_bounds__(tile_threads(BM, BN, kEpiAct), OCC) void gemm_act_kernel(GemmActParams p) {
+// The products of a launch, one or two of them: workgroups from `first` on
+// compute tiles of the second.  (A type of its own for one: indexed by the
+// workgroup, the arguments would be loaded again wherever they are used, which
+// cost a few-rows launch 0.5 us.)
+template <int COUNT>
+struct Products {
+  GemmActParams p[COUNT];
+  int first;  // tiles of p[0]
+};
+template <int COUNT>
+__device__ __forceinline__ const GemmActParams& product_of(const Products<COUNT>& all, int& tile) {
+  if constexpr (COUNT == 1) return all.p[0];
+  if (tile < all.first) return all.p[0];
+  tile -= all.first;
+  return all.p[1];
+}
+
+template <int FMT, int BM, int BN, int OCC, int COUNT>
+__global__ __launch_bounds__(tile_threads(BM, BN, kEpiAct), OCC) void gemm_act_kernel(Products<COUNT> all) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[Cfg<FMT, BM, BN, kDense, kEpiAct, OCC>::kSmem];
-  gemm_tile<FMT, BM, BN, kDense, kEpiAct, OCC>(p, blockIdx.x, 0, 0, smem);
+  int tile = blockIdx.x;
+  const GemmActParams& p = product_of(all, tile);
+  gemm_tile<FMT, BM, BN, kDense, kEpiAct, OCC>(p, tile, 0, 0, smem);
 }
 
 // ------------------------------------------------------------------ few rows
@@ -104,14 +123,16 @@ __device__ __forceinline__ void memory_fence() {
 #endif
 }
 
-template <int FMT, int MI, int NJ, int W, int D>
-__global__ __launch_bounds__(64 * W) void gemm_rows_kernel(GemmActParams p) {
+template <int FMT, int MI, int NJ, int W, int D, int COUNT>
+__global__ __launch_bounds__(64 * W) void gemm_rows_kernel(Products<COUNT> all) {
   using CF = RowsCfg<FMT, MI, NJ, W, D>;
+  int tile = blockIdx.x;
+  const GemmActParams& p = product_of(all, tile);
   __shared__ __attribute__((aligned(16))) uint8_t smem[CF::kSmem];
   const int t = threadIdx.x, lane = t & 63, wave = wave_uniform(t >> 6);
   const int x = lane & 15, g = lane >> 4;
   const int tiles_m = (int)((p.M + CF::kTR - 1) / CF::kTR);
-  const int tn = blockIdx.x / tiles_m, tm = blockIdx.x - tn * tiles_m;
+  const int tn = tile / tiles_m, tm = tile - tn * tiles_m;
   const int64_t m0 = (int64_t)tm * CF::kTR, n0 = (int64_t)tn * CF::kTC;
   const int nq = (int)((p.K + 127) / 128);
   const int n_own = wave < nq ? (nq - wave + W - 1) / W : 0;  // this wavefront's K groups
@@ -233,10 +254,12 @@ __global__ __launch_bounds__(64 * W) void gemm_rows_kernel(GemmActParams p) {
       }
     }
     if (p.saved_codes != nullptr) {
-      const uint32_t s = scale_byte<kE4M3, kRceil>(max_over8(abs_max4(v)));
-      const uint32_t w = e4m3_encode4(v, s);
+      const uint32_t s = scale_byte<kE4M3, kRceil>(max_over8(abs_max(v)));
+      float u[4] = {v[0], v[1], v[2], v[3]};
+      uint32_t w[1];
+      e4m3_encode(u, s, w);
       if (in) {
-        *reinterpret_cast<uint32_t*>(p.saved_codes + code_group(m, n, p.M, 8) + (n & 127)) = w;
+        *reinterpret_cast<uint32_t*>(p.saved_codes + code_group(m, n, p.M, 8) + (n & 127)) = w[0];
         if ((lane & 7) == 0) p.saved_scales[scale_offset(m, n >> 5, p.M)] = (uint8_t)s;
       }
     }
@@ -285,26 +308,40 @@ __global__ __launch_bounds__(64 * W) void gemm_rows_kernel(GemmActParams p) {
 }
 
 // ------------------------------------------------------------------ launch
+int64_t tile_count(const GemmActParams& p, int bm, int bn) { return ((p.M + bm - 1) / bm) * ((p.N + bn - 1) / bn); }
+
+// q: a second product for the same launch, or nullptr.
 template <int FMT, int BM, int BN, int OCC>
-hipError_t launch_tiles(const GemmActParams& p, hipStream_t stream) {
-  const int64_t tiles = ((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
-  if (tiles >= (1ll << 31)) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((gemm_act_kernel<FMT, BM, BN, OCC>), dim3((unsigned)tiles),
-                     dim3(Cfg<FMT, BM, BN, kDense, kEpiAct, OCC>::kThreads), 0, stream, p);
+hipError_t launch_tiles(const GemmActParams& p, const GemmActParams* q, hipStream_t stream) {
+  constexpr int kThreads = Cfg<FMT, BM, BN, kDense, kEpiAct, OCC>::kThreads;
+  const int64_t first = tile_count(p, BM, BN), all = first + (q ? tile_count(*q, BM, BN) : 0);
+  if (all >= (1ll << 31)) return hipErrorInvalidValue;
+  if (q)
+    hipLaunchKernelGGL((gemm_act_kernel<FMT, BM, BN, OCC, 2>), dim3((unsigned)all), dim3(kThreads), 0, stream,
+                       (Products<2>{{p, *q}, (int)first}));
+  else
+    hipLaunchKernelGGL((gemm_act_kernel<FMT, BM, BN, OCC, 1>), dim3((unsigned)all), dim3(kThreads), 0, stream,
+                       (Products<1>{{p}, (int)first}));
   return hipGetLastError();
 }
 
 template <int FMT, int MI, int NJ, int W, int D>
-hipError_t launch_rows(const GemmActParams& p, hipStream_t stream) {
-  using CF = RowsCfg<FMT, MI, NJ, W, D>;
-  const int64_t tiles = ((p.M + CF::kTR - 1) / CF::kTR) * ((p.N + CF::kTC - 1) / CF::kTC);
-  if (tiles >= (1ll << 31)) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((gemm_rows_kernel<FMT, MI, NJ, W, D>), dim3((unsigned)tiles), dim3(64 * W), 0, stream, p);
+hipError_t launch_rows(const GemmActParams& p, const GemmActParams* q, hipStream_t stream) {
+  const int64_t first = tile_count(p, 16 * MI, 16 * NJ), all = first + (q ? tile_count(*q, 16 * MI, 16 * NJ) : 0);
+  if (all >= (1ll << 31)) return hipErrorInvalidValue;
+  if (q)
+    hipLaunchKernelGGL((gemm_rows_kernel<FMT, MI, NJ, W, D, 2>), dim3((unsigned)all), dim3(64 * W), 0, stream,
+                       (Products<2>{{p, *q}, (int)first}));
+  else
+    hipLaunchKernelGGL((gemm_rows_kernel<FMT, MI, NJ, W, D, 1>), dim3((unsigned)all), dim3(64 * W), 0, stream,
+                       (Products<1>{{p}, (int)first}));
   return hipGetLastError();
 }
 
 // The kernel variants: rows_<tile>, the few-rows kernel, and tile_<size>.
-enum Shape { kRows16x32, kRows16x32Deep, kRows32x32, kRows32x32Deep, kRows64x32, kRows64x64, kTile128, kTile256 };
+enum Shape {
+  kRows16x32, kRows16x32Deep, kRows32x32, kRows32x32Deep, kRows64x32, kRows64x64, kTile128, kTile256x128, kTile256
+};
 
 // Which one (times in us, measured with one variant after the other on the
 // same operands; E2M1 / E2M3 / E4M3):
@@ -322,36 +359,53 @@ enum Shape { kRows16x32, kRows16x32Deep, kRows32x32, kRows32x32Deep, kRows64x32,
 //  - beyond, 256x256 tiles or, where those would leave compute units idle,
 //    128x128 at two per unit: 8191 x 2048 x 8192 256x256 66 / 79 / 112, 128x128
 //    75 / 102 / 140; 1500 x 4096 x 4096 27 / 28 / 45 against 21 / 26 / 29.
-//    Their cost per round of the chip goes by area, 128x128 15% more.
-int pick_shape(const GemmActParams& p) {
-  const auto tiles = [&](int64_t m, int64_t n) { return ((p.M + m - 1) / m) * ((p.N + n - 1) / n); };
+//    Their cost per round of the chip goes by area, 128x128 15% more.  With a
+//    checkpoint (E2M1: or an activation) in the epilogue, over several rounds,
+//    256x128 at two per unit, so that one tile's epilogue runs beside
+//    another's products: 8192 x 8192 x 2048 GELU + checkpoint 126 / 151 / 194,
+//    256x256 144 / 158 / 192; without either 99 / 123 against 103 / 121.
+int pick_shape(int fmt, const GemmActParams& p) {
   const int64_t cus = cu_count();
-  if (p.M <= 16) return tiles(16, 32) >= cus ? kRows16x32 : kRows16x32Deep;
-  if (p.M <= 32) return tiles(32, 32) >= cus ? kRows32x32 : kRows32x32Deep;
-  const int64_t t64 = tiles(64, 64);
+  if (p.M <= 16) return tile_count(p, 16, 32) >= cus ? kRows16x32 : kRows16x32Deep;
+  if (p.M <= 32) return tile_count(p, 32, 32) >= cus ? kRows32x32 : kRows32x32Deep;
+  const int64_t t64 = tile_count(p, 64, 64);
   if (p.M <= 64 || t64 <= cus + cus / 4) {
-    if (t64 < cus * 5 / 8) return tiles(64, 32) >= cus / 2 ? kRows64x32 : kRows32x32Deep;
+    if (t64 < cus * 5 / 8) return tile_count(p, 64, 32) >= cus / 2 ? kRows64x32 : kRows32x32Deep;
     if (p.M <= 64 || p.K > 3 * 128) return kRows64x64;
     return kTile128;
   }
-  const int64_t t256 = tiles(256, 256), t128 = tiles(128, 128);
+  const int64_t t256 = tile_count(p, 256, 256), t128 = tile_count(p, 128, 128);
   const int64_t rest = t128 % (2 * cus);  // a last round of at most one tile per unit takes 2/3 of a full one
   const int64_t cost256 = (t256 + cus - 1) / cus * 65536;
   const int64_t cost128 = (t128 / (2 * cus) * 32768 + (rest == 0 ? 0 : rest <= cus ? 22000 : 32768)) * 115 / 100;
-  return cost256 <= cost128 ? kTile256 : kTile128;
+  if (cost256 > cost128) return kTile128;
+  const bool busy = p.saved_codes != nullptr || (fmt == kE2M1 && p.act != kActNone);
+  return fmt != kE4M3 && busy && t256 > cus ? kTile256x128 : kTile256;
 }
 
 template <int FMT>
-hipError_t launch_shape(const GemmActParams& p, int shape, hipStream_t stream) {
+hipError_t launch_shape(const GemmActParams& p, const GemmActParams* q, int shape, hipStream_t stream) {
   switch (shape) {
-    case kRows16x32: return launch_rows<FMT, 1, 2, 4, 3>(p, stream);
-    case kRows16x32Deep: return launch_rows<FMT, 1, 2, 8, 2>(p, stream);
-    case kRows32x32: return launch_rows<FMT, 2, 2, 4, 2>(p, stream);
-    case kRows32x32Deep: return launch_rows<FMT, 2, 2, 8, 2>(p, stream);
-    case kRows64x32: return launch_rows<FMT, 4, 2, 4, 2>(p, stream);
-    case kRows64x64: return launch_rows<FMT, 4, 4, 4, 2>(p, stream);
-    case kTile128: return launch_tiles<FMT, 128, 128, 2>(p, stream);
-    case kTile256: return launch_tiles<FMT, 256, 256, 1>(p, stream);
+    case kRows16x32: return launch_rows<FMT, 1, 2, 4, 3>(p, q, stream);
+    case kRows16x32Deep: return launch_rows<FMT, 1, 2, 8, 2>(p, q, stream);
+    case kRows32x32: return launch_rows<FMT, 2, 2, 4, 2>(p, q, stream);
+    case kRows32x32Deep: return launch_rows<FMT, 2, 2, 8, 2>(p, q, stream);
+    case kRows64x32: return launch_rows<FMT, 4, 2, 4, 2>(p, q, stream);
+    case kRows64x64: return launch_rows<FMT, 4, 4, 4, 2>(p, q, stream);
+    case kTile128: return launch_tiles<FMT, 128, 128, 2>(p, q, stream);
+    case kTile256x128:
+      if constexpr (FMT != kE4M3) return launch_tiles<FMT, 256, 128, 2>(p, q, stream);
+      else return hipErrorInvalidValue;
+    case kTile256: return launch_tiles<FMT, 256, 256, 1>(p, q, stream);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+hipError_t launch_fmt(int fmt, const GemmActParams& p, const GemmActParams* q, int shape, hipStream_t stream) {
+  switch (fmt) {
+    case kE2M1: return launch_shape<kE2M1>(p, q, shape, stream);
+    case kE2M3: return launch_shape<kE2M3>(p, q, shape, stream);
+    case kE4M3: return launch_shape<kE4M3>(p, q, shape, stream);
     default: return hipErrorInvalidValue;
   }
 }
@@ -360,13 +414,16 @@ hipError_t launch_shape(const GemmActParams& p, int shape, hipStream_t stream) {
 
 hipError_t launch_gemm_act(const GemmActParams& p, int fmt, hipStream_t stream) {
   if (p.M == 0 || p.N == 0) return hipSuccess;
-  const int shape = pick_shape(p);
-  switch (fmt) {
-    case kE2M1: return launch_shape<kE2M1>(p, shape, stream);
-    case kE2M3: return launch_shape<kE2M3>(p, shape, stream);
-    case kE4M3: return launch_shape<kE4M3>(p, shape, stream);
-    default: return hipErrorInvalidValue;
-  }
+  return launch_fmt(fmt, p, nullptr, pick_shape(fmt, p), stream);
+}
+
+// The results do not depend on whether a launch is shared: each product keeps
+// the variant it has alone.
+hipError_t launch_gemm_act_pair(const GemmActParams& p, const GemmActParams& q, int fmt, hipStream_t stream) {
+  const bool both = p.M > 0 && p.N > 0 && q.M > 0 && q.N > 0;
+  if (both && pick_shape(fmt, p) == pick_shape(fmt, q)) return launch_fmt(fmt, p, &q, pick_shape(fmt, p), stream);
+  const hipError_t e = launch_gemm_act(p, fmt, stream);
+  return e == hipSuccess ? launch_gemm_act(q, fmt, stream) : e;
 }
 
 }  // namespace mx

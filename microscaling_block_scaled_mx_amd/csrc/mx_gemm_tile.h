@@ -298,34 +298,24 @@ __device__ __forceinline__ void dense_tile(int bid, int tiles_m, int tiles_n, in
   tn = r / gsize;
 }
 
-// Four consecutive codes of a 32-column MFMA tile row per lane -> its 32-byte
-// E4M3 block.  Lane l holds columns 8 (e / 4) + 4 (l / 32) + e % 4 (e = 0..15)
-// of row l % 32, so the row's maximum and its bytes come from lanes l and
-// l ^ 32: one half-wavefront exchange for the maximum, two for the codes,
-// after which each lane owns 16 consecutive bytes.  `codes` and `scale` are
-// this row's; nothing is stored where `store` is false.
-__device__ __forceinline__ void checkpoint_block(const float (&v)[16], int g, uint8_t* codes, uint8_t* scale,
-                                                 bool store) {
+// One row's 32-byte E4M3 block from a 32-column MFMA tile: lane l holds
+// columns 8 (e / 4) + 4 (l / 32) + e % 4 (e = 0..15) of row l % 32, so the
+// row's maximum and its bytes come from lanes l and l ^ 32: one exchange of
+// half wavefronts for the maximum, two for the codes, after which each lane
+// owns the 16 bytes at 16 (l / 32).  Returns the scale byte.
+__device__ __forceinline__ uint32_t checkpoint_block(float (&v)[16], uint4& codes) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  float q[4][4];
-  uint32_t m = 0u;
-#pragma unroll
-  for (int d = 0; d < 4; ++d) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) q[d][e] = v[4 * d + e];
-    m = abs_max4(q[d], m);
-  }
+  const uint32_t m = abs_max(v);
   const auto mm = __builtin_amdgcn_permlane32_swap(m, m, false, false);
   const uint32_t s = scale_byte<kE4M3, kRceil>(max_u32(mm[0], mm[1]));
   uint32_t w[4];
-#pragma unroll
-  for (int d = 0; d < 4; ++d) w[d] = e4m3_encode4(q[d], s);
+  e4m3_encode(v, s, w);
   const auto x = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
   const auto y = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-  if (store) {
-    *reinterpret_cast<uint4*>(codes + 16 * g) = make_uint4(x[0], x[1], y[0], y[1]);
-    if (g == 0) *scale = (uint8_t)s;
-  }
+  codes = make_uint4(x[0], x[1], y[0], y[1]);
+  return s;
+#else
+  return 0u;
 #endif
 }
 
@@ -977,23 +967,24 @@ __device__ __forceinline__ void gemm_tile(const P& p, int bx, int by, int bz, ui
         const int r = 32 * i + lrow;
         const int64_t m = mw + r;
         const bool in_m = m < p.M;
+        // this row's part of the checkpoint: 64 columns of one K group
+        uint8_t* row_codes = p.saved_codes + code_group(m, nw, p.M, 8) + (nw & 127) + 16 * g;
+        uint32_t scales = 0;
 #pragma unroll
         for (int j = 0; j < CF::kNJ; ++j) {
           const int64_t n = nw + 32 * j;
-          if (n >= p.N) {  // past the columns: the pad blocks of the checkpoint's last K group
-            if (p.saved_codes != nullptr && n < ((p.N + 127) & ~(int64_t)127) && in_m) {
-              *reinterpret_cast<uint4*>(p.saved_codes + code_group(m, n, p.M, 8) + (n & 127) + 16 * g) =
-                  make_uint4(0u, 0u, 0u, 0u);
-              if (g == 0) p.saved_scales[scale_offset(m, n >> 5, p.M)] = 0;
-            }
-            continue;
-          }
+          if (n >= p.N) continue;
           float v[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) v[e] = acc[i][j][e] + bv[j][e];
-          if (p.saved_codes != nullptr)
-            checkpoint_block(v, g, p.saved_codes + code_group(m, n, p.M, 8) + (n & 127),
-                             p.saved_scales + scale_offset(m, n >> 5, p.M), in_m);
+          if (p.saved_codes != nullptr) {
+            float u[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) u[e] = v[e];
+            uint4 codes;
+            scales |= checkpoint_block(u, codes) << (8 * j);
+            if (in_m) *reinterpret_cast<uint4*>(row_codes + 32 * j) = codes;
+          }
           if (p.c == nullptr) continue;
 #pragma unroll
           for (int e = 0; e < 16; ++e) v[e] = act_value<ACT>(v[e]);
@@ -1033,8 +1024,16 @@ __device__ __forceinline__ void gemm_tile(const P& p, int bx, int by, int bz, ui
             }
           }
         }
+        if (p.saved_codes != nullptr && in_m && nw < ((p.N + 127) & ~(int64_t)127)) {
+          // pad blocks (past N, to the end of the last K group): zeros
+#pragma unroll
+          for (int j = 0; j < CF::kNJ; ++j)
+            if (nw + 32 * j >= p.N) *reinterpret_cast<uint4*>(row_codes + 32 * j) = make_uint4(0u, 0u, 0u, 0u);
+          if (g == 0) *reinterpret_cast<uint16_t*>(p.saved_scales + scale_offset(m, nw >> 5, p.M)) = (uint16_t)scales;
+        }
       }
     };
+    static_assert(CF::kWN == 64, "a wavefront's columns are two blocks of one K group");
     if (p.act == kActGelu) finish(std::integral_constant<int, kActGelu>{});
     else if (p.act == kActSilu) finish(std::integral_constant<int, kActSilu>{});
     else finish(std::integral_constant<int, kActNone>{});

@@ -36,23 +36,21 @@ __device__ __forceinline__ Eight<F32> load8(const void* base, int64_t at) {
   return q;
 }
 template <int F32>
-__device__ __forceinline__ void values8(const Eight<F32>& q, float (&lo)[4], float (&hi)[4]) {
+__device__ __forceinline__ void values8(const Eight<F32>& q, float (&v)[8]) {
   if constexpr (F32) {
     const uint32_t a[4] = {q.w[0].x, q.w[0].y, q.w[0].z, q.w[0].w}, b[4] = {q.w[1].x, q.w[1].y, q.w[1].z, q.w[1].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      lo[i] = __uint_as_float(a[i]);
-      hi[i] = __uint_as_float(b[i]);
+      v[i] = __uint_as_float(a[i]);
+      v[4 + i] = __uint_as_float(b[i]);
     }
   } else {
-    lo[0] = bf16_lo(q.w[0].x);
-    lo[1] = bf16_hi(q.w[0].x);
-    lo[2] = bf16_lo(q.w[0].y);
-    lo[3] = bf16_hi(q.w[0].y);
-    hi[0] = bf16_lo(q.w[0].z);
-    hi[1] = bf16_hi(q.w[0].z);
-    hi[2] = bf16_lo(q.w[0].w);
-    hi[3] = bf16_hi(q.w[0].w);
+    const uint32_t a[4] = {q.w[0].x, q.w[0].y, q.w[0].z, q.w[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = bf16_lo(a[i]);
+      v[2 * i + 1] = bf16_hi(a[i]);
+    }
   }
 }
 
@@ -79,17 +77,18 @@ __global__ __launch_bounds__(256) void checkpoint_save_kernel(const void* __rest
 #pragma unroll
   for (int i = 0; i < kCkptSteps; ++i) {
     const int64_t r = r0 + 16 * i;
-    float lo[4], hi[4];
-    values8<F32>(in[i], lo, hi);
+    float v[8];
+    values8<F32>(in[i], v);
     // an all-zero block gets scale byte 0, and so does a pad block
-    const uint32_t s = scale_byte<kE4M3, kRceil>(max_over4(abs_max4(hi, abs_max4(lo))));
-    const uint2 w = make_uint2(e4m3_encode4(lo, s), e4m3_encode4(hi, s));
+    const uint32_t s = scale_byte<kE4M3, kRceil>(max_over4(abs_max(v)));
+    uint32_t w[2];
+    e4m3_encode(v, s, w);
     // the row's scale dword: byte b from the lanes of block b = ch / 4
     uint32_t d = s << (8 * (ch >> 2));
     d |= dpp_move<kDppRor8>(d);
     d |= dpp_move<kDppRor4>(d);
     if (r < R) {
-      *reinterpret_cast<uint2*>(codes + (q * R + r) * 128 + ch * 8) = w;
+      *reinterpret_cast<uint2*>(codes + (q * R + r) * 128 + ch * 8) = make_uint2(w[0], w[1]);
       if (ch == 0) *reinterpret_cast<uint32_t*>(scales + (q * R + r) * 4) = d;
     }
   }
@@ -158,6 +157,16 @@ __device__ __forceinline__ float sum_over_rows4(float v) {
 #endif
 }
 
+// db[c] = the partials of column c in increasing order, from +0.
+__device__ __forceinline__ void finish_column_sums(const SavedPackParams& p, int64_t c) {
+  if (c >= p.sum_cols) return;
+  const float* src = p.sum_partials + c;
+  float s = 0.0f;
+#pragma unroll 16
+  for (int64_t b = 0; b < p.sum_rows; ++b) s = s + src[b * p.sum_cols];
+  p.sum_out[c] = s;
+}
+
 // HASX: v = x act'(saved) (ACT none: v = x, no checkpoint), else v = act(saved).
 template <int FMT, int MODE, int HAD, int ACT, int HASX>
 __global__ __launch_bounds__(256) void quantize_saved_kernel(SavedPackParams p) {
@@ -166,8 +175,13 @@ __global__ __launch_bounds__(256) void quantize_saved_kernel(SavedPackParams p) 
   __shared__ __attribute__((aligned(16))) uint8_t tile[kTileBytes];
   __shared__ float part[4][kTile];
   const int t = threadIdx.x, ch = t & 15, row_t = t >> 4;
+  const int sums = p.sum_out != nullptr ? (int)((p.sum_cols + 255) / 256) : 0;
+  if ((int)blockIdx.x < sums) {  // the first workgroups finish an earlier pack's column sums
+    finish_column_sums(p, (int64_t)blockIdx.x * 256 + t);
+    return;
+  }
   const int tx = (int)((p.C + kTile - 1) / kTile);
-  const int64_t by = blockIdx.x / tx, bx = blockIdx.x - by * tx;
+  const int64_t by = (blockIdx.x - sums) / tx, bx = (blockIdx.x - sums) - by * tx;
   const int64_t r0 = by * kTile, c0 = bx * kTile, c = c0 + ch * 8;
 
   // 1. every load of the tile in flight, then v, its sums, and bf16 in LDS
@@ -331,7 +345,8 @@ hipError_t launch_checkpoint_load(const uint8_t* codes, const uint8_t* scales, i
 
 hipError_t launch_quantize_saved(const SavedPackParams& p, int fmt, int mode, int had, int act, hipStream_t stream) {
   SavedFn fn = pick_saved(fmt, mode, had, act, p.x != nullptr);
-  const int64_t tiles = ((p.C + kTile - 1) / kTile) * ((p.R + kTile - 1) / kTile);
+  const int64_t tiles = ((p.C + kTile - 1) / kTile) * ((p.R + kTile - 1) / kTile) +
+                        (p.sum_out != nullptr ? (p.sum_cols + 255) / 256 : 0);
   if (!fn || tiles >= (1ll << 31)) return hipErrorInvalidValue;
   if (tiles == 0) return hipSuccess;
   hipLaunchKernelGGL(fn, dim3((unsigned)tiles), dim3(256), 0, stream, p);
