@@ -505,18 +505,17 @@ _pack_linear_bwd = _packer(LinearBwdArgs)
 
 
 def _current():
-    """The current device and its current stream's handle."""
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
-    return dev, torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else 0
+    """The current device (-1: none in use yet) and its current stream's handle."""
+    if not torch.cuda.is_initialized():
+        return (torch.cuda.current_device() if torch.cuda.is_available() else -1), 0
+    dev = torch._C._cuda_getDevice()
+    return dev, torch._C._cuda_getCurrentRawStream(dev)
 
 
-def _on_device(t, dev: int, what: str):
-    """Address of a tensor, refused where the kernels could not reach it."""
+def _refuse_device(t, dev: int, what: str):
     at = t.get_device()
-    if at != dev or at < 0:
-        raise MXError(7, f"{what}: tensor is not on a GPU (the kernels take device memory)" if at < 0 else
-                      f"{what}: tensor is on cuda:{at}, the current device is cuda:{dev}")
-    return t.data_ptr()
+    raise MXError(7, f"{what}: tensor is not on a GPU (the kernels take device memory)" if at < 0 else
+                  f"{what}: tensor is on cuda:{at}, the current device is cuda:{dev}")
 
 
 _DTYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.int16: BF16, torch.uint16: BF16}
@@ -528,7 +527,7 @@ def _matrix(t, R: int, C: int, dev: int, what: str, dtypes=(BF16, F32)):
     a contiguous one of R * C elements.  float32 is MX_F32; bfloat16 and the
     16-bit integers that carry bf16 patterns are MX_BF16."""
     if t is None:
-        return 0, max(C, 0), dtypes[0]
+        return 0, C, dtypes[0]
     dtype = _DTYPES.get(t.dtype, -1)
     if dtype not in dtypes:
         raise MXError(4, f"{what}: {t.dtype} is not served here" if dtype >= 0 else
@@ -541,7 +540,9 @@ def _matrix(t, R: int, C: int, dev: int, what: str, dtypes=(BF16, F32)):
             ld = t.stride(0)
     elif t.numel() != R * C:
         raise MXError(2, f"{what}: {tuple(t.shape)} does not hold [{R}][{C}]")
-    return _on_device(t, dev, what), ld, dtype
+    if t.get_device() != dev or dev < 0:
+        _refuse_device(t, dev, what)
+    return t.data_ptr(), ld, dtype
 
 
 def _operand(p, rows: int, K: int, fmt: int, dev: int, what: str):
@@ -549,13 +550,16 @@ def _operand(p, rows: int, K: int, fmt: int, dev: int, what: str):
     if p is None:
         return 0, 0
     codes, scales = p
+    n = (K + 127) // 128 * rows * 4
+    need = n * 4 * BITS.get(fmt, 0)
     if not (codes.is_contiguous() and scales.is_contiguous()):
         raise MXError(2, f"{what}: tensor argument is a strided view; pass a contiguous tensor")
-    n = (K + 127) // 128 * rows * 4
-    if codes.nbytes < n * BITS.get(fmt, 0) * 4 or scales.nbytes < n:
+    if codes.nbytes < need or scales.nbytes < n:
         raise MXError(2, f"{what}: codes and scales hold {codes.nbytes} and {scales.nbytes} bytes, "
-                         f"the call touches {n * BITS.get(fmt, 0) * 4} and {n}")
-    return _on_device(codes, dev, what), _on_device(scales, dev, what)
+                         f"the call touches {need} and {n}")
+    if codes.get_device() != dev or scales.get_device() != dev or dev < 0:
+        _refuse_device(codes if codes.get_device() != dev else scales, dev, what)
+    return codes.data_ptr(), scales.data_ptr()
 
 
 def _handle(stream, current: int):
