@@ -134,14 +134,14 @@ __global__ __launch_bounds__(256) void checkpoint_load_kernel(const uint8_t* __r
 }
 
 // ------------------------------------------------------------------ packs from a checkpoint
-// One 256-thread workgroup turns a 128 x 128 tile of v into rows' and columns'
+// One 512-thread workgroup turns a 128 x 128 tile of v into rows' and columns'
 // blocks: inputs -> v in registers (its column sums are taken there, in
 // binary32) -> bf16 in LDS -> one quantization pass per axis.  Tile geometry
 // as in the bf16 packer: row pitch 272 bytes, every 32-row block shifted by a
 // further 32 so that a column pass's four blocks fall in different banks.
 constexpr int kTile = 128, kPitch = kTile * 2 + 16, kBlockSkew = 32;
 constexpr int kTileBytes = kTile * kPitch + 3 * kBlockSkew;
-constexpr int kSteps = 8;  // 16-row steps of a tile
+constexpr int kSteps = 4;  // 32-row steps of a tile
 __device__ __forceinline__ int lds_row_at(int row) { return row * kPitch + (row >> 5) * kBlockSkew; }
 
 // Sum over the four lanes l, l ^ 16, l ^ 32, l ^ 48 (a fixed order).
@@ -169,15 +169,15 @@ __device__ __forceinline__ void finish_column_sums(const SavedPackParams& p, int
 
 // HASX: v = x act'(saved) (ACT none: v = x, no checkpoint), else v = act(saved).
 template <int FMT, int MODE, int HAD, int ACT, int HASX>
-__global__ __launch_bounds__(256) void quantize_saved_kernel(SavedPackParams p) {
+__global__ __launch_bounds__(512) void quantize_saved_kernel(SavedPackParams p) {
   constexpr int B = FmtTraits<FMT>::kBits;
   constexpr bool kSaved = !HASX || ACT != kActNone;
   __shared__ __attribute__((aligned(16))) uint8_t tile[kTileBytes];
-  __shared__ float part[4][kTile];
+  __shared__ float part[8][kTile];
   const int t = threadIdx.x, ch = t & 15, row_t = t >> 4;
-  const int sums = p.sum_out != nullptr ? (int)((p.sum_cols + 255) / 256) : 0;
+  const int sums = p.sum_out != nullptr ? (int)((p.sum_cols + 511) / 512) : 0;
   if ((int)blockIdx.x < sums) {  // the first workgroups finish an earlier pack's column sums
-    finish_column_sums(p, (int64_t)blockIdx.x * 256 + t);
+    finish_column_sums(p, (int64_t)blockIdx.x * 512 + t);
     return;
   }
   const int tx = (int)((p.C + kTile - 1) / kTile);
@@ -190,7 +190,7 @@ __global__ __launch_bounds__(256) void quantize_saved_kernel(SavedPackParams p) 
   uint32_t s[kSteps];
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
-    const int64_t r = r0 + row_t + 16 * i;
+    const int64_t r = r0 + row_t + 32 * i;
     x[i] = make_uint4(0u, 0u, 0u, 0u);
     w[i] = make_uint2(0u, 0u);
     s[i] = 0u;
@@ -230,7 +230,7 @@ __global__ __launch_bounds__(256) void quantize_saved_kernel(SavedPackParams p) 
     // (rows and columns past the end hold zeros: act(0) = 0, 0 act'(0) = 0)
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum[e] = sum[e] + v[e];
-    *reinterpret_cast<uint4*>(tile + row_t * kPitch + ch * 16 + i * 16 * kPitch + (i >> 1) * kBlockSkew) =
+    *reinterpret_cast<uint4*>(tile + row_t * kPitch + ch * 16 + i * (32 * kPitch + kBlockSkew)) =
         make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                    pack_bf16x2(v[6], v[7]));
   }
@@ -243,26 +243,27 @@ __global__ __launch_bounds__(256) void quantize_saved_kernel(SavedPackParams p) 
     }
   }
   __syncthreads();
-  if (p.partials != nullptr && t < kTile && c0 + t < p.C)
-    p.partials[by * p.C + c0 + t] = ((part[0][t] + part[1][t]) + part[2][t]) + part[3][t];
+  if (p.partials != nullptr && t < kTile && c0 + t < p.C) {
+    float total = part[0][t];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) total = total + part[w][t];
+    p.partials[by * p.C + c0 + t] = total;
+  }
 
   // 2. rowwise blocks: the four of a row come from four adjacent lanes
   if (p.row_codes != nullptr) {
     uint8_t* const codes = p.row_codes + (bx * p.R + r0) * (16 * B);
     uint8_t* const scales = p.row_scales + (bx * p.R + r0) * 4;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int q = t + 256 * h, row = q >> 2, blk = q & 3;
-      const int64_t r = r0 + row;
-      if (r < p.R) {
-        if (c0 + blk * 32 < p.C) {
-          float v[32];
-          lds_row_block(tile + lds_row_at(row), 0, 0, blk * 32, v);
-          quant_store<FMT, MODE, HAD>(v, codes + row * (16 * B), blk, r, scales + (row * 4 + blk));
-        } else {
-          scales[row * 4 + blk] = 0;
-          zero_block<FMT>(codes + row * (16 * B), blk, r);
-        }
+    const int row = t >> 2, blk = t & 3;
+    const int64_t r = r0 + row;
+    if (r < p.R) {
+      if (c0 + blk * 32 < p.C) {
+        float v[32];
+        lds_row_block(tile + lds_row_at(row), 0, 0, blk * 32, v);
+        quant_store<FMT, MODE, HAD>(v, codes + row * (16 * B), blk, r, scales + (row * 4 + blk));
+      } else {
+        scales[row * 4 + blk] = 0;
+        zero_block<FMT>(codes + row * (16 * B), blk, r);
       }
     }
   }
@@ -272,20 +273,17 @@ __global__ __launch_bounds__(256) void quantize_saved_kernel(SavedPackParams p) 
   if (p.col_codes != nullptr) {
     uint8_t* const codes = p.col_codes + (by * p.C + c0) * (16 * B);
     uint8_t* const scales = p.col_scales + (by * p.C + c0) * 4;
+    const int col = t >> 2, blk = t & 3;
+    if (c0 + col < p.C) {
+      if (r0 + blk * 32 < p.R) {
+        float v[32];
+        const uint16_t* src = reinterpret_cast<const uint16_t*>(tile + lds_row_at(32 * blk)) + col;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int q = t + 256 * h, col = q >> 2, blk = q & 3;
-      if (c0 + col < p.C) {
-        if (r0 + blk * 32 < p.R) {
-          float v[32];
-          const uint16_t* src = reinterpret_cast<const uint16_t*>(tile + lds_row_at(32 * blk)) + col;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = bf16_to_f32(src[i * (kPitch / 2)]);
-          quant_store<FMT, MODE, HAD>(v, codes + col * (16 * B), blk, c0 + col, scales + (col * 4 + blk));
-        } else {
-          scales[col * 4 + blk] = 0;
-          zero_block<FMT>(codes + col * (16 * B), blk, c0 + col);
-        }
+        for (int i = 0; i < 32; ++i) v[i] = bf16_to_f32(src[i * (kPitch / 2)]);
+        quant_store<FMT, MODE, HAD>(v, codes + col * (16 * B), blk, c0 + col, scales + (col * 4 + blk));
+      } else {
+        scales[col * 4 + blk] = 0;
+        zero_block<FMT>(codes + col * (16 * B), blk, c0 + col);
       }
     }
   }
@@ -346,10 +344,10 @@ hipError_t launch_checkpoint_load(const uint8_t* codes, const uint8_t* scales, i
 hipError_t launch_quantize_saved(const SavedPackParams& p, int fmt, int mode, int had, int act, hipStream_t stream) {
   SavedFn fn = pick_saved(fmt, mode, had, act, p.x != nullptr);
   const int64_t tiles = ((p.C + kTile - 1) / kTile) * ((p.R + kTile - 1) / kTile) +
-                        (p.sum_out != nullptr ? (p.sum_cols + 255) / 256 : 0);
+                        (p.sum_out != nullptr ? (p.sum_cols + 511) / 512 : 0);
   if (!fn || tiles >= (1ll << 31)) return hipErrorInvalidValue;
   if (tiles == 0) return hipSuccess;
-  hipLaunchKernelGGL(fn, dim3((unsigned)tiles), dim3(256), 0, stream, p);
+  hipLaunchKernelGGL(fn, dim3((unsigned)tiles), dim3(512), 0, stream, p);
   return hipGetLastError();
 }
 
