@@ -52,15 +52,22 @@ template <int ACT>
 __device__ __forceinline__ float act_slope(float x) {
   if constexpr (ACT == kActNone) return 1.0f;
   const float s = sigmoid2(act_exponent<ACT>(x));
-  const float w = __builtin_fmaf(-s, s, s);  // s (1 - s): 0 once |z| passes 25, the term it scales then below s's rounding
-  // the term's other factor, kept finite so that w = 0 ends it
-  const float y = __builtin_fminf(__builtin_fmaxf(x, -0x1p40f), 0x1p40f);
+  // s (1 - s): exactly 0 once |z| passes 25, where the term it scales is
+  // below the rounding of s; its other factor may have overflowed by then,
+  // so the product is the one whose zeros win
+  const float w = __builtin_fmaf(-s, s, s);
+  float xz = x;
   if constexpr (ACT == kActGelu) {
     const float C = 0x1.988454p+0f, D = 0x1.b6676cp-3f;  // z' = C + D x^2
-    return __builtin_fmaf(y * __builtin_fmaf(y * y, D, C), w, s);
-  } else {
-    return __builtin_fmaf(y, w, s);
+    xz = x * __builtin_fmaf(x * x, D, C);
   }
+#if defined(__HIP_DEVICE_COMPILE__)
+  float term;  // xz w, 0 wherever w is 0
+  asm("v_mul_legacy_f32 %0, %1, %2" : "=v"(term) : "v"(xz), "v"(w));
+  return term + s;
+#else
+  return xz * w + s;
+#endif
 }
 
 // 2^(byte - 127) of an E8M0 scale; 0 gives 2^-127 (a subnormal), 0xff gives

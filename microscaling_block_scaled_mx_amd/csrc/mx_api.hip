@@ -308,38 +308,33 @@ int validate_quantize_saved(const mx_quantize_saved_args& a) {
   return MX_OK;
 }
 
-// `before`: a pack earlier on the stream whose column sums this launch
-// finishes beside its own work (nullptr: none).  `finish`: whether this
-// pack's own are finished by a launch after it.
-int quantize_saved_launch(const mx_quantize_saved_args& a, hipStream_t s, const mx_quantize_saved_args* before = nullptr,
-                          bool finish = true) {
-  if (a.C == 0) return MX_OK;
-  int st = MX_OK;
-  if (a.R > 0) {
-    mx::SavedPackParams p;
-    memset(&p, 0, sizeof p);
-    if (before) {
-      p.sum_partials = before->colsum_partials;
-      p.sum_rows = (before->R + 127) / 128;
-      p.sum_cols = before->C;
-      p.sum_out = before->colsum;
-    }
-    p.x = static_cast<const uint16_t*>(a.x);
-    p.ldx = a.ldx;
-    p.saved_codes = bytes(a.saved.codes);
-    p.saved_scales = bytes(a.saved.scales);
-    p.R = a.R;
-    p.C = a.C;
-    p.row_codes = bytes(a.row.codes);
-    p.row_scales = bytes(a.row.scales);
-    p.col_codes = bytes(a.col.codes);
-    p.col_scales = bytes(a.col.scales);
-    p.partials = a.colsum_partials;
-    st = launched(mx::launch_quantize_saved(p, a.fmt, a.scale_mode, a.hadamard, a.act, s));
-  }
-  if (st == MX_OK && a.colsum && finish)  // no rows: no partials, zeros
-    st = launched(mx::launch_colsum_finish(a.colsum_partials, (a.R + 127) / 128, a.C, a.colsum, 1, s));
-  return st;
+mx::SavedPackParams saved_pack_params(const mx_quantize_saved_args& a) {
+  mx::SavedPackParams p;
+  p.x = static_cast<const uint16_t*>(a.x);
+  p.ldx = a.ldx;
+  p.saved_codes = bytes(a.saved.codes);
+  p.saved_scales = bytes(a.saved.scales);
+  p.R = a.R;
+  p.C = a.C;
+  p.row_codes = bytes(a.row.codes);
+  p.row_scales = bytes(a.row.scales);
+  p.col_codes = bytes(a.col.codes);
+  p.col_scales = bytes(a.col.scales);
+  p.partials = a.colsum_partials;
+  p.act = a.act;
+  return p;
+}
+
+// The pack, and in the same launch that of `b` (nullptr: none).
+int quantize_saved_launch(const mx_quantize_saved_args& a, const mx_quantize_saved_args* b, hipStream_t s) {
+  const mx::SavedPackParams p = saved_pack_params(a), q = saved_pack_params(b ? *b : a);
+  return launched(mx::launch_quantize_saved(p, b ? &q : nullptr, a.fmt, a.scale_mode, a.hadamard, s));
+}
+
+// The column sums of a pack from its partials (no rows: zeros).
+int finish_sums_launch(const mx_quantize_saved_args& a, hipStream_t s) {
+  if (!a.colsum || a.C == 0) return MX_OK;
+  return launched(mx::launch_colsum_finish(a.colsum_partials, (a.R + 127) / 128, a.C, a.colsum, 1, s));
 }
 
 }  // namespace
@@ -841,7 +836,9 @@ int mx_quantize_saved(const mx_quantize_saved_args* args, void* stream) {
   int st = validate_quantize_saved(*args);
   if (st != MX_OK) return st;
   if ((st = check_device()) != MX_OK) return st;
-  return quantize_saved_launch(*args, static_cast<hipStream_t>(stream));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if ((st = quantize_saved_launch(*args, nullptr, s)) != MX_OK) return st;
+  return finish_sums_launch(*args, s);
 }
 
 int mx_linear_bwd_saved(const mx_linear_bwd_args* args, void* stream) {
@@ -916,12 +913,13 @@ int mx_linear_bwd_saved(const mx_linear_bwd_args* args, void* stream) {
   if (want_dw && (st = validate_gemm_act(w)) != MX_OK) return st;
   if ((st = check_device()) != MX_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  // db's partials are finished beside the pack of X, where there is one
-  const bool beside = want_dw && a.db && a.M > 0;
-  if (want_g && (st = quantize_saved_launch(g, s, nullptr, !beside)) != MX_OK) return st;
-  if (want_dw && (st = quantize_saved_launch(x, s, beside ? &g : nullptr)) != MX_OK) return st;
-  if (want_dx && want_dw)
-    return launched(mx::launch_gemm_act_pair(gemm_act_params(d), gemm_act_params(w), a.fmt, s));
+  // two launches: the packs, then the products and the column sums
+  if (want_g && (st = quantize_saved_launch(g, want_dw ? &x : nullptr, s)) != MX_OK) return st;
+  if (want_dx && want_dw) {
+    const mx::ColumnSums sums = {a.db_partials, (a.M + 127) / 128, a.N, a.db};
+    return launched(mx::launch_gemm_act_pair(gemm_act_params(d), gemm_act_params(w), sums, a.fmt, s));
+  }
+  if ((st = finish_sums_launch(g, s)) != MX_OK) return st;
   if (want_dx) return gemm_act_launch(d, s);
   return want_dw ? gemm_act_launch(w, s) : MX_OK;
 }

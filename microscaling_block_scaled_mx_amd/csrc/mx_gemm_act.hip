@@ -31,6 +31,8 @@ template <int COUNT>
 struct Products {
   GemmActParams p[COUNT];
   int first;  // tiles of p[0]
+  int summing;      // COUNT = 2: workgroups before them that finish column sums
+  ColumnSums sums;
 };
 template <int COUNT>
 __device__ __forceinline__ const GemmActParams& product_of(const Products<COUNT>& all, int& tile) {
@@ -39,11 +41,25 @@ __device__ __forceinline__ const GemmActParams& product_of(const Products<COUNT>
   tile -= all.first;
   return all.p[1];
 }
+// Whether this workgroup's work was column sums; if not, its tile.
+template <int COUNT>
+__device__ __forceinline__ bool summed(const Products<COUNT>& all, int& tile) {
+  tile = blockIdx.x;
+  if constexpr (COUNT == 2) {
+    if (tile < all.summing) {
+      finish_column_sum(all.sums, (int64_t)tile * blockDim.x + threadIdx.x);
+      return true;
+    }
+    tile -= all.summing;
+  }
+  return false;
+}
 
 template <int FMT, int BM, int BN, int OCC, int COUNT>
 __global__ __launch_bounds__(tile_threads(BM, BN, kEpiAct), OCC) void gemm_act_kernel(Products<COUNT> all) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[Cfg<FMT, BM, BN, kDense, kEpiAct, OCC>::kSmem];
-  int tile = blockIdx.x;
+  int tile;
+  if (summed(all, tile)) return;
   const GemmActParams& p = product_of(all, tile);
   gemm_tile<FMT, BM, BN, kDense, kEpiAct, OCC>(p, tile, 0, 0, smem);
 }
@@ -126,7 +142,8 @@ __device__ __forceinline__ void memory_fence() {
 template <int FMT, int MI, int NJ, int W, int D, int COUNT>
 __global__ __launch_bounds__(64 * W) void gemm_rows_kernel(Products<COUNT> all) {
   using CF = RowsCfg<FMT, MI, NJ, W, D>;
-  int tile = blockIdx.x;
+  int tile;
+  if (summed(all, tile)) return;
   const GemmActParams& p = product_of(all, tile);
   __shared__ __attribute__((aligned(16))) uint8_t smem[CF::kSmem];
   const int t = threadIdx.x, lane = t & 63, wave = wave_uniform(t >> 6);
@@ -310,32 +327,40 @@ __global__ __launch_bounds__(64 * W) void gemm_rows_kernel(Products<COUNT> all) 
 // ------------------------------------------------------------------ launch
 int64_t tile_count(const GemmActParams& p, int bm, int bn) { return ((p.M + bm - 1) / bm) * ((p.N + bn - 1) / bn); }
 
-// q: a second product for the same launch, or nullptr.
-template <int FMT, int BM, int BN, int OCC>
-hipError_t launch_tiles(const GemmActParams& p, const GemmActParams* q, hipStream_t stream) {
-  constexpr int kThreads = Cfg<FMT, BM, BN, kDense, kEpiAct, OCC>::kThreads;
-  const int64_t first = tile_count(p, BM, BN), all = first + (q ? tile_count(*q, BM, BN) : 0);
+// A second product and column sums for the same launch.
+struct Second {
+  const GemmActParams& q;
+  const ColumnSums& sums;
+};
+
+// One launch of `one`, or of `two` with a second product.
+template <class F1, class F2>
+hipError_t launch_products(F1 one, F2 two, int threads, int bm, int bn, const GemmActParams& p, const Second* more,
+                           hipStream_t stream) {
+  const int64_t first = tile_count(p, bm, bn);
+  if (!more) {
+    if (first >= (1ll << 31)) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(one, dim3((unsigned)first), dim3(threads), 0, stream, (Products<1>{{p}, (int)first, 0, {}}));
+    return hipGetLastError();
+  }
+  const int64_t summing = more->sums.out ? (more->sums.cols + threads - 1) / threads : 0;
+  const int64_t all = summing + first + tile_count(more->q, bm, bn);
   if (all >= (1ll << 31)) return hipErrorInvalidValue;
-  if (q)
-    hipLaunchKernelGGL((gemm_act_kernel<FMT, BM, BN, OCC, 2>), dim3((unsigned)all), dim3(kThreads), 0, stream,
-                       (Products<2>{{p, *q}, (int)first}));
-  else
-    hipLaunchKernelGGL((gemm_act_kernel<FMT, BM, BN, OCC, 1>), dim3((unsigned)all), dim3(kThreads), 0, stream,
-                       (Products<1>{{p}, (int)first}));
+  hipLaunchKernelGGL(two, dim3((unsigned)all), dim3(threads), 0, stream,
+                     (Products<2>{{p, more->q}, (int)first, (int)summing, more->sums}));
   return hipGetLastError();
 }
 
+template <int FMT, int BM, int BN, int OCC>
+hipError_t launch_tiles(const GemmActParams& p, const Second* more, hipStream_t stream) {
+  return launch_products(gemm_act_kernel<FMT, BM, BN, OCC, 1>, gemm_act_kernel<FMT, BM, BN, OCC, 2>,
+                         Cfg<FMT, BM, BN, kDense, kEpiAct, OCC>::kThreads, BM, BN, p, more, stream);
+}
+
 template <int FMT, int MI, int NJ, int W, int D>
-hipError_t launch_rows(const GemmActParams& p, const GemmActParams* q, hipStream_t stream) {
-  const int64_t first = tile_count(p, 16 * MI, 16 * NJ), all = first + (q ? tile_count(*q, 16 * MI, 16 * NJ) : 0);
-  if (all >= (1ll << 31)) return hipErrorInvalidValue;
-  if (q)
-    hipLaunchKernelGGL((gemm_rows_kernel<FMT, MI, NJ, W, D, 2>), dim3((unsigned)all), dim3(64 * W), 0, stream,
-                       (Products<2>{{p, *q}, (int)first}));
-  else
-    hipLaunchKernelGGL((gemm_rows_kernel<FMT, MI, NJ, W, D, 1>), dim3((unsigned)all), dim3(64 * W), 0, stream,
-                       (Products<1>{{p}, (int)first}));
-  return hipGetLastError();
+hipError_t launch_rows(const GemmActParams& p, const Second* more, hipStream_t stream) {
+  return launch_products(gemm_rows_kernel<FMT, MI, NJ, W, D, 1>, gemm_rows_kernel<FMT, MI, NJ, W, D, 2>, 64 * W,
+                         16 * MI, 16 * NJ, p, more, stream);
 }
 
 // The kernel variants: rows_<tile>, the few-rows kernel, and tile_<size>.
@@ -384,28 +409,28 @@ int pick_shape(int fmt, const GemmActParams& p) {
 }
 
 template <int FMT>
-hipError_t launch_shape(const GemmActParams& p, const GemmActParams* q, int shape, hipStream_t stream) {
+hipError_t launch_shape(const GemmActParams& p, const Second* more, int shape, hipStream_t stream) {
   switch (shape) {
-    case kRows16x32: return launch_rows<FMT, 1, 2, 4, 3>(p, q, stream);
-    case kRows16x32Deep: return launch_rows<FMT, 1, 2, 8, 2>(p, q, stream);
-    case kRows32x32: return launch_rows<FMT, 2, 2, 4, 2>(p, q, stream);
-    case kRows32x32Deep: return launch_rows<FMT, 2, 2, 8, 2>(p, q, stream);
-    case kRows64x32: return launch_rows<FMT, 4, 2, 4, 2>(p, q, stream);
-    case kRows64x64: return launch_rows<FMT, 4, 4, 4, 2>(p, q, stream);
-    case kTile128: return launch_tiles<FMT, 128, 128, 2>(p, q, stream);
+    case kRows16x32: return launch_rows<FMT, 1, 2, 4, 3>(p, more, stream);
+    case kRows16x32Deep: return launch_rows<FMT, 1, 2, 8, 2>(p, more, stream);
+    case kRows32x32: return launch_rows<FMT, 2, 2, 4, 2>(p, more, stream);
+    case kRows32x32Deep: return launch_rows<FMT, 2, 2, 8, 2>(p, more, stream);
+    case kRows64x32: return launch_rows<FMT, 4, 2, 4, 2>(p, more, stream);
+    case kRows64x64: return launch_rows<FMT, 4, 4, 4, 2>(p, more, stream);
+    case kTile128: return launch_tiles<FMT, 128, 128, 2>(p, more, stream);
     case kTile256x128:
-      if constexpr (FMT != kE4M3) return launch_tiles<FMT, 256, 128, 2>(p, q, stream);
+      if constexpr (FMT != kE4M3) return launch_tiles<FMT, 256, 128, 2>(p, more, stream);
       else return hipErrorInvalidValue;
-    case kTile256: return launch_tiles<FMT, 256, 256, 1>(p, q, stream);
+    case kTile256: return launch_tiles<FMT, 256, 256, 1>(p, more, stream);
     default: return hipErrorInvalidValue;
   }
 }
 
-hipError_t launch_fmt(int fmt, const GemmActParams& p, const GemmActParams* q, int shape, hipStream_t stream) {
+hipError_t launch_fmt(int fmt, const GemmActParams& p, const Second* more, int shape, hipStream_t stream) {
   switch (fmt) {
-    case kE2M1: return launch_shape<kE2M1>(p, q, shape, stream);
-    case kE2M3: return launch_shape<kE2M3>(p, q, shape, stream);
-    case kE4M3: return launch_shape<kE4M3>(p, q, shape, stream);
+    case kE2M1: return launch_shape<kE2M1>(p, more, shape, stream);
+    case kE2M3: return launch_shape<kE2M3>(p, more, shape, stream);
+    case kE4M3: return launch_shape<kE4M3>(p, more, shape, stream);
     default: return hipErrorInvalidValue;
   }
 }
@@ -418,11 +443,19 @@ hipError_t launch_gemm_act(const GemmActParams& p, int fmt, hipStream_t stream) 
 }
 
 // The results do not depend on whether a launch is shared: each product keeps
-// the variant it has alone.
-hipError_t launch_gemm_act_pair(const GemmActParams& p, const GemmActParams& q, int fmt, hipStream_t stream) {
+// the variant it has alone.  The one with the longer sums goes first, so that
+// the shorter tiles even out the end (4095 x 2016 x 2080 with 2080 x 2016 x
+// 4096 in E2M1: SHARED us, the other way round 32).
+hipError_t launch_gemm_act_pair(const GemmActParams& p, const GemmActParams& q, const ColumnSums& sums, int fmt,
+                                hipStream_t stream) {
+  if (q.K > p.K) return launch_gemm_act_pair(q, p, sums, fmt, stream);
   const bool both = p.M > 0 && p.N > 0 && q.M > 0 && q.N > 0;
-  if (both && pick_shape(fmt, p) == pick_shape(fmt, q)) return launch_fmt(fmt, p, &q, pick_shape(fmt, p), stream);
-  const hipError_t e = launch_gemm_act(p, fmt, stream);
+  const Second more = {q, sums};
+  if (both && pick_shape(fmt, p) == pick_shape(fmt, q)) return launch_fmt(fmt, p, &more, pick_shape(fmt, p), stream);
+  hipError_t e = hipSuccess;
+  if (sums.out && sums.cols > 0)
+    e = launch_colsum_finish(sums.partials, sums.rows, sums.cols, sums.out, 1, stream);
+  if (e == hipSuccess) e = launch_gemm_act(p, fmt, stream);
   return e == hipSuccess ? launch_gemm_act(q, fmt, stream) : e;
 }
 

@@ -24,9 +24,28 @@ struct GemmActParams : GemmParams {
   uint8_t* saved_scales;
 };
 hipError_t launch_gemm_act(const GemmActParams& p, int fmt, hipStream_t stream);
-// Two independent products of one format, with the results of two launches
-// (one launch where both take the same kernel variant).
-hipError_t launch_gemm_act_pair(const GemmActParams& p, const GemmActParams& q, int fmt, hipStream_t stream);
+
+// Column sums to finish: out[c] = partials [rows][cols] of column c in
+// increasing order, from +0 (out nullptr: none).
+struct ColumnSums {
+  const float* partials;
+  int64_t rows, cols;
+  float* out;
+};
+__device__ __forceinline__ void finish_column_sum(const ColumnSums& s, int64_t c) {
+  if (c >= s.cols) return;
+  const float* src = s.partials + c;
+  float sum = 0.0f;
+#pragma unroll 16
+  for (int64_t b = 0; b < s.rows; ++b) sum = sum + src[b * s.cols];
+  s.out[c] = sum;
+}
+
+// Two independent products of one format and column sums to finish, with the
+// results of separate launches (one launch where both products take the same
+// kernel variant).
+hipError_t launch_gemm_act_pair(const GemmActParams& p, const GemmActParams& q, const ColumnSums& sums, int fmt,
+                                hipStream_t stream);
 
 // x [R][ldx] (bf16 or binary32) -> E4M3 operand [R] x K=C, RCEIL scales.
 hipError_t launch_checkpoint_save(const void* x, int x_f32, int64_t R, int64_t C, int64_t ldx, uint8_t* codes,
@@ -48,12 +67,11 @@ struct SavedPackParams {
   uint8_t* col_codes;           // [C] x K=R (rounded up to 32), or nullptr
   uint8_t* col_scales;
   float* partials;              // [ceil(R/128)][C] or nullptr
-  // a column sum to finish beside the pack, of partials written earlier on
-  // the stream: sum_out[c] = the sum of sum_rows partials [sum_rows][sum_cols]
-  const float* sum_partials;
-  int64_t sum_rows, sum_cols;
-  float* sum_out;               // nullptr: none
+  int act;                      // Act
 };
-hipError_t launch_quantize_saved(const SavedPackParams& p, int fmt, int mode, int had, int act, hipStream_t stream);
+// One pack, or two in a launch (q may be nullptr), of one format, scale mode
+// and rotation.
+hipError_t launch_quantize_saved(const SavedPackParams& p, const SavedPackParams* q, int fmt, int mode, int had,
+                                 hipStream_t stream);
 
 }  // namespace mx

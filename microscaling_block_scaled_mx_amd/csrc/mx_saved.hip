@@ -157,34 +157,15 @@ __device__ __forceinline__ float sum_over_rows4(float v) {
 #endif
 }
 
-// db[c] = the partials of column c in increasing order, from +0.
-__device__ __forceinline__ void finish_column_sums(const SavedPackParams& p, int64_t c) {
-  if (c >= p.sum_cols) return;
-  const float* src = p.sum_partials + c;
-  float s = 0.0f;
-#pragma unroll 16
-  for (int64_t b = 0; b < p.sum_rows; ++b) s = s + src[b * p.sum_cols];
-  p.sum_out[c] = s;
-}
-
-// HASX: v = x act'(saved) (ACT none: v = x, no checkpoint), else v = act(saved).
-template <int FMT, int MODE, int HAD, int ACT, int HASX>
-__global__ __launch_bounds__(512) void quantize_saved_kernel(SavedPackParams p) {
-  constexpr int B = FmtTraits<FMT>::kBits;
+// Step 1 of a tile: every load in flight, then v, its column sums, and bf16 in
+// LDS.  HASX: v = x act'(saved) (ACT none: v = x, no checkpoint), else
+// v = act(saved).
+template <int ACT, int HASX>
+__device__ __forceinline__ void form_tile(const SavedPackParams& p, int64_t bx, int64_t by, uint8_t* tile,
+                                          float (&part)[8][kTile]) {
   constexpr bool kSaved = !HASX || ACT != kActNone;
-  __shared__ __attribute__((aligned(16))) uint8_t tile[kTileBytes];
-  __shared__ float part[8][kTile];
   const int t = threadIdx.x, ch = t & 15, row_t = t >> 4;
-  const int sums = p.sum_out != nullptr ? (int)((p.sum_cols + 511) / 512) : 0;
-  if ((int)blockIdx.x < sums) {  // the first workgroups finish an earlier pack's column sums
-    finish_column_sums(p, (int64_t)blockIdx.x * 512 + t);
-    return;
-  }
-  const int tx = (int)((p.C + kTile - 1) / kTile);
-  const int64_t by = (blockIdx.x - sums) / tx, bx = (blockIdx.x - sums) - by * tx;
-  const int64_t r0 = by * kTile, c0 = bx * kTile, c = c0 + ch * 8;
-
-  // 1. every load of the tile in flight, then v, its sums, and bf16 in LDS
+  const int64_t r0 = by * kTile, c = bx * kTile + ch * 8;
   uint4 x[kSteps];
   uint2 w[kSteps];
   uint32_t s[kSteps];
@@ -228,8 +209,10 @@ __global__ __launch_bounds__(512) void quantize_saved_kernel(SavedPackParams p) 
       }
     }
     // (rows and columns past the end hold zeros: act(0) = 0, 0 act'(0) = 0)
+    if (p.partials != nullptr) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum[e] = sum[e] + v[e];
+      for (int e = 0; e < 8; ++e) sum[e] = sum[e] + v[e];
+    }
     *reinterpret_cast<uint4*>(tile + row_t * kPitch + ch * 16 + i * (32 * kPitch + kBlockSkew)) =
         make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                    pack_bf16x2(v[6], v[7]));
@@ -241,6 +224,37 @@ __global__ __launch_bounds__(512) void quantize_saved_kernel(SavedPackParams p) 
 #pragma unroll
       for (int e = 0; e < 8; ++e) part[t >> 6][ch * 8 + e] = sum[e];
     }
+  }
+}
+
+// The packs of a launch, one or two: workgroups from `first` on take tiles of
+// the second.
+template <int COUNT>
+struct SavedPacks {
+  SavedPackParams p[COUNT];
+  int first;  // tiles of p[0]
+};
+
+template <int FMT, int MODE, int HAD, int COUNT>
+__global__ __launch_bounds__(512) void quantize_saved_kernel(SavedPacks<COUNT> all) {
+  constexpr int B = FmtTraits<FMT>::kBits;
+  __shared__ __attribute__((aligned(16))) uint8_t tile[kTileBytes];
+  __shared__ float part[8][kTile];
+  const int second = COUNT == 2 && (int)blockIdx.x >= all.first ? 1 : 0;
+  const SavedPackParams& p = all.p[COUNT == 2 ? second : 0];
+  const int local = blockIdx.x - (second ? all.first : 0);
+  const int t = threadIdx.x;
+  const int tx = (int)((p.C + kTile - 1) / kTile);
+  const int64_t by = local / tx, bx = local - by * tx;
+  const int64_t r0 = by * kTile, c0 = bx * kTile;
+  if (p.x != nullptr) {  // (uniform)
+    if (p.act == kActGelu) form_tile<kActGelu, 1>(p, bx, by, tile, part);
+    else if (p.act == kActSilu) form_tile<kActSilu, 1>(p, bx, by, tile, part);
+    else form_tile<kActNone, 1>(p, bx, by, tile, part);
+  } else {
+    if (p.act == kActGelu) form_tile<kActGelu, 0>(p, bx, by, tile, part);
+    else if (p.act == kActSilu) form_tile<kActSilu, 0>(p, bx, by, tile, part);
+    else form_tile<kActNone, 0>(p, bx, by, tile, part);
   }
   __syncthreads();
   if (p.partials != nullptr && t < kTile && c0 + t < p.C) {
@@ -289,25 +303,20 @@ __global__ __launch_bounds__(512) void quantize_saved_kernel(SavedPackParams p) 
   }
 }
 
-using SavedFn = void (*)(SavedPackParams);
-
 template <int FMT, int MODE, int HAD>
-SavedFn pick_act(int act, bool has_x) {
-  switch (act) {
-    case kActNone: return has_x ? quantize_saved_kernel<FMT, MODE, HAD, kActNone, 1> : quantize_saved_kernel<FMT, MODE, HAD, kActNone, 0>;
-    case kActGelu: return has_x ? quantize_saved_kernel<FMT, MODE, HAD, kActGelu, 1> : quantize_saved_kernel<FMT, MODE, HAD, kActGelu, 0>;
-    case kActSilu: return has_x ? quantize_saved_kernel<FMT, MODE, HAD, kActSilu, 1> : quantize_saved_kernel<FMT, MODE, HAD, kActSilu, 0>;
-    default: return nullptr;
-  }
+hipError_t launch_packs(const SavedPackParams& p, const SavedPackParams* q, int64_t first, int64_t all,
+                        hipStream_t stream) {
+  if (q)
+    hipLaunchKernelGGL((quantize_saved_kernel<FMT, MODE, HAD, 2>), dim3((unsigned)all), dim3(512), 0, stream,
+                       (SavedPacks<2>{{p, *q}, (int)first}));
+  else
+    hipLaunchKernelGGL((quantize_saved_kernel<FMT, MODE, HAD, 1>), dim3((unsigned)all), dim3(512), 0, stream,
+                       (SavedPacks<1>{{p}, (int)first}));
+  return hipGetLastError();
 }
 
-SavedFn pick_saved(int fmt, int mode, int had, int act, bool has_x) {
-  if (fmt == kE2M1 && mode == kFloor && !had) return pick_act<kE2M1, kFloor, 0>(act, has_x);
-  if (fmt == kE2M3 && mode == kFloor && !had) return pick_act<kE2M3, kFloor, 0>(act, has_x);
-  if (fmt == kE2M3 && mode == kFloor && had) return pick_act<kE2M3, kFloor, 1>(act, has_x);
-  if (fmt == kE4M3 && mode == kRceil && !had) return pick_act<kE4M3, kRceil, 0>(act, has_x);
-  if (fmt == kE4M3 && mode == kFloor && !had) return pick_act<kE4M3, kFloor, 0>(act, has_x);
-  return nullptr;
+int64_t pack_tiles(const SavedPackParams& p) {
+  return ((p.C + kTile - 1) / kTile) * ((p.R + kTile - 1) / kTile);
 }
 
 // Workgroups of a save / load launch, or -1 if they do not fit a grid.
@@ -341,14 +350,17 @@ hipError_t launch_checkpoint_load(const uint8_t* codes, const uint8_t* scales, i
   return hipGetLastError();
 }
 
-hipError_t launch_quantize_saved(const SavedPackParams& p, int fmt, int mode, int had, int act, hipStream_t stream) {
-  SavedFn fn = pick_saved(fmt, mode, had, act, p.x != nullptr);
-  const int64_t tiles = ((p.C + kTile - 1) / kTile) * ((p.R + kTile - 1) / kTile) +
-                        (p.sum_out != nullptr ? (p.sum_cols + 511) / 512 : 0);
-  if (!fn || tiles >= (1ll << 31)) return hipErrorInvalidValue;
-  if (tiles == 0) return hipSuccess;
-  hipLaunchKernelGGL(fn, dim3((unsigned)tiles), dim3(512), 0, stream, p);
-  return hipGetLastError();
+hipError_t launch_quantize_saved(const SavedPackParams& p, const SavedPackParams* q, int fmt, int mode, int had,
+                                 hipStream_t stream) {
+  const int64_t first = pack_tiles(p), all = first + (q ? pack_tiles(*q) : 0);
+  if (all >= (1ll << 31)) return hipErrorInvalidValue;
+  if (all == 0) return hipSuccess;
+  if (fmt == kE2M1 && mode == kFloor && !had) return launch_packs<kE2M1, kFloor, 0>(p, q, first, all, stream);
+  if (fmt == kE2M3 && mode == kFloor && !had) return launch_packs<kE2M3, kFloor, 0>(p, q, first, all, stream);
+  if (fmt == kE2M3 && mode == kFloor && had) return launch_packs<kE2M3, kFloor, 1>(p, q, first, all, stream);
+  if (fmt == kE4M3 && mode == kRceil && !had) return launch_packs<kE4M3, kRceil, 0>(p, q, first, all, stream);
+  if (fmt == kE4M3 && mode == kFloor && !had) return launch_packs<kE4M3, kFloor, 0>(p, q, first, all, stream);
+  return hipErrorInvalidValue;
 }
 
 }  // namespace mx
