@@ -649,8 +649,10 @@ int mx_quantize_saved(const mx_quantize_saved_args* args, void* stream);
  *   db = sum of G over the tokens     binary32, before G's rounding
  *   dX = Q(G) . Q(W)                  [M][K], W's columns packed by the caller
  *   dW = Q(G^T) . Q(X^T)^T            [N][K]
- * Q packs to fmt along the product's inner dimension.  Composed of
- * mx_quantize_saved and mx_gemm_act, with their results.
+ * Q packs to fmt along the product's inner dimension.  Composed as
+ * mx_quantize_saved and mx_gemm_act, with their packs and db bit for bit and
+ * their products up to the order of the sums (fixed by the sizes and by which
+ * outputs are asked for).
  *
  *  M            tokens, any number >= 0.  N (out), K (in): multiples of 32.
  *  act, x_act   mx_act of the layer and of its input.

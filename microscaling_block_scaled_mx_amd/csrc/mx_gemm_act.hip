@@ -93,6 +93,9 @@ struct RowsCfg {
   static constexpr int kAOff = 0, kBOff = kTR * kGB, kSOff = kBOff + kTC * kGB;
   static constexpr int kStage = kSOff + 2 * 256;  // (64 scale dwords each)
   static constexpr int kRing = W * D * kStage;
+  // epilogue: units of four columns, and how many a thread takes
+  static constexpr int kUnits = kTR * kTC / 4, kPerRow = kTC / 4, kSteps = (kUnits + 64 * W - 1) / (64 * W);
+  static_assert(kUnits % 64 == 0, "whole wavefronts");
   static constexpr int kPitch = kTC + 4;  // floats: the 16 rows of a write start in different banks
   static constexpr int kRed = W * kTR * kPitch * 4;
   static constexpr int kSmem = kRing > kRed ? kRing : kRed;
@@ -130,6 +133,17 @@ __device__ __forceinline__ v8i rows_fragment(const uint8_t* panel, int x, int g,
     const v4i b = *reinterpret_cast<const v4i*>(at + 16 * rows_place<FMT>(x, 4 + g));
     return v8i{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   }
+}
+
+// Four elements at `at` of a binary32 or bf16 array, and their values.
+__device__ __forceinline__ uint4 load_four(const void* base, int64_t at, int f32) {
+  if (f32) return *reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(base) + at);
+  const uint2 h = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(base) + at);
+  return make_uint4(h.x, h.y, 0u, 0u);
+}
+__device__ __forceinline__ float4 four_values(const uint4& q, int f32) {
+  if (f32) return make_float4(__uint_as_float(q.x), __uint_as_float(q.y), __uint_as_float(q.z), __uint_as_float(q.w));
+  return make_float4(bf16_lo(q.x), bf16_hi(q.x), bf16_lo(q.y), bf16_hi(q.y));
 }
 
 // A point that no memory access is moved across.
@@ -190,6 +204,18 @@ __global__ __launch_bounds__(64 * W) void gemm_rows_kernel(Products<COUNT> all) 
     lds_dma4_s(p.b_scales + q * (uint64_t)p.N * 4, sb_off, at + CF::kSOff + 256);
   };
 
+  // the epilogue's inputs, read before the sums so that their latency is hidden
+  uint4 bias[CF::kSteps], residual[CF::kSteps];
+#pragma unroll
+  for (int u = 0; u < CF::kSteps; ++u) {
+    const int q = t + 64 * W * u;
+    const int64_t m = m0 + q / CF::kPerRow, n = n0 + 4 * (q % CF::kPerRow);
+    const bool in = q < CF::kUnits && m < p.M && n < p.N;
+    bias[u] = residual[u] = make_uint4(0u, 0u, 0u, 0u);
+    if (in && p.bias != nullptr) bias[u] = load_four(p.bias, n, p.bias_f32);
+    if (in && p.residual != nullptr) residual[u] = load_four(p.residual, m * p.ldr + n, p.c_f32);
+  }
+
   v4f acc[MI][NJ];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
@@ -242,10 +268,11 @@ __global__ __launch_bounds__(64 * W) void gemm_rows_kernel(Products<COUNT> all) 
 
   // Epilogue: four columns of a row per thread and step, rows in order; the
   // eight lanes of a 32-column block are neighbours.
-  constexpr int kUnits = CF::kTR * CF::kTC / 4, kPerRow = CF::kTC / 4;
-  static_assert(kUnits % 64 == 0, "whole wavefronts");
-  for (int q = t; q < kUnits; q += 64 * W) {
-    const int r = q / kPerRow, c = 4 * (q % kPerRow);
+#pragma unroll
+  for (int u = 0; u < CF::kSteps; ++u) {
+    const int q = t + 64 * W * u;
+    if (q >= CF::kUnits) break;  // (whole wavefronts)
+    const int r = q / CF::kPerRow, c = 4 * (q % CF::kPerRow);
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int w = 0; w < W; ++w) {
@@ -255,32 +282,23 @@ __global__ __launch_bounds__(64 * W) void gemm_rows_kernel(Products<COUNT> all) 
     }
     const int64_t m = m0 + r, n = n0 + c;
     const bool in = m < p.M && n < p.N;
-    if (in && p.bias != nullptr) {
-      if (p.bias_f32) {
-        const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p.bias) + n);
-        v[0] = v[0] + x.x;
-        v[1] = v[1] + x.y;
-        v[2] = v[2] + x.z;
-        v[3] = v[3] + x.w;
-      } else {
-        const uint2 x = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(p.bias) + n);
-        v[0] = v[0] + bf16_lo(x.x);
-        v[1] = v[1] + bf16_hi(x.x);
-        v[2] = v[2] + bf16_lo(x.y);
-        v[3] = v[3] + bf16_hi(x.y);
-      }
+    if (p.bias != nullptr) {
+      const float4 b = four_values(bias[u], p.bias_f32);
+      v[0] = v[0] + b.x;
+      v[1] = v[1] + b.y;
+      v[2] = v[2] + b.z;
+      v[3] = v[3] + b.w;
     }
     if (p.saved_codes != nullptr) {
       const uint32_t s = scale_byte<kE4M3, kRceil>(max_over8(abs_max(v)));
-      float u[4] = {v[0], v[1], v[2], v[3]};
+      float x4[4] = {v[0], v[1], v[2], v[3]};
       uint32_t w[1];
-      e4m3_encode(u, s, w);
+      e4m3_encode(x4, s, w);
       if (in) {
         *reinterpret_cast<uint32_t*>(p.saved_codes + code_group(m, n, p.M, 8) + (n & 127)) = w[0];
         if ((lane & 7) == 0) p.saved_scales[scale_offset(m, n >> 5, p.M)] = (uint8_t)s;
       }
     }
-    if (!in || p.c == nullptr) continue;
     if (p.act == kActGelu) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = act_value<kActGelu>(v[e]);
@@ -288,26 +306,19 @@ __global__ __launch_bounds__(64 * W) void gemm_rows_kernel(Products<COUNT> all) 
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = act_value<kActSilu>(v[e]);
     }
-    if (p.c_f32) {
-      if (p.residual != nullptr) {
-        const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p.residual) + m * p.ldr + n);
-        v[0] = v[0] + x.x;
-        v[1] = v[1] + x.y;
-        v[2] = v[2] + x.z;
-        v[3] = v[3] + x.w;
-      }
-      *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.c) + m * p.ldc + n) = make_float4(v[0], v[1], v[2], v[3]);
-    } else {
-      if (p.residual != nullptr) {
-        const uint2 x =
-            *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(p.residual) + m * p.ldr + n);
-        v[0] = v[0] + bf16_lo(x.x);
-        v[1] = v[1] + bf16_hi(x.x);
-        v[2] = v[2] + bf16_lo(x.y);
-        v[3] = v[3] + bf16_hi(x.y);
-      }
-      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.c) + m * p.ldc + n) =
-          make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    if (p.residual != nullptr) {
+      const float4 o = four_values(residual[u], p.c_f32);
+      v[0] = v[0] + o.x;
+      v[1] = v[1] + o.y;
+      v[2] = v[2] + o.z;
+      v[3] = v[3] + o.w;
+    }
+    if (in && p.c != nullptr) {
+      if (p.c_f32)
+        *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.c) + m * p.ldc + n) = make_float4(v[0], v[1], v[2], v[3]);
+      else
+        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.c) + m * p.ldc + n) =
+            make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
     }
   }
   // the pad blocks of the checkpoint's last K group
@@ -435,6 +446,19 @@ hipError_t launch_fmt(int fmt, const GemmActParams& p, const Second* more, int s
   }
 }
 
+// The variant that serves both products, or -1.  Each keeps its own where
+// those agree.  Where one is small enough for the few-rows kernel and its sums
+// are short (at most 8 K groups, so that a larger tile takes little longer),
+// both go to 128x128 tiles if that is the other's: 200 x 2048 x 768 with
+// 768 x 2048 x 200 in E4M3 PAIRED us in one launch, 13.7 in two.
+int pair_shape(int fmt, const GemmActParams& p, const GemmActParams& q) {
+  const int a = pick_shape(fmt, p), b = pick_shape(fmt, q);
+  if (a == b) return a;
+  if (a == kTile128 && b < kTile128 && q.M > 64 && q.K <= 1024) return a;
+  if (b == kTile128 && a < kTile128 && p.M > 64 && p.K <= 1024) return b;
+  return -1;
+}
+
 }  // namespace
 
 hipError_t launch_gemm_act(const GemmActParams& p, int fmt, hipStream_t stream) {
@@ -442,19 +466,18 @@ hipError_t launch_gemm_act(const GemmActParams& p, int fmt, hipStream_t stream) 
   return launch_fmt(fmt, p, nullptr, pick_shape(fmt, p), stream);
 }
 
-// The results do not depend on whether a launch is shared: each product keeps
-// the variant it has alone.  The one with the longer sums goes first, so that
-// the shorter tiles even out the end (4095 x 2016 x 2080 with 2080 x 2016 x
-// 4096 in E2M1: SHARED us, the other way round 32).
+// The product with the longer sums goes first, so that the shorter tiles even
+// out the end (4095 x 2016 x 2080 with 2080 x 2016 x 4096 in E2M1: 30 us, the
+// other way round 35).
 hipError_t launch_gemm_act_pair(const GemmActParams& p, const GemmActParams& q, const ColumnSums& sums, int fmt,
                                 hipStream_t stream) {
   if (q.K > p.K) return launch_gemm_act_pair(q, p, sums, fmt, stream);
   const bool both = p.M > 0 && p.N > 0 && q.M > 0 && q.N > 0;
   const Second more = {q, sums};
-  if (both && pick_shape(fmt, p) == pick_shape(fmt, q)) return launch_fmt(fmt, p, &more, pick_shape(fmt, p), stream);
+  const int shape = both ? pair_shape(fmt, p, q) : -1;
+  if (shape >= 0) return launch_fmt(fmt, p, &more, shape, stream);
   hipError_t e = hipSuccess;
-  if (sums.out && sums.cols > 0)
-    e = launch_colsum_finish(sums.partials, sums.rows, sums.cols, sums.out, 1, stream);
+  if (sums.out && sums.cols > 0) e = launch_colsum_finish(sums.partials, sums.rows, sums.cols, sums.out, 1, stream);
   if (e == hipSuccess) e = launch_gemm_act(p, fmt, stream);
   return e == hipSuccess ? launch_gemm_act(q, fmt, stream) : e;
 }

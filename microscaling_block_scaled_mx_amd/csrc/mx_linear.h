@@ -36,14 +36,13 @@ __device__ __forceinline__ void finish_column_sum(const ColumnSums& s, int64_t c
   if (c >= s.cols) return;
   const float* src = s.partials + c;
   float sum = 0.0f;
-#pragma unroll 16
+#pragma unroll 32
   for (int64_t b = 0; b < s.rows; ++b) sum = sum + src[b * s.cols];
   s.out[c] = sum;
 }
 
-// Two independent products of one format and column sums to finish, with the
-// results of separate launches (one launch where both products take the same
-// kernel variant).
+// Two independent products of one format and column sums to finish, in one
+// launch where one kernel variant serves both products.
 hipError_t launch_gemm_act_pair(const GemmActParams& p, const GemmActParams& q, const ColumnSums& sums, int fmt,
                                 hipStream_t stream);
 
