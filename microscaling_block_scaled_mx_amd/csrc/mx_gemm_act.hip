@@ -108,11 +108,11 @@ template <int FMT>
 __device__ __forceinline__ int rows_place(int x, int c) {
   if constexpr (FMT == kE4M3) return c ^ ((x >> 1) & 7);
   else if constexpr (FMT == kE2M1) return c ^ ((x >> 2) & 3);
-  else return (c + (x >> 3)) % 6;
+  else return c + (x >> 3) == 6 ? 0 : c + (x >> 3);
 }
 template <int FMT>
 __device__ __forceinline__ int rows_chunk(int x, int place) {
-  if constexpr (FMT == kE2M3) return (place + 6 - (x >> 3)) % 6;
+  if constexpr (FMT == kE2M3) return place < (x >> 3) ? 5 : place - (x >> 3);
   else return rows_place<FMT>(x, place);
 }
 
@@ -135,15 +135,18 @@ __device__ __forceinline__ v8i rows_fragment(const uint8_t* panel, int x, int g,
   }
 }
 
-// Four elements at `at` of a binary32 or bf16 array, and their values.
-__device__ __forceinline__ uint4 load_four(const void* base, int64_t at, int f32) {
-  if (f32) return *reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(base) + at);
-  const uint2 h = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(base) + at);
-  return make_uint4(h.x, h.y, 0u, 0u);
+// Four consecutive elements (8 bytes of bf16, 16 of binary32) and their values.
+__device__ __forceinline__ uint4 load_four(const uint8_t* at, int f32) {
+  const uint2 lo = *reinterpret_cast<const uint2*>(at);
+  uint2 hi = make_uint2(0u, 0u);
+  if (f32) hi = *reinterpret_cast<const uint2*>(at + 8);
+  return make_uint4(lo.x, lo.y, hi.x, hi.y);
 }
-__device__ __forceinline__ float4 four_values(const uint4& q, int f32) {
-  if (f32) return make_float4(__uint_as_float(q.x), __uint_as_float(q.y), __uint_as_float(q.z), __uint_as_float(q.w));
-  return make_float4(bf16_lo(q.x), bf16_hi(q.x), bf16_lo(q.y), bf16_hi(q.y));
+__device__ __forceinline__ void add_four(float (&v)[4], const uint4& q, int f32) {
+  v[0] = v[0] + (f32 ? __uint_as_float(q.x) : bf16_lo(q.x));
+  v[1] = v[1] + (f32 ? __uint_as_float(q.y) : bf16_hi(q.x));
+  v[2] = v[2] + (f32 ? __uint_as_float(q.z) : bf16_lo(q.y));
+  v[3] = v[3] + (f32 ? __uint_as_float(q.w) : bf16_hi(q.y));
 }
 
 // A point that no memory access is moved across.
@@ -162,59 +165,50 @@ __global__ __launch_bounds__(64 * W) void gemm_rows_kernel(Products<COUNT> all) 
   __shared__ __attribute__((aligned(16))) uint8_t smem[CF::kSmem];
   const int t = threadIdx.x, lane = t & 63, wave = wave_uniform(t >> 6);
   const int x = lane & 15, g = lane >> 4;
-  const int tiles_m = (int)((p.M + CF::kTR - 1) / CF::kTR);
+  // (M and N are below 2^31, a tile's rows and columns below 64)
+  const uint32_t M = (uint32_t)p.M, N = (uint32_t)p.N;
+  const int tiles_m = (int)((M + CF::kTR - 1) / CF::kTR);
   const int tn = tile / tiles_m, tm = tile - tn * tiles_m;
-  const int64_t m0 = (int64_t)tm * CF::kTR, n0 = (int64_t)tn * CF::kTC;
+  const uint32_t m0 = (uint32_t)tm * CF::kTR, n0 = (uint32_t)tn * CF::kTC;
   const int nq = (int)((p.K + 127) / 128);
   const int n_own = wave < nq ? (nq - wave + W - 1) / W : 0;  // this wavefront's K groups
 
   // byte offsets of this lane's loads within a K group (32-bit: operands are
   // under 2 GiB)
-  const auto row_of = [](int64_t first, int r, int64_t rows) {
-    return (uint32_t)(first + r < rows ? first + r : rows - 1);
+  const auto row_of = [](uint32_t first, int r, uint32_t rows) {
+    const uint32_t row = first + (uint32_t)r;
+    return row < rows ? row : rows - 1;
   };
   uint32_t a_off[CF::kALoads], b_off[CF::kBLoads];
 #pragma unroll
-  for (int i = 0; i < CF::kALoads; ++i) {
-    const int s = 64 * i + lane, r = s / CF::kChunks;
-    a_off[i] = row_of(m0, r, p.M) * CF::kGB + 16 * rows_chunk<FMT>(r & 15, s % CF::kChunks);
+  for (int i = 0; i < CF::kBLoads; ++i) {
+    const uint32_t s = 64 * i + lane, r = s / CF::kChunks;
+    b_off[i] = row_of(n0, r, N) * CF::kGB + 16 * rows_chunk<FMT>(r & 15, s - r * CF::kChunks);
   }
 #pragma unroll
-  for (int i = 0; i < CF::kBLoads; ++i) {
-    const int s = 64 * i + lane, r = s / CF::kChunks;
-    b_off[i] = row_of(n0, r, p.N) * CF::kGB + 16 * rows_chunk<FMT>(r & 15, s % CF::kChunks);
+  for (int i = 0; i < CF::kALoads; ++i) {
+    const uint32_t s = 64 * i + lane, r = s / CF::kChunks;
+    a_off[i] = row_of(m0, r, M) * CF::kGB + 16 * rows_chunk<FMT>(r & 15, s - r * CF::kChunks);
   }
-  const uint32_t sa_off = row_of(m0, lane < CF::kTR ? lane : 0, p.M) * 4;
-  const uint32_t sb_off = row_of(n0, lane < CF::kTC ? lane : 0, p.N) * 4;
+  const uint32_t sa_off = row_of(m0, lane < CF::kTR ? lane : 0, M) * 4;
+  const uint32_t sb_off = row_of(n0, lane < CF::kTC ? lane : 0, N) * 4;
 
   uint8_t* const ring = smem + wave * (D * CF::kStage);
   const uint32_t ring_lds = (uint32_t)wave_uniform((int)lds_addr(ring));
   const auto issue = [&](int it, int buf) __attribute__((always_inline)) {
     const uint64_t q = (uint64_t)(wave + it * W);
     const uint32_t at = ring_lds + (uint32_t)(buf * CF::kStage);
-    const uint8_t* ac = p.a_codes + q * (uint64_t)p.M * CF::kGB;
-    const uint8_t* bc = p.b_codes + q * (uint64_t)p.N * CF::kGB;
+    const uint8_t* ac = p.a_codes + q * (M * CF::kGB);  // (a K group's bytes fit 32 bits)
+    const uint8_t* bc = p.b_codes + q * (N * CF::kGB);
 #pragma unroll
     for (int i = 0; i < CF::kBLoads; ++i)
       if (64 * (i + 1) <= CF::kTC * CF::kChunks || lane < 32) lds_dma16_s(bc, b_off[i], at + CF::kBOff + 1024 * i);
 #pragma unroll
     for (int i = 0; i < CF::kALoads; ++i)
       if (64 * (i + 1) <= CF::kTR * CF::kChunks || lane < 32) lds_dma16_s(ac, a_off[i], at + CF::kAOff + 1024 * i);
-    lds_dma4_s(p.a_scales + q * (uint64_t)p.M * 4, sa_off, at + CF::kSOff);
-    lds_dma4_s(p.b_scales + q * (uint64_t)p.N * 4, sb_off, at + CF::kSOff + 256);
+    lds_dma4_s(p.a_scales + q * (M * 4), sa_off, at + CF::kSOff);
+    lds_dma4_s(p.b_scales + q * (N * 4), sb_off, at + CF::kSOff + 256);
   };
-
-  // the epilogue's inputs, read before the sums so that their latency is hidden
-  uint4 bias[CF::kSteps], residual[CF::kSteps];
-#pragma unroll
-  for (int u = 0; u < CF::kSteps; ++u) {
-    const int q = t + 64 * W * u;
-    const int64_t m = m0 + q / CF::kPerRow, n = n0 + 4 * (q % CF::kPerRow);
-    const bool in = q < CF::kUnits && m < p.M && n < p.N;
-    bias[u] = residual[u] = make_uint4(0u, 0u, 0u, 0u);
-    if (in && p.bias != nullptr) bias[u] = load_four(p.bias, n, p.bias_f32);
-    if (in && p.residual != nullptr) residual[u] = load_four(p.residual, m * p.ldr + n, p.c_f32);
-  }
 
   v4f acc[MI][NJ];
 #pragma unroll
@@ -227,6 +221,20 @@ __global__ __launch_bounds__(64 * W) void gemm_rows_kernel(Products<COUNT> all) 
 #pragma unroll
   for (int it = 0; it < D - 1; ++it)
     if (it < n_own) issue(it, it);
+  // the epilogue's inputs, read beside the sums (older in the count of
+  // outstanding loads than any that a group's wait lets fly)
+  const int c_bytes = p.c_f32 ? 4 : 2, bias_bytes = p.bias_f32 ? 4 : 2;
+  const uint8_t* const res0 = reinterpret_cast<const uint8_t*>(p.residual) + ((int64_t)m0 * p.ldr + n0) * c_bytes;
+  const uint8_t* const bias0 = reinterpret_cast<const uint8_t*>(p.bias) + (int64_t)n0 * bias_bytes;
+  uint4 bias[CF::kSteps], residual[CF::kSteps];
+#pragma unroll
+  for (int u = 0; u < CF::kSteps; ++u) {
+    const int q = t + 64 * W * u, r = q / CF::kPerRow, c = 4 * (q % CF::kPerRow);
+    const bool in = q < CF::kUnits && m0 + r < M && n0 + c < N;
+    bias[u] = residual[u] = make_uint4(0u, 0u, 0u, 0u);
+    if (in && p.bias != nullptr) bias[u] = load_four(bias0 + c * bias_bytes, p.bias_f32);
+    if (in && p.residual != nullptr) residual[u] = load_four(res0 + (r * p.ldr + c) * c_bytes, p.c_f32);
+  }
   int buf = 0;
   for (int it = 0; it < n_own; ++it) {
     if (it + D - 1 < n_own) {
@@ -241,12 +249,12 @@ __global__ __launch_bounds__(64 * W) void gemm_rows_kernel(Products<COUNT> all) 
     int sb[NJ];
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      b[j] = rows_fragment<FMT>(stage + CF::kBOff + 16 * j * CF::kGB, x, g, row_of(n0, 16 * j + x, p.N));
+      b[j] = rows_fragment<FMT>(stage + CF::kBOff + 16 * j * CF::kGB, x, g, row_of(n0, 16 * j + x, N));
       sb[j] = (int)(*reinterpret_cast<const uint32_t*>(stage + CF::kSOff + 256 + 4 * (16 * j + x)) >> (8 * g));
     }
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-      const v8i a = rows_fragment<FMT>(stage + CF::kAOff + 16 * i * CF::kGB, x, g, row_of(m0, 16 * i + x, p.M));
+      const v8i a = rows_fragment<FMT>(stage + CF::kAOff + 16 * i * CF::kGB, x, g, row_of(m0, 16 * i + x, M));
       const int sa = (int)(*reinterpret_cast<const uint32_t*>(stage + CF::kSOff + 4 * (16 * i + x)) >> (8 * g));
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
@@ -268,6 +276,10 @@ __global__ __launch_bounds__(64 * W) void gemm_rows_kernel(Products<COUNT> all) 
 
   // Epilogue: four columns of a row per thread and step, rows in order; the
   // eight lanes of a 32-column block are neighbours.
+  // A tile's columns lie in one K group of the checkpoint.
+  uint8_t* const codes0 = p.saved_codes + code_group(m0, n0, M, 8) + (n0 & 127);
+  uint8_t* const scales0 = p.saved_scales + scale_offset(m0, n0 >> 5, M);
+  uint8_t* const c0 = reinterpret_cast<uint8_t*>(p.c) + ((int64_t)m0 * p.ldc + n0) * c_bytes;
 #pragma unroll
   for (int u = 0; u < CF::kSteps; ++u) {
     const int q = t + 64 * W * u;
@@ -280,23 +292,16 @@ __global__ __launch_bounds__(64 * W) void gemm_rows_kernel(Products<COUNT> all) 
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = v[e] + part[e];
     }
-    const int64_t m = m0 + r, n = n0 + c;
-    const bool in = m < p.M && n < p.N;
-    if (p.bias != nullptr) {
-      const float4 b = four_values(bias[u], p.bias_f32);
-      v[0] = v[0] + b.x;
-      v[1] = v[1] + b.y;
-      v[2] = v[2] + b.z;
-      v[3] = v[3] + b.w;
-    }
+    const bool in = m0 + r < M && n0 + c < N;
+    if (p.bias != nullptr) add_four(v, bias[u], p.bias_f32);
     if (p.saved_codes != nullptr) {
       const uint32_t s = scale_byte<kE4M3, kRceil>(max_over8(abs_max(v)));
       float x4[4] = {v[0], v[1], v[2], v[3]};
       uint32_t w[1];
       e4m3_encode(x4, s, w);
       if (in) {
-        *reinterpret_cast<uint32_t*>(p.saved_codes + code_group(m, n, p.M, 8) + (n & 127)) = w[0];
-        if ((lane & 7) == 0) p.saved_scales[scale_offset(m, n >> 5, p.M)] = (uint8_t)s;
+        *reinterpret_cast<uint32_t*>(codes0 + (r * 128 + c)) = w[0];
+        if ((lane & 7) == 0) scales0[r * 4 + (c >> 5)] = (uint8_t)s;
       }
     }
     if (p.act == kActGelu) {
@@ -306,30 +311,22 @@ __global__ __launch_bounds__(64 * W) void gemm_rows_kernel(Products<COUNT> all) 
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = act_value<kActSilu>(v[e]);
     }
-    if (p.residual != nullptr) {
-      const float4 o = four_values(residual[u], p.c_f32);
-      v[0] = v[0] + o.x;
-      v[1] = v[1] + o.y;
-      v[2] = v[2] + o.z;
-      v[3] = v[3] + o.w;
-    }
+    if (p.residual != nullptr) add_four(v, residual[u], p.c_f32);
     if (in && p.c != nullptr) {
-      if (p.c_f32)
-        *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.c) + m * p.ldc + n) = make_float4(v[0], v[1], v[2], v[3]);
-      else
-        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.c) + m * p.ldc + n) =
-            make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+      uint8_t* const at = c0 + (r * p.ldc + c) * c_bytes;
+      if (p.c_f32) *reinterpret_cast<float4*>(at) = make_float4(v[0], v[1], v[2], v[3]);
+      else *reinterpret_cast<uint2*>(at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
     }
   }
-  // the pad blocks of the checkpoint's last K group
-  if (p.saved_codes != nullptr && n0 + CF::kTC >= p.N) {
-    const int pad = (int)(((p.N + 127) & ~(int64_t)127) - p.N);  // 0, 32, 64 or 96 columns
+  // the pad blocks of the checkpoint's last K group: 0, 32, 64 or 96 columns
+  if (p.saved_codes != nullptr && n0 + CF::kTC >= N) {
+    const int pad = (int)(((N + 127) & ~127u) - N);
     for (int q = t; q < CF::kTR * pad / 4; q += 64 * W) {
       const int r = q / (pad / 4);
-      const int64_t m = m0 + r, n = p.N + 4 * (q - r * (pad / 4));
-      if (m < p.M) {
-        *reinterpret_cast<uint32_t*>(p.saved_codes + code_group(m, n, p.M, 8) + (n & 127)) = 0u;
-        if ((n & 31) == 0) p.saved_scales[scale_offset(m, n >> 5, p.M)] = 0;
+      const uint32_t m = m0 + r, n = N + 4 * (q - r * (pad / 4));
+      if (m < M) {
+        *reinterpret_cast<uint32_t*>(p.saved_codes + code_group(m, n, M, 8) + (n & 127)) = 0u;
+        if ((n & 31) == 0) p.saved_scales[scale_offset(m, n >> 5, M)] = 0;
       }
     }
   }
