@@ -395,8 +395,10 @@ enum Shape {
 //    Their cost per round of the chip goes by area, 128x128 15% more.  With a
 //    checkpoint (E2M1: or an activation) in the epilogue, over several rounds,
 //    256x128 at two per unit, so that one tile's epilogue runs beside
-//    another's products: 8192 x 8192 x 2048 GELU + checkpoint 126 / 151 / 194,
-//    256x256 144 / 158 / 192; without either 99 / 123 against 103 / 121.
+//    another's products -- while the sums are short, since its main loop is
+//    the slower one: 8192 x 8192 x 2048 with GELU and checkpoint 129 / 155 /
+//    198, 256x256 156 / 168 / 194; 16384 x 8192 x 4096 with GELU 329 / 448 /
+//    635 against 340 / 398 / 537.
 int pick_shape(int fmt, const GemmActParams& p) {
   const int64_t cus = cu_count();
   if (p.M <= 16) return tile_count(p, 16, 32) >= cus ? kRows16x32 : kRows16x32Deep;
@@ -412,8 +414,10 @@ int pick_shape(int fmt, const GemmActParams& p) {
   const int64_t cost256 = (t256 + cus - 1) / cus * 65536;
   const int64_t cost128 = (t128 / (2 * cus) * 32768 + (rest == 0 ? 0 : rest <= cus ? 22000 : 32768)) * 115 / 100;
   if (cost256 > cost128) return kTile128;
-  const bool busy = p.saved_codes != nullptr || (fmt == kE2M1 && p.act != kActNone);
-  return fmt != kE4M3 && busy && t256 > cus ? kTile256x128 : kTile256;
+  const bool overlap = fmt == kE2M1   ? (p.saved_codes != nullptr || p.act != kActNone) && p.K <= 4096
+                       : fmt == kE2M3 ? p.saved_codes != nullptr && p.K <= 2048
+                                      : false;
+  return overlap && t256 > cus ? kTile256x128 : kTile256;
 }
 
 template <int FMT>
