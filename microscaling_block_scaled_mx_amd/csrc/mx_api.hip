@@ -217,13 +217,16 @@ bool dtype_ok(int d) { return d == MX_BF16 || d == MX_F32; }
 int64_t up32(int64_t n) { return (n + 31) / 32 * 32; }
 // sizes past this are refused before they are multiplied
 constexpr int64_t kMaxExtent = 1ll << 40;
-// row pitch of an [R][C] tensor: in 8-element steps, the last row's end addressable
-bool pitch_ok(int64_t ld, int64_t C) { return ld >= C && ld % 8 == 0 && ld <= kMaxExtent; }
+// row pitch of a tensor with C columns: in 8-element steps
+bool pitch_ok(int64_t ld, int64_t C) { return ld >= C && ld % 8 == 0; }
+// the byte offset of a row fits 64 bits with room to spare
+bool rows_fit(int64_t R, int64_t ld) { return R <= kMaxExtent && ld <= (1ll << 60) / (R > 0 ? R : 1); }
 
 int validate_gemm_act(const mx_gemm_act_args& a) {
   if (bits_of(a.fmt) == 0 || !act_ok(a.act) || !dtype_ok(a.c_dtype) || !dtype_ok(a.bias_dtype)) return MX_ERR_FORMAT;
   if (a.M < 0 || a.N < 0 || a.K < 0 || a.N % 32 || a.K % 32) return MX_ERR_SHAPE;
   if (a.M > kMaxExtent || a.N > kMaxExtent || a.K > kMaxExtent) return MX_ERR_INDEX_OVERFLOW;
+  if ((a.C && !rows_fit(a.M, a.ldc)) || (a.residual && !rows_fit(a.M, a.ldr))) return MX_ERR_INDEX_OVERFLOW;
   if (packed_ok(a.saved) == packed_none(a.saved)) return MX_ERR_NULL;  // half a pair
   if (a.C && !pitch_ok(a.ldc, a.N)) return MX_ERR_SHAPE;
   if (a.residual && !pitch_ok(a.ldr, a.N)) return MX_ERR_SHAPE;
@@ -277,7 +280,7 @@ int validate_checkpoint(const void* x, int dtype, int64_t R, int64_t C, int64_t 
                         const void* scales) {
   if (!dtype_ok(dtype)) return MX_ERR_FORMAT;
   if (R < 0 || C < 0 || C % 32 || !pitch_ok(ld, C)) return MX_ERR_SHAPE;
-  if (R > kMaxExtent || C > kMaxExtent) return MX_ERR_INDEX_OVERFLOW;
+  if (C > kMaxExtent || !rows_fit(R, ld)) return MX_ERR_INDEX_OVERFLOW;
   const void* ptrs[] = {x, codes, scales};
   for (const void* q : ptrs)
     if (q && !aligned16(q)) return MX_ERR_ALIGN;
@@ -295,6 +298,7 @@ int validate_quantize_saved(const mx_quantize_saved_args& a) {
     if (packed_ok(*q) == packed_none(*q)) return MX_ERR_NULL;
   if (a.colsum && !a.colsum_partials && a.R > 0) return MX_ERR_NULL;
   if (a.x && !pitch_ok(a.ldx, a.C)) return MX_ERR_SHAPE;
+  if (a.x && !rows_fit(a.R, a.ldx)) return MX_ERR_INDEX_OVERFLOW;
   const void* ptrs[] = {a.x, a.saved.codes, a.saved.scales, a.row.codes, a.row.scales,
                         a.col.codes, a.col.scales, a.colsum_partials, a.colsum};
   for (const void* q : ptrs)

@@ -341,34 +341,41 @@ struct Second {
   const ColumnSums& sums;
 };
 
-// One launch of `one`, or of `two` with a second product.
-template <class F1, class F2>
-hipError_t launch_products(F1 one, F2 two, int threads, int bm, int bn, const GemmActParams& p, const Second* more,
-                           hipStream_t stream) {
-  const int64_t first = tile_count(p, bm, bn);
-  if (!more) {
-    if (first >= (1ll << 31)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(one, dim3((unsigned)first), dim3(threads), 0, stream, (Products<1>{{p}, (int)first, 0, {}}));
-    return hipGetLastError();
-  }
-  const int64_t summing = more->sums.out ? (more->sums.cols + threads - 1) / threads : 0;
-  const int64_t all = summing + first + tile_count(more->q, bm, bn);
-  if (all >= (1ll << 31)) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(two, dim3((unsigned)all), dim3(threads), 0, stream,
-                     (Products<2>{{p, more->q}, (int)first, (int)summing, more->sums}));
+template <class F>
+hipError_t launch_one_product(F kernel, int threads, int bm, int bn, const GemmActParams& p, hipStream_t stream) {
+  const int64_t tiles = tile_count(p, bm, bn);
+  if (tiles >= (1ll << 31)) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)tiles), dim3(threads), 0, stream, (Products<1>{{p}, (int)tiles, 0, {}}));
   return hipGetLastError();
 }
 
-template <int FMT, int BM, int BN, int OCC>
-hipError_t launch_tiles(const GemmActParams& p, const Second* more, hipStream_t stream) {
-  return launch_products(gemm_act_kernel<FMT, BM, BN, OCC, 1>, gemm_act_kernel<FMT, BM, BN, OCC, 2>,
-                         Cfg<FMT, BM, BN, kDense, kEpiAct, OCC>::kThreads, BM, BN, p, more, stream);
+template <class F>
+hipError_t launch_two_products(F kernel, int threads, int bm, int bn, const GemmActParams& p, const Second& more,
+                               hipStream_t stream) {
+  const int64_t summing = more.sums.out ? (more.sums.cols + threads - 1) / threads : 0;
+  const int64_t first = tile_count(p, bm, bn), all = summing + first + tile_count(more.q, bm, bn);
+  if (all >= (1ll << 31)) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)all), dim3(threads), 0, stream,
+                     (Products<2>{{p, more.q}, (int)first, (int)summing, more.sums}));
+  return hipGetLastError();
 }
 
-template <int FMT, int MI, int NJ, int W, int D>
+// PAIRS: whether two products may share a launch of this variant (kernels
+// that no pair takes are not built).
+template <int FMT, int BM, int BN, int OCC, bool PAIRS = true>
+hipError_t launch_tiles(const GemmActParams& p, const Second* more, hipStream_t stream) {
+  constexpr int kThreads = Cfg<FMT, BM, BN, kDense, kEpiAct, OCC>::kThreads;
+  if (!more) return launch_one_product(gemm_act_kernel<FMT, BM, BN, OCC, 1>, kThreads, BM, BN, p, stream);
+  if constexpr (PAIRS) return launch_two_products(gemm_act_kernel<FMT, BM, BN, OCC, 2>, kThreads, BM, BN, p, *more, stream);
+  return hipErrorInvalidValue;
+}
+
+template <int FMT, int MI, int NJ, int W, int D, bool PAIRS = true>
 hipError_t launch_rows(const GemmActParams& p, const Second* more, hipStream_t stream) {
-  return launch_products(gemm_rows_kernel<FMT, MI, NJ, W, D, 1>, gemm_rows_kernel<FMT, MI, NJ, W, D, 2>, 64 * W,
-                         16 * MI, 16 * NJ, p, more, stream);
+  if (!more) return launch_one_product(gemm_rows_kernel<FMT, MI, NJ, W, D, 1>, 64 * W, 16 * MI, 16 * NJ, p, stream);
+  if constexpr (PAIRS)
+    return launch_two_products(gemm_rows_kernel<FMT, MI, NJ, W, D, 2>, 64 * W, 16 * MI, 16 * NJ, p, *more, stream);
+  return hipErrorInvalidValue;
 }
 
 // The kernel variants: rows_<tile>, the few-rows kernel, and tile_<size>.
@@ -423,15 +430,15 @@ int pick_shape(int fmt, const GemmActParams& p) {
 template <int FMT>
 hipError_t launch_shape(const GemmActParams& p, const Second* more, int shape, hipStream_t stream) {
   switch (shape) {
-    case kRows16x32: return launch_rows<FMT, 1, 2, 4, 3>(p, more, stream);
-    case kRows16x32Deep: return launch_rows<FMT, 1, 2, 8, 2>(p, more, stream);
+    case kRows16x32: return launch_rows<FMT, 1, 2, 4, 3, false>(p, more, stream);
+    case kRows16x32Deep: return launch_rows<FMT, 1, 2, 8, 2, false>(p, more, stream);
     case kRows32x32: return launch_rows<FMT, 2, 2, 4, 2>(p, more, stream);
     case kRows32x32Deep: return launch_rows<FMT, 2, 2, 8, 2>(p, more, stream);
     case kRows64x32: return launch_rows<FMT, 4, 2, 4, 2>(p, more, stream);
     case kRows64x64: return launch_rows<FMT, 4, 4, 4, 2>(p, more, stream);
     case kTile128: return launch_tiles<FMT, 128, 128, 2>(p, more, stream);
     case kTile256x128:
-      if constexpr (FMT != kE4M3) return launch_tiles<FMT, 256, 128, 2>(p, more, stream);
+      if constexpr (FMT != kE4M3) return launch_tiles<FMT, 256, 128, 2, false>(p, more, stream);
       else return hipErrorInvalidValue;
     case kTile256: return launch_tiles<FMT, 256, 256, 1>(p, more, stream);
     default: return hipErrorInvalidValue;
@@ -454,6 +461,8 @@ hipError_t launch_fmt(int fmt, const GemmActParams& p, const Second* more, int s
 // 768 x 2048 x 200 in E4M3 PAIRED us in one launch, 13.7 in two.
 int pair_shape(int fmt, const GemmActParams& p, const GemmActParams& q) {
   const int a = pick_shape(fmt, p), b = pick_shape(fmt, q);
+  const auto single = [](int v) { return v == kRows16x32 || v == kRows16x32Deep || v == kTile256x128; };
+  if (single(a) || single(b)) return -1;  // (a weight gradient has 32 rows or more, neither product a checkpoint)
   if (a == b) return a;
   if (a == kTile128 && b < kTile128 && q.M > 64 && q.K <= 1024) return a;
   if (b == kTile128 && a < kTile128 && p.M > 64 && p.K <= 1024) return b;

@@ -162,7 +162,7 @@ def gemm_args(**kw):
     (dict(C=ctypes.c_void_p(0x1008)), ALIGN), (dict(bias=ctypes.c_void_p(0x1002)), ALIGN),
     (dict(saved=mx.Packed(ctypes.c_void_p(0x1001), P[1])), ALIGN),
     (dict(M=1 << 31), OVERFLOW), (dict(M=1 << 25, K=4096), OVERFLOW), (dict(N=1 << 25, K=4096, ldc=1 << 25, ldr=1 << 25), OVERFLOW),
-    (dict(M=1 << 50), OVERFLOW), (dict(M=1 << 20, N=1 << 20, K=32, ldc=1 << 20, ldr=1 << 20), OVERFLOW),
+    (dict(M=1 << 50), OVERFLOW), (dict(ldc=1 << 60), OVERFLOW), (dict(ldr=1 << 60), OVERFLOW), (dict(M=1 << 20, N=1 << 20, K=32, ldc=1 << 20, ldr=1 << 20), OVERFLOW),
 ])
 def test_gemm_act_refusals(kw, want):
     assert mx.lib().mx_gemm_act(ctypes.byref(gemm_args(**kw)), None) == want
@@ -322,7 +322,7 @@ def test_checkpoint_of_a_column_slice_leaves_its_neighbours():
 # ---------------------------------------------------------------- GEMM
 SIZES = [(1, 32, 32), (1, 2080, 160), (5, 96, 128), (16, 64, 2048), (17, 64, 96), (32, 160, 384), (33, 32, 1056),
          (3, 8224, 160), (29, 8224, 416), (64, 288, 256), (65, 64, 32), (100, 352, 800), (130, 2080, 416), (257, 4096, 96),
-         (200, 4128, 640), (300, 8224, 64), (2039, 8160, 96), (4100, 4128, 160)]
+         (200, 4128, 640), (300, 8224, 64), (2039, 8160, 96), (4100, 4128, 160), (4090, 8160, 64)]
 
 
 @gpu
@@ -565,7 +565,8 @@ def bwd_work(M, N, K, fmt):
 @pytest.mark.parametrize("fmt,mode,had", FMTS)
 @pytest.mark.parametrize("act,x_act", [(mx.ACT_NONE, mx.ACT_GELU_TANH), (mx.ACT_GELU_TANH, mx.ACT_NONE),
                                        (mx.ACT_SILU, mx.ACT_SILU)])
-@pytest.mark.parametrize("M,N,K", [(1, 64, 96), (50, 96, 160), (333, 256, 416), (200, 768, 2048), (700, 2080, 1024)])
+@pytest.mark.parametrize("M,N,K", [(1, 64, 96), (50, 96, 160), (333, 256, 416), (200, 768, 2048), (700, 2080, 1024), (300, 320, 1024),
+                                   (700, 704, 1024), (20, 32, 8224)])
 def test_linear_bwd_against_64_bits(M, N, K, act, x_act, fmt, mode, had):
     rng = np.random.default_rng(M + N + K + fmt + act)
     dY = dev_bf16(rng.standard_normal((M, N)))
@@ -616,6 +617,33 @@ def test_linear_bwd_against_64_bits(M, N, K, act, x_act, fmt, mode, had):
     mx.linear_bwd_saved(M, N, K, dY, cx, None, dW=acc, dPc=work["dPc"], Xc=work["Xc"], accumulate=True, **kw)
     torch.cuda.synchronize()
     assert same(only, dX) and same(acc - 1, dW)
+
+
+@gpu
+@pytest.mark.parametrize("fmt,mode,had", FMTS)
+def test_linear_bwd_of_large_tiles_is_its_parts(fmt, mode, had):
+    """Both products of 256 x 256 tiles, column sums beside them: one launch, bit for bit the separate calls."""
+    M, N, K = 2040, 2048, 8192
+    rng = np.random.default_rng(fmt)
+    t = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32)).bfloat16().cuda()
+    dY, cx, cp = t(M, N), mx.alloc_packed(M, K, mx.E4M3), mx.alloc_packed(M, N, mx.E4M3)
+    mx.checkpoint_save(t(M, K), cx)
+    mx.checkpoint_save(t(M, N), cp)
+    Wc = mx.alloc_packed(K, N, fmt)
+    mx.quantize_saved(K, N, fmt, mode, had, x=t(K, N), row=Wc)
+    outs = [[torch.empty(M, K, dtype=torch.bfloat16, device="cuda"), torch.empty(N, K, device="cuda"), torch.empty(N, device="cuda")]
+            for _ in range(2)]
+    (dX, dW, db), (dX2, dW2, db2) = outs
+    w, v = bwd_work(M, N, K, fmt), bwd_work(M, N, K, fmt)
+    q = dict(fmt=fmt, scale_mode=mode, hadamard=had)
+    mx.linear_bwd_saved(M, N, K, dY, cx, Wc, act=mx.ACT_SILU, saved_pre=cp, dX=dX, dW=dW, db=db, **q, **w)
+    mx.quantize_saved(M, N, act=mx.ACT_SILU, x=dY, saved=cp, row=v["dPr"], col=v["dPc"], colsum_partials=v["db_partials"],
+                      colsum=db2, **q)
+    mx.quantize_saved(M, K, saved=cx, col=v["Xc"], **q)
+    mx.gemm_act(v["dPr"], Wc, M, K, N, fmt, dX2)
+    mx.gemm_act(v["dPc"], v["Xc"], N, K, 2048, fmt, dW2)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(*outs))
 
 
 @gpu
