@@ -370,12 +370,10 @@ hipError_t launch_tiles(const GemmActParams& p, const Second* more, hipStream_t 
   return hipErrorInvalidValue;
 }
 
-template <int FMT, int MI, int NJ, int W, int D, bool PAIRS = true>
+template <int FMT, int MI, int NJ, int W, int D>
 hipError_t launch_rows(const GemmActParams& p, const Second* more, hipStream_t stream) {
   if (!more) return launch_one_product(gemm_rows_kernel<FMT, MI, NJ, W, D, 1>, 64 * W, 16 * MI, 16 * NJ, p, stream);
-  if constexpr (PAIRS)
-    return launch_two_products(gemm_rows_kernel<FMT, MI, NJ, W, D, 2>, 64 * W, 16 * MI, 16 * NJ, p, *more, stream);
-  return hipErrorInvalidValue;
+  return launch_two_products(gemm_rows_kernel<FMT, MI, NJ, W, D, 2>, 64 * W, 16 * MI, 16 * NJ, p, *more, stream);
 }
 
 // The kernel variants: rows_<tile>, the few-rows kernel, and tile_<size>.
@@ -430,8 +428,8 @@ int pick_shape(int fmt, const GemmActParams& p) {
 template <int FMT>
 hipError_t launch_shape(const GemmActParams& p, const Second* more, int shape, hipStream_t stream) {
   switch (shape) {
-    case kRows16x32: return launch_rows<FMT, 1, 2, 4, 3, false>(p, more, stream);
-    case kRows16x32Deep: return launch_rows<FMT, 1, 2, 8, 2, false>(p, more, stream);
+    case kRows16x32: return launch_rows<FMT, 1, 2, 4, 3>(p, more, stream);
+    case kRows16x32Deep: return launch_rows<FMT, 1, 2, 8, 2>(p, more, stream);
     case kRows32x32: return launch_rows<FMT, 2, 2, 4, 2>(p, more, stream);
     case kRows32x32Deep: return launch_rows<FMT, 2, 2, 8, 2>(p, more, stream);
     case kRows64x32: return launch_rows<FMT, 4, 2, 4, 2>(p, more, stream);
@@ -455,18 +453,18 @@ hipError_t launch_fmt(int fmt, const GemmActParams& p, const Second* more, int s
 }
 
 // The variant that serves both products, or -1.  Each keeps its own where
-// those agree.  Where one is small enough for the few-rows kernel and its sums
-// are short (at most 8 K groups, so that a larger tile takes little longer),
-// both go to 128x128 tiles if that is the other's: 200 x 2048 x 768 with
-// 768 x 2048 x 200 in E4M3 PAIRED us in one launch, 13.7 in two.
+// those agree.  Else the smaller tile's product takes the larger's variant if
+// that costs it less than the launch it saves (about 4 us): its sums are then
+// split over fewer wavefronts, or over none, so they have to be short.
+// 200 x 2048 x 768 with 768 x 2048 x 200 in E4M3 took 9.9 us so, 13.7 in two
+// launches.
 int pair_shape(int fmt, const GemmActParams& p, const GemmActParams& q) {
   const int a = pick_shape(fmt, p), b = pick_shape(fmt, q);
-  const auto single = [](int v) { return v == kRows16x32 || v == kRows16x32Deep || v == kTile256x128; };
-  if (single(a) || single(b)) return -1;  // (a weight gradient has 32 rows or more, neither product a checkpoint)
   if (a == b) return a;
-  if (a == kTile128 && b < kTile128 && q.M > 64 && q.K <= 1024) return a;
-  if (b == kTile128 && a < kTile128 && p.M > 64 && p.K <= 1024) return b;
-  return -1;
+  const int large = a > b ? a : b;
+  const int64_t groups = ((a > b ? q : p).K + 127) / 128;
+  if (large < kTile128) return groups <= 48 ? large : -1;
+  return large == kTile128 && groups <= 16 ? large : -1;
 }
 
 }  // namespace
@@ -483,12 +481,19 @@ hipError_t launch_gemm_act_pair(const GemmActParams& p, const GemmActParams& q, 
                                 hipStream_t stream) {
   if (q.K > p.K) return launch_gemm_act_pair(q, p, sums, fmt, stream);
   const bool both = p.M > 0 && p.N > 0 && q.M > 0 && q.N > 0;
-  const Second more = {q, sums};
   const int shape = both ? pair_shape(fmt, p, q) : -1;
+  const Second more = {q, sums};
   if (shape >= 0) return launch_fmt(fmt, p, &more, shape, stream);
+  // two launches, the column sums with the first
+  GemmActParams none = q;
+  none.M = 0;
+  const Second only_sums = {none, sums};
+  const bool carry = p.M > 0 && p.N > 0;
   hipError_t e = hipSuccess;
-  if (sums.out && sums.cols > 0) e = launch_colsum_finish(sums.partials, sums.rows, sums.cols, sums.out, 1, stream);
-  if (e == hipSuccess) e = launch_gemm_act(p, fmt, stream);
+  if (carry)
+    e = launch_fmt(fmt, p, sums.out ? &only_sums : nullptr, pick_shape(fmt, p), stream);
+  else if (sums.out && sums.cols > 0)
+    e = launch_colsum_finish(sums.partials, sums.rows, sums.cols, sums.out, 1, stream);
   return e == hipSuccess ? launch_gemm_act(q, fmt, stream) : e;
 }
 

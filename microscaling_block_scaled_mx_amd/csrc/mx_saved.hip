@@ -157,20 +157,21 @@ __device__ __forceinline__ float sum_over_rows4(float v) {
 #endif
 }
 
-// Step 1 of a tile: every load in flight, then v, its column sums, and bf16 in
-// LDS.  HASX: v = x act'(saved) (ACT none: v = x, no checkpoint), else
-// v = act(saved).
-template <int ACT, int HASX>
-__device__ __forceinline__ void form_tile(const SavedPackParams& p, int64_t bx, int64_t by, uint8_t* tile,
-                                          float (&part)[8][kTile]) {
+// STEPS 32-row steps of a tile from step i0 on: every load in flight, then v,
+// its column sums, and bf16 in LDS.  HASX: v = x act'(saved) (ACT none: v = x,
+// no checkpoint), else v = act(saved).
+template <int ACT, int HASX, int STEPS>
+__device__ __forceinline__ void form_steps(const SavedPackParams& p, int64_t bx, int64_t by, int i0, uint8_t* tile,
+                                           float (&sum)[8]) {
   constexpr bool kSaved = !HASX || ACT != kActNone;
   const int t = threadIdx.x, ch = t & 15, row_t = t >> 4;
-  const int64_t r0 = by * kTile, c = bx * kTile + ch * 8;
-  uint4 x[kSteps];
-  uint2 w[kSteps];
-  uint32_t s[kSteps];
+  const int64_t r0 = by * kTile + 32 * i0, c = bx * kTile + ch * 8;
+  uint8_t* const lds = tile + i0 * (32 * kPitch + kBlockSkew) + row_t * kPitch + ch * 16;
+  uint4 x[STEPS];
+  uint2 w[STEPS];
+  uint32_t s[STEPS];
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
+  for (int i = 0; i < STEPS; ++i) {
     const int64_t r = r0 + row_t + 32 * i;
     x[i] = make_uint4(0u, 0u, 0u, 0u);
     w[i] = make_uint2(0u, 0u);
@@ -183,11 +184,8 @@ __device__ __forceinline__ void form_tile(const SavedPackParams& p, int64_t bx, 
       }
     }
   }
-  float sum[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
+  for (int i = 0; i < STEPS; ++i) {
     float v[8];
     if constexpr (kSaved) {
       const float sc = e8m0_value((s[i] >> (8 * (ch >> 2))) & 255u);
@@ -213,9 +211,28 @@ __device__ __forceinline__ void form_tile(const SavedPackParams& p, int64_t bx, 
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum[e] = sum[e] + v[e];
     }
-    *reinterpret_cast<uint4*>(tile + row_t * kPitch + ch * 16 + i * (32 * kPitch + kBlockSkew)) =
+    *reinterpret_cast<uint4*>(lds + i * (32 * kPitch + kBlockSkew)) =
         make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                    pack_bf16x2(v[6], v[7]));
+  }
+}
+
+// Step 1 of a tile.  The tile that ends past R takes its steps one by one and
+// leaves out those that hold no row, which nothing reads: a tile of a few
+// rows then costs a quarter.
+template <int ACT, int HASX>
+__device__ __forceinline__ void form_tile(const SavedPackParams& p, int64_t bx, int64_t by, uint8_t* tile,
+                                          float (&part)[8][kTile]) {
+  const int t = threadIdx.x, ch = t & 15;
+  float sum[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
+  const int64_t rows = p.R - by * kTile;
+  if (rows >= kTile) {
+    form_steps<ACT, HASX, kSteps>(p, bx, by, 0, tile, sum);
+  } else {
+#pragma unroll 1
+    for (int i = 0; 32 * i < rows; ++i) form_steps<ACT, HASX, 1>(p, bx, by, i, tile, sum);
   }
   if (p.partials != nullptr) {
 #pragma unroll
