@@ -392,18 +392,20 @@ enum Shape {
 //    compute units one: 512 x 2048 x 2048 64x64 6.8 / 8.4 / 9.8, 128x128
 //    8.2 / 9.5 / 14.9; 128 x 4096 x 4096 64x32 7.0 / 8.2 / 9.7, 64x64
 //    8.1 / 8.9 / 10.3; 64 x 2048 x 12288 32x32 8.0 / 10.3 / 12.6, 64x32
-//    11.4 / 12.8 / 14.7.  With fewer K groups than wavefronts the 128x128
-//    tiles are faster (768 x 2048 x 224: 5.6 / 5.8 / 6.2, 64x64 4.9 / 7.5 / 7.5).
+//    11.4 / 12.8 / 14.7.  With at most three K groups the four wavefronts have
+//    too little to share and the 128x128 tiles are taken (768 x 2048 x 224,
+//    GELU: 6.5 / 7.3 / 7.1, 64x64 6.1 / 9.8 / 9.6).
 //  - beyond, 256x256 tiles or, where those would leave compute units idle,
 //    128x128 at two per unit: 8191 x 2048 x 8192 256x256 66 / 79 / 112, 128x128
 //    75 / 102 / 140; 1500 x 4096 x 4096 27 / 28 / 45 against 21 / 26 / 29.
-//    Their cost per round of the chip goes by area, 128x128 15% more.  With a
-//    checkpoint (E2M1: or an activation) in the epilogue, over several rounds,
-//    256x128 at two per unit, so that one tile's epilogue runs beside
-//    another's products -- while the sums are short, since its main loop is
-//    the slower one: 8192 x 8192 x 2048 with GELU and checkpoint 129 / 155 /
-//    198, 256x256 156 / 168 / 194; 16384 x 8192 x 4096 with GELU 329 / 448 /
-//    635 against 340 / 398 / 537.
+//    Their cost per round of the chip goes by area, 128x128 15% more.
+//  - over several rounds, with a checkpoint (E2M1: or a residual, or an
+//    activation) in the epilogue and short sums, 256x128 at two per unit: one
+//    tile's epilogue then runs beside another's products, at the price of a
+//    slower main loop.  8192 x 8192 x 2048, GELU and checkpoint 118 / 143 /
+//    193, 256x256 137 / 153 / 186; residual 142 / 178 / 203 against 156 / 170 /
+//    201; 8192 x 8192 x 4096, GELU and checkpoint 178 / 222 / 320 against
+//    183 / 212 / 276; GELU alone 165 / 207 / 300 against 162 / 190 / 255.
 int pick_shape(int fmt, const GemmActParams& p) {
   const int64_t cus = cu_count();
   if (p.M <= 16) return tile_count(p, 16, 32) >= cus ? kRows16x32 : kRows16x32Deep;
@@ -419,9 +421,11 @@ int pick_shape(int fmt, const GemmActParams& p) {
   const int64_t cost256 = (t256 + cus - 1) / cus * 65536;
   const int64_t cost128 = (t128 / (2 * cus) * 32768 + (rest == 0 ? 0 : rest <= cus ? 22000 : 32768)) * 115 / 100;
   if (cost256 > cost128) return kTile128;
-  const bool overlap = fmt == kE2M1   ? (p.saved_codes != nullptr || p.act != kActNone) && p.K <= 4096
-                       : fmt == kE2M3 ? p.saved_codes != nullptr && p.K <= 2048
-                                      : false;
+  const bool traffic = p.saved_codes != nullptr || p.residual != nullptr;
+  const int64_t longest = fmt == kE2M1   ? (traffic ? 4096 : p.act != kActNone ? 2048 : 0)
+                          : fmt == kE2M3 ? (p.saved_codes != nullptr ? 2048 : 0)
+                                         : 0;
+  const bool overlap = p.K <= longest;
   return overlap && t256 > cus ? kTile256x128 : kTile256;
 }
 

@@ -137,7 +137,11 @@ struct Cfg {
   static constexpr int kEpiBytes = EPI == kEpiSwiglu    ? BM * kZPitch
                                    : EPI == kEpiDSwiglu ? 2 * BM * kDPitch
                                                         : kWaves * kWM * kCPitch;
-  static constexpr int kSmem = (kJOff + kJunk > kEpiBytes) ? kJOff + kJunk : kEpiBytes;
+  static constexpr int kBiasAt = (kJOff + kJunk > kEpiBytes) ? kJOff + kJunk : kEpiBytes;
+  static constexpr int kSmem = kBiasAt + (EPI == kEpiAct ? BN * 4 : 0);  // kEpiAct: the tile's bias beside the ring
+  // kEpiAct: the residual's tile waits in registers while the sums run, where
+  // the accumulators leave them
+  static constexpr bool kResidualAhead = EPI == kEpiAct && kAccRegs <= 64;
   static_assert(kSmem <= kLds, "LDS budget");
 };
 
@@ -695,6 +699,32 @@ __device__ __forceinline__ void gemm_tile(const P& p, int bx, int by, int bz, ui
     pin_arg(p.q_col_scales);
     if constexpr (EPI == kEpiDSwiglu) pin_arg(p.aux);
   }
+  // kEpiAct: the epilogue's inputs, asked for before the operands so that their
+  // latency is hidden.  Unconditional loads (an `if` around them would be
+  // waited for at its end): what is not wanted is read from the output.
+  constexpr int kRowChunks = CF::kWN / 8;
+  constexpr int kAhead = CF::kResidualAhead ? CF::kWM * kRowChunks / 64 : 1;
+  [[maybe_unused]] uint4 ahead[kAhead];
+  [[maybe_unused]] uint32_t bias_word = 0;
+  if constexpr (EPI == kEpiAct) {
+    const uint8_t* const any = p.c != nullptr ? reinterpret_cast<const uint8_t*>(p.c) : p.saved_codes;
+    const int64_t n = n0 + t % BN < p.N ? n0 + t % BN : p.N - 1;
+    const uint8_t* const at = p.bias == nullptr ? any
+                              : p.bias_f32      ? reinterpret_cast<const uint8_t*>(p.bias) + 4 * n
+                                                : reinterpret_cast<const uint8_t*>(p.bias) + 2 * (n & ~(int64_t)1);
+    bias_word = *reinterpret_cast<const uint32_t*>(at);
+    if constexpr (CF::kResidualAhead) {
+      const bool wanted = p.residual != nullptr && !p.c_f32;
+      const uint8_t* const base = wanted ? reinterpret_cast<const uint8_t*>(p.residual) : any;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int q = lane + 64 * i;
+        const int64_t m = m0 + wm * CF::kWM + q / kRowChunks, c = n0 + wn * CF::kWN + 8 * (q % kRowChunks);
+        const int64_t off = (m < p.M ? m : p.M - 1) * p.ldr + (c < p.N ? c : p.N - 8);
+        ahead[i] = *reinterpret_cast<const uint4*>(base + (wanted ? 2 * off : 0));
+      }
+    }
+  }
   if (nk > 0) {  // (a ragged-K group may be empty)
     // prologue: stages 0 .. S - 2 and the first window step of stage S - 1
     // in flight; stage 0's scales and first fragments read
@@ -925,41 +955,36 @@ __device__ __forceinline__ void gemm_tile(const P& p, int bx, int by, int bz, ui
     // result there, and the tile leaves the same way.
     const int64_t mw = m0 + wm * CF::kWM, nw = n0 + wn * CF::kWN;
     uint8_t* wt = smem + wave * CF::kWM * CF::kCPitch;
-    constexpr int kRowChunks = CF::kWN / 8;
     const bool staged = p.c != nullptr && !p.c_f32;
     if (staged && p.residual != nullptr) {
       const uint16_t* R = reinterpret_cast<const uint16_t*>(p.residual);
-#pragma unroll 8
-      for (int q = lane; q < CF::kWM * kRowChunks; q += 64) {
-        const int r = q / kRowChunks, ch = q % kRowChunks;
-        if (mw + r < p.M && nw + 8 * ch < p.N) {
-          const uint4 x = *reinterpret_cast<const uint4*>(R + (mw + r) * p.ldr + nw + 8 * ch);
-          *reinterpret_cast<uint2*>(wt + r * CF::kCPitch + ch * 16) = make_uint2(x.x, x.y);
-          *reinterpret_cast<uint2*>(wt + r * CF::kCPitch + ch * 16 + 8) = make_uint2(x.z, x.w);
-        }
+#pragma unroll
+      for (int i = 0; i < CF::kWM * kRowChunks / 64; ++i) {
+        const int q = lane + 64 * i, r = q / kRowChunks, ch = q % kRowChunks;
+        uint4 x;
+        if constexpr (CF::kResidualAhead) x = ahead[i];
+        else if (mw + r < p.M && nw + 8 * ch < p.N) x = *reinterpret_cast<const uint4*>(R + (mw + r) * p.ldr + nw + 8 * ch);
+        *reinterpret_cast<uint2*>(wt + r * CF::kCPitch + ch * 16) = make_uint2(x.x, x.y);
+        *reinterpret_cast<uint2*>(wt + r * CF::kCPitch + ch * 16 + 8) = make_uint2(x.z, x.w);
       }
     }
+    float* const tile_bias = reinterpret_cast<float*>(smem + CF::kBiasAt);
+    if (t < BN) {
+      const float b = p.bias_f32 ? __uint_as_float(bias_word) : ((n0 + t) & 1) ? bf16_hi(bias_word) : bf16_lo(bias_word);
+      tile_bias[t] = p.bias != nullptr ? b : 0.0f;
+    }
+    __syncthreads();
     float bv[CF::kNJ][16];
 #pragma unroll
-    for (int j = 0; j < CF::kNJ; ++j) {
-      const int64_t nb = nw + 32 * j + 4 * g;
-      const bool in = p.bias != nullptr && nw + 32 * j < p.N;  // uniform
+    for (int j = 0; j < CF::kNJ; ++j)
 #pragma unroll
       for (int e4 = 0; e4 < 4; ++e4) {
-        float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (in && p.bias_f32) {
-          q = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p.bias) + nb + 8 * e4);
-        } else if (in) {
-          const uint2 h = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(p.bias) + nb + 8 * e4);
-          q = make_float4(bf16_lo(h.x), bf16_hi(h.x), bf16_lo(h.y), bf16_hi(h.y));
-        }
+        const float4 q = *reinterpret_cast<const float4*>(tile_bias + wn * CF::kWN + 32 * j + 8 * e4 + 4 * g);
         bv[j][4 * e4 + 0] = q.x;
         bv[j][4 * e4 + 1] = q.y;
         bv[j][4 * e4 + 2] = q.z;
         bv[j][4 * e4 + 3] = q.w;
       }
-    }
-    __syncthreads();
     auto finish = [&](auto actc) __attribute__((always_inline)) {
       constexpr int ACT = decltype(actc)::value;
 #pragma unroll

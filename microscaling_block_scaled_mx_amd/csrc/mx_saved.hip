@@ -217,9 +217,9 @@ __device__ __forceinline__ void form_steps(const SavedPackParams& p, int64_t bx,
   }
 }
 
-// Step 1 of a tile.  The tile that ends past R takes its steps one by one and
-// leaves out those that hold no row, which nothing reads: a tile of a few
-// rows then costs a quarter.
+// Step 1 of a tile.  A tile with steps that hold no row (past R; nothing reads
+// them) takes the others one by one: a tile of a few rows then costs a
+// quarter.
 template <int ACT, int HASX>
 __device__ __forceinline__ void form_tile(const SavedPackParams& p, int64_t bx, int64_t by, uint8_t* tile,
                                           float (&part)[8][kTile]) {
@@ -228,7 +228,7 @@ __device__ __forceinline__ void form_tile(const SavedPackParams& p, int64_t bx, 
 #pragma unroll
   for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
   const int64_t rows = p.R - by * kTile;
-  if (rows >= kTile) {
+  if (rows > kTile - 32) {  // all steps
     form_steps<ACT, HASX, kSteps>(p, bx, by, 0, tile, sum);
   } else {
 #pragma unroll 1
