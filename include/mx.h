@@ -564,8 +564,10 @@ typedef enum { MX_ACT_NONE = 0, MX_ACT_GELU_TANH = 1, MX_ACT_SILU = 2 } mx_act;
  * Errors: MX_ERR_NULL, MX_ERR_SHAPE, MX_ERR_ALIGN, MX_ERR_FORMAT,
  * MX_ERR_INDEX_OVERFLOW, MX_ERR_DEVICE, MX_ERR_LAUNCH.  M = 0 or N = 0
  * enqueues nothing (pointers may then be NULL, and A and B may be where
- * K = 0).  The accumulation order depends on M, N and whether a checkpoint
- * is asked for, never on timing.
+ * K = 0).  The accumulation order depends on the sizes, fmt and which inputs
+ * and outputs there are, never on timing.  E2M1 and E2M3 products are summed
+ * to binary32 accuracy; the matrix cores align E4M3 products before adding
+ * them, which leaves about 1.5e-5 of the result's norm (measured).
  */
 typedef struct {
   int64_t M, N, K;
@@ -666,8 +668,10 @@ int mx_quantize_saved(const mx_quantize_saved_args* args, void* stream);
  *  db           binary32 [N] with db_partials [ceil(M/128)][N], or NULL.
  *  dPr, dPc, Xc work operands of fmt: [M] x K=N (for dX); [N] and [K] x K = M
  *               rounded up to 32 (for dW).
- * M = 0 sets dW (unless accumulating) and db to zero.  Errors: as the
- * calls it is made of; nothing is enqueued on an error.
+ * M = 0 sets dW (unless accumulating) and db to zero.  No output or work
+ * buffer may overlap another or an input; calls that share work buffers must
+ * be ordered (same stream).  Errors: as the calls it is made of; nothing is
+ * enqueued on an error.
  */
 typedef struct {
   int64_t M, N, K;
