@@ -45,7 +45,7 @@ METRIC = "MX GEMM TFLOP/s and % of MXFP4/6/8 MFMA peak (Flux-12B shapes); quanti
 # sources are those the counters were taken with
 GEMM_TRAFFIC = {"bytes_per_launch": 236.8e6,
                 "sources": ("mx_gemm.hip", "mx_gemm_tile.h", "mx_device.h", "mx_kernels.h", "mx_tuned.inc"),
-                "sources_sha1": "06d34645206d0fa0f5620c26592c480785081df0"}
+                "sources_sha1": "fc88dbb7f2aa789347c912b9d1ec3cc9bb34633b"}
 # VALU wavefront-instructions per launch of the fused pack (rocprofv3
 # SQ_INSTS_VALU), valid while the pack sources are those it was counted with
 PACK_VALU = {"instructions_per_launch": 1.028e7, "sources": ("mx_pack.hip", "mx_device.h", "mx_kernels.h"),

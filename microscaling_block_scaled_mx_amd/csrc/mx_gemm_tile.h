@@ -23,6 +23,10 @@
 // the start of its last step, so that the next stage's first operands are
 // read while the current stage's last MFMAs run.
 
+// The epilogue kEpiAct (GemmActParams) adds a bias, applies an activation,
+// writes the 8-bit checkpoint of the pre-activation and adds a residual, for
+// any number of rows.
+
 // Dense tiles are ordered for cache reuse: workgroups are dealt round-robin
 // to the 8 XCDs (each with its own L2), so consecutive workgroup ids are
 // remapped to give every XCD a contiguous range of tiles, and each range is
