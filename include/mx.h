@@ -670,8 +670,8 @@ int mx_quantize_saved(const mx_quantize_saved_args* args, void* stream);
  *               rounded up to 32 (for dW).
  * M = 0 sets dW (unless accumulating) and db to zero.  No output or work
  * buffer may overlap another or an input; calls that share work buffers must
- * be ordered (same stream).  Errors: as the calls it is made of; nothing is
- * enqueued on an error.
+ * be ordered (same stream).  Errors: as the calls it is made of; every argument
+ * is checked before anything is enqueued.
  */
 typedef struct {
   int64_t M, N, K;

@@ -367,9 +367,9 @@ hipError_t launch_two_products(F kernel, int threads, int bm, int bn, const Gemm
   return hipGetLastError();
 }
 
-// PAIRS: whether two products may share a launch of this variant (kernels
-// that no pair takes are not built).
-template <int FMT, int BM, int BN, int OCC, bool PAIRS = true>
+// PAIRS: whether the variant is built for two products, or for one and column
+// sums (takes_two).
+template <int FMT, int BM, int BN, int OCC, bool PAIRS>
 hipError_t launch_tiles(const GemmActParams& p, const Second* more, hipStream_t stream) {
   constexpr int kThreads = Cfg<FMT, BM, BN, kDense, kEpiAct, OCC>::kThreads;
   if (!more) return launch_one_product(gemm_act_kernel<FMT, BM, BN, OCC, 1>, kThreads, BM, BN, p, stream);
@@ -387,6 +387,12 @@ hipError_t launch_rows(const GemmActParams& p, const Second* more, hipStream_t s
 enum Shape {
   kRows16x32, kRows16x32Deep, kRows32x32, kRows32x32Deep, kRows64x32, kRows64x64, kTile128, kTile256x128, kTile256
 };
+
+// Whether a launch of the variant can take a second product or column sums.
+// 256x128 cannot: of a layer's two products only the weight gradient ever
+// takes it (the other has no epilogue inputs), so no pair shares it, and the
+// column sums go beside the other product.
+constexpr bool takes_two(int shape) { return shape != kTile256x128; }
 
 // Which one (times in us, measured with one variant after the other on the
 // same operands; E2M1 / E2M3 / E4M3):
@@ -445,11 +451,11 @@ hipError_t launch_shape(const GemmActParams& p, const Second* more, int shape, h
     case kRows32x32Deep: return launch_rows<FMT, 2, 2, 8, 2>(p, more, stream);
     case kRows64x32: return launch_rows<FMT, 4, 2, 4, 2>(p, more, stream);
     case kRows64x64: return launch_rows<FMT, 4, 4, 4, 2>(p, more, stream);
-    case kTile128: return launch_tiles<FMT, 128, 128, 2>(p, more, stream);
+    case kTile128: return launch_tiles<FMT, 128, 128, 2, takes_two(kTile128)>(p, more, stream);
     case kTile256x128:
-      if constexpr (FMT != kE4M3) return launch_tiles<FMT, 256, 128, 2, false>(p, more, stream);
+      if constexpr (FMT != kE4M3) return launch_tiles<FMT, 256, 128, 2, takes_two(kTile256x128)>(p, more, stream);
       else return hipErrorInvalidValue;
-    case kTile256: return launch_tiles<FMT, 256, 256, 1>(p, more, stream);
+    case kTile256: return launch_tiles<FMT, 256, 256, 1, takes_two(kTile256)>(p, more, stream);
     default: return hipErrorInvalidValue;
   }
 }
@@ -471,7 +477,7 @@ hipError_t launch_fmt(int fmt, const GemmActParams& p, const Second* more, int s
 // launches.
 int pair_shape(int fmt, const GemmActParams& p, const GemmActParams& q) {
   const int a = pick_shape(fmt, p), b = pick_shape(fmt, q);
-  if (a == b) return a;
+  if (a == b) return takes_two(a) ? a : -1;
   const int large = a > b ? a : b;
   const int64_t groups = ((a > b ? q : p).K + 127) / 128;
   if (large < kTile128) return groups <= 48 ? large : -1;
@@ -492,20 +498,23 @@ hipError_t launch_gemm_act_pair(const GemmActParams& p, const GemmActParams& q, 
                                 hipStream_t stream) {
   if (q.K > p.K) return launch_gemm_act_pair(q, p, sums, fmt, stream);
   const bool both = p.M > 0 && p.N > 0 && q.M > 0 && q.N > 0;
-  const int shape = both ? pair_shape(fmt, p, q) : -1;
+  const int shared = both ? pair_shape(fmt, p, q) : -1;
   const Second more = {q, sums};
-  if (shape >= 0) return launch_fmt(fmt, p, &more, shape, stream);
-  // two launches, the column sums with the first
-  GemmActParams none = q;
-  none.M = 0;
-  const Second only_sums = {none, sums};
-  const bool carry = p.M > 0 && p.N > 0;
-  hipError_t e = hipSuccess;
-  if (carry)
-    e = launch_fmt(fmt, p, sums.out ? &only_sums : nullptr, pick_shape(fmt, p), stream);
-  else if (sums.out && sums.cols > 0)
-    e = launch_colsum_finish(sums.partials, sums.rows, sums.cols, sums.out, 1, stream);
-  return e == hipSuccess ? launch_gemm_act(q, fmt, stream) : e;
+  if (shared >= 0) return launch_fmt(fmt, p, &more, shared, stream);
+  // a launch each, the column sums beside the first one that can take them
+  bool summing = sums.out != nullptr && sums.cols > 0;
+  for (const GemmActParams* x : {&p, &q}) {
+    if (x->M == 0 || x->N == 0) continue;
+    const int shape = pick_shape(fmt, *x);
+    const bool carries = summing && takes_two(shape);
+    GemmActParams none = *x;
+    none.M = 0;
+    const Second only_sums = {none, sums};
+    const hipError_t e = launch_fmt(fmt, *x, carries ? &only_sums : nullptr, shape, stream);
+    if (e != hipSuccess) return e;
+    if (carries) summing = false;
+  }
+  return summing ? launch_colsum_finish(sums.partials, sums.rows, sums.cols, sums.out, 1, stream) : hipSuccess;
 }
 
 }  // namespace mx

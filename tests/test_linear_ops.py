@@ -783,3 +783,38 @@ def test_checkpoint_offsets_past_32_bits():
     mx.checkpoint_load(small, want)
     torch.cuda.synchronize()
     assert torch.equal(x[:64], want) and torch.equal(x[-64:], want) and not x[64:-64].any()
+
+
+@gpu
+@pytest.mark.parametrize("fmt,mode,had", FMTS)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,N,K", [(4096, 2048, 16384), (2100, 1952, 16352), (520, 4096, 2080)])
+def test_accumulating_backward_with_every_output_is_its_parts(M, N, K, dtype, fmt, mode, had):
+    """dX, dW added into its main_grad, and db in one call, against the separate calls.  The first two sizes give the
+    MXFP4 weight gradient 256 x 128 tiles and the longer sums.  Where the products share a launch of unlike variants
+    the sums' order may differ, so those agree to REL; packs and db are bit for bit."""
+    g = torch.Generator(device="cuda").manual_seed(M + N + K + fmt)
+    t = lambda *s: torch.randn(s, generator=g, device="cuda")
+    dY, cx, cp = t(M, N).bfloat16(), mx.alloc_packed(M, K, mx.E4M3), mx.alloc_packed(M, N, mx.E4M3)
+    mx.checkpoint_save(t(M, K), cx)
+    mx.checkpoint_save(t(M, N), cp)
+    Wc = mx.alloc_packed(K, N, fmt)
+    q = dict(fmt=fmt, scale_mode=mode, hadamard=had)
+    mx.quantize_saved(K, N, x=t(K, N).bfloat16(), row=Wc, **q)
+    old = (t(N, K) * 8).to(dtype)
+    dX, dW, db = torch.empty(M, K, dtype=torch.bfloat16, device="cuda"), old.clone(), torch.empty(N, device="cuda")
+    w, v = bwd_work(M, N, K, fmt), bwd_work(M, N, K, fmt)
+    mx.linear_bwd_saved(M, N, K, dY, cx, Wc, act=mx.ACT_GELU_TANH, saved_pre=cp, dX=dX, dW=dW, db=db, accumulate=True, **q, **w)
+    dX2, dW2, db2 = torch.empty_like(dX), old.clone(), torch.empty_like(db)
+    mx.quantize_saved(M, N, act=mx.ACT_GELU_TANH, x=dY, saved=cp, row=v["dPr"], col=v["dPc"], colsum_partials=v["db_partials"],
+                      colsum=db2, **q)
+    mx.quantize_saved(M, K, saved=cx, col=v["Xc"], **q)
+    mx.gemm_act(v["dPr"], Wc, M, K, N, fmt, dX2)
+    mx.gemm_act(v["dPc"], v["Xc"], N, K, (M + 31) // 32 * 32, fmt, dW2, residual=dW2)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for k in ("dPr", "dPc", "Xc") for x, y in zip(w[k], v[k]))
+    assert torch.equal(db, db2)
+    for got, want, grad in ((dX, dX2, dX2.double()), (dW, dW2, dW2.double() - old.double())):
+        step = 2.0 ** -7 if got.dtype == torch.bfloat16 else 2.0 ** -23  # two roundings, half a step each
+        assert ((got.double() - want.double()).abs() <= REL * grad.abs().max() + step * want.double().abs()).all()
+    assert not torch.equal(dW, old)
