@@ -419,6 +419,11 @@ constexpr bool takes_two(int shape) { return shape != kTile256x128; }
 //    193, 256x256 137 / 153 / 186; residual 142 / 178 / 203 against 156 / 170 /
 //    201; 8192 x 8192 x 4096, GELU and checkpoint 178 / 222 / 320 against
 //    183 / 212 / 276; GELU alone 165 / 207 / 300 against 162 / 190 / 255.
+//    overlap_k is the longest K that takes them, -1 where none does (an empty
+//    sum is no shorter than that).
+constexpr int64_t overlap_k(int fmt, bool saved, bool residual, bool act) {
+  return fmt == kE2M1 ? (saved || residual ? 4096 : act ? 2048 : -1) : fmt == kE2M3 && saved ? 2048 : -1;
+}
 int pick_shape(int fmt, const GemmActParams& p) {
   const int64_t cus = cu_count();
   if (p.M <= 16) return tile_count(p, 16, 32) >= cus ? kRows16x32 : kRows16x32Deep;
@@ -434,12 +439,8 @@ int pick_shape(int fmt, const GemmActParams& p) {
   const int64_t cost256 = (t256 + cus - 1) / cus * 65536;
   const int64_t cost128 = (t128 / (2 * cus) * 32768 + (rest == 0 ? 0 : rest <= cus ? 22000 : 32768)) * 115 / 100;
   if (cost256 > cost128) return kTile128;
-  const bool traffic = p.saved_codes != nullptr || p.residual != nullptr;
-  const int64_t longest = fmt == kE2M1   ? (traffic ? 4096 : p.act != kActNone ? 2048 : 0)
-                          : fmt == kE2M3 ? (p.saved_codes != nullptr ? 2048 : 0)
-                                         : 0;
-  const bool overlap = p.K <= longest;
-  return overlap && t256 > cus ? kTile256x128 : kTile256;
+  const int64_t longest = overlap_k(fmt, p.saved_codes != nullptr, p.residual != nullptr, p.act != kActNone);
+  return p.K <= longest && t256 > cus ? kTile256x128 : kTile256;
 }
 
 template <int FMT>
@@ -453,8 +454,9 @@ hipError_t launch_shape(const GemmActParams& p, const Second* more, int shape, h
     case kRows64x64: return launch_rows<FMT, 4, 4, 4, 2>(p, more, stream);
     case kTile128: return launch_tiles<FMT, 128, 128, 2, takes_two(kTile128)>(p, more, stream);
     case kTile256x128:
-      if constexpr (FMT != kE4M3) return launch_tiles<FMT, 256, 128, 2, takes_two(kTile256x128)>(p, more, stream);
-      else return hipErrorInvalidValue;
+      if constexpr (overlap_k(FMT, true, true, true) >= 0)
+        return launch_tiles<FMT, 256, 128, 2, takes_two(kTile256x128)>(p, more, stream);
+      return hipErrorInvalidValue;
     case kTile256: return launch_tiles<FMT, 256, 256, 1, takes_two(kTile256)>(p, more, stream);
     default: return hipErrorInvalidValue;
   }

@@ -818,3 +818,99 @@ def test_accumulating_backward_with_every_output_is_its_parts(M, N, K, dtype, fm
         step = 2.0 ** -7 if got.dtype == torch.bfloat16 else 2.0 ** -23  # two roundings, half a step each
         assert ((got.double() - want.double()).abs() <= REL * grad.abs().max() + step * want.double().abs()).all()
     assert not torch.equal(dW, old)
+
+
+@gpu
+@pytest.mark.parametrize("fmt,mode,had", FMTS)
+@pytest.mark.parametrize("M,N", [(8192, 8192), (4096, 12288), (1500, 4096), (30, 96)])
+def test_empty_sums_at_every_tile_size(M, N, fmt, mode, had):
+    """K = 0 is act(bias) + residual, and a backward pass without tokens zeroes dW (N = 0: dX), whatever variant serves it."""
+    c = torch.full((M, N), 9.0, dtype=torch.bfloat16, device="cuda")
+    mx.gemm_act(None, None, M, N, 0, fmt, c)
+    torch.cuda.synchronize()
+    assert not c.any()
+    bias = torch.arange(N, device="cuda").float() % 64 - 32
+    for residual in (None, c):
+        c.fill_(3.0)
+        saved = mx.alloc_packed(M, N, mx.E4M3)
+        mx.gemm_act(None, None, M, N, 0, fmt, c, bias=bias, residual=residual, saved=saved)
+        torch.cuda.synchronize()
+        want = bias + (0 if residual is None else 3)  # small integers: exact
+        assert torch.equal(c.float(), want.expand(M, N))
+        mx.checkpoint_load(saved, c)
+        ref = mx.alloc_packed(1, N, mx.E4M3)
+        mx.checkpoint_save(bias.reshape(1, N), ref)
+        row = torch.empty(1, N, dtype=torch.bfloat16, device="cuda")
+        mx.checkpoint_load(ref, row)
+        torch.cuda.synchronize()
+        assert torch.equal(c, row.expand(M, N))
+    O = (M + 31) // 32 * 32  # (an output width)
+    dW, db = torch.full((O, N), 5.0, device="cuda"), torch.full((O,), 5.0, device="cuda")
+    e = lambda rows, k, f=fmt: mx.alloc_packed(rows, k, f)
+    y = torch.empty(0, O, dtype=torch.bfloat16, device="cuda")
+    kw = dict(fmt=fmt, scale_mode=mode, hadamard=had)
+    for accumulate in (True, False):
+        db.fill_(5.0)
+        mx.linear_bwd_saved(0, O, N, y, e(0, N, mx.E4M3), e(N, O), dX=torch.empty(0, N, dtype=torch.bfloat16, device="cuda"), dW=dW,
+                            db=db, dPr=e(0, O), dPc=e(O, 0), Xc=e(N, 0), db_partials=torch.empty(0, O, device="cuda"),
+                            accumulate=accumulate, **kw)
+        torch.cuda.synchronize()
+        assert (dW == (5 if accumulate else 0)).all() and not db.any()
+    dX = torch.full((M, N), 5.0, dtype=torch.bfloat16, device="cuda")
+    mx.linear_bwd_saved(M, 0, N, torch.empty(M, 0, dtype=torch.bfloat16, device="cuda"), None, None, dX=dX, dPr=None, **kw)
+    torch.cuda.synchronize()
+    assert not dX.any()
+
+
+@gpu
+@pytest.mark.parametrize("fmt,mode,had", FMTS)
+def test_every_size_and_choice_of_outputs_reaches_a_kernel(fmt, mode, had):
+    """Sizes over the whole range, every epilogue and every choice of outputs: each call is served.  (Zero operands, so
+    that the outputs have to be bias, residual or zero.)"""
+    rng = np.random.default_rng(fmt)
+    big = 8192 * 8192
+    room = {k: torch.zeros(big * b, dtype=torch.uint8, device="cuda") for k, b in
+            dict(a=1, as_=1, b=1, bs=1, x=1, xs=1, p=1, ps=1, c=1, cs=1, r=1, rs=1).items()}
+    out, add, g2 = (torch.zeros(big, dtype=torch.float32, device="cuda") for _ in range(3))
+    bf = torch.zeros(2, big, dtype=torch.bfloat16, device="cuda")
+
+    def operand_of(name, rows, k, f):
+        n, b = (k + 127) // 128 * rows * 4, mx.BITS[f] * 4
+        return room[name][:n * b], room[name + ("s" if name != "a" else "s_")][:n]
+
+    size = lambda top: int(round(np.exp(rng.uniform(0, np.log(top)))))
+    for _ in range(120):
+        M, N, K = size(8192), 32 * size(256), 32 * size(256)
+        if rng.random() < 0.15:
+            K = 0
+        act, flags = int(rng.integers(3)), rng.random(4) < 0.5
+        f32 = bool(flags[0])
+        store = out if f32 else bf[0]
+        c = store[:M * N].fill_(9.0).reshape(M, N)
+        res = (add if f32 else bf[1])[:M * N].reshape(M, N) if flags[1] else None
+        mx.gemm_act(operand_of("a", M, K, fmt), operand_of("b", N, K, fmt), M, N, K, fmt, c, act=act, residual=res,
+                    saved=operand_of("x", M, N, mx.E4M3) if flags[2] else None)
+        assert not c.any(), (M, N, K, act, flags)
+        room["x"][:((N + 127) // 128) * M * 128].zero_()
+        room["xs"][:((N + 127) // 128) * M * 4].zero_()
+
+        want = rng.random(3) < 0.7
+        if not want.any():
+            want[:] = True
+        N, K = max(32, N), max(32, K)
+        Mp = (M + 31) // 32 * 32
+        acc = bool(rng.random() < 0.5)
+        dW = (g2 if f32 else bf[1])[:N * K].fill_(1.0).reshape(N, K)
+        dX = bf[0][:M * K].fill_(9.0).reshape(M, K)
+        db, part = torch.full((N,), 9.0, device="cuda"), out[:(M + 127) // 128 * N].reshape(-1, N)
+        dY = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+        mx.linear_bwd_saved(M, N, K, dY, operand_of("x", M, K, mx.E4M3), operand_of("b", K, N, fmt), fmt, mode, had, act=act,
+                            saved_pre=operand_of("a", M, N, mx.E4M3) if act else None, dX=dX if want[0] else None,
+                            dW=dW if want[1] else None, db=db if want[2] else None, db_partials=part,
+                            dPr=operand_of("p", M, N, fmt), dPc=operand_of("c", N, Mp, fmt), Xc=operand_of("r", K, Mp, fmt),
+                            accumulate=acc)
+        case = (M, N, K, act, f32, want, acc)
+        assert (dX == (0 if want[0] else 9)).all() and (db == (0 if want[2] else 9)).all(), case
+        assert (dW == (1 if acc or not want[1] else 0)).all(), case
+        bf[1].zero_()
+        room["a"].zero_(), room["as_"].zero_()
