@@ -69,10 +69,10 @@ __device__ __forceinline__ float act_slope(float x) {
 #endif
 }
 
-// 2^(byte - 127) of an E8M0 scale; 0 gives 2^-127 (a subnormal), 0xff gives
-// +inf, so that the zero codes of a NaN block decode to NaN.
+// 2^(byte - 127) of an E8M0 scale; 0 gives 2^-127 (a subnormal), 0xff NaN, so
+// that every code of a NaN block decodes to NaN.
 __device__ __forceinline__ float e8m0_value(uint32_t byte) {
-  return __uint_as_float(byte == 0u ? 0x00400000u : byte << 23);
+  return __uint_as_float(byte == 0u ? 0x00400000u : byte == 0xffu ? 0x7fc00000u : byte << 23);
 }
 
 // Four E4M3 codes (one dword) times a scale.

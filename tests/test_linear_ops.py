@@ -914,3 +914,30 @@ def test_every_size_and_choice_of_outputs_reaches_a_kernel(fmt, mode, had):
         assert (dW == (1 if acc or not want[1] else 0)).all(), case
         bf[1].zero_()
         room["a"].zero_(), room["as_"].zero_()
+
+
+@gpu
+def test_a_nan_scale_is_nan_whatever_the_codes():
+    """Operands packed elsewhere may hold any codes under the scale byte 0xff: zeros, numbers of either sign, NaN codes."""
+    R, C = 40, 128
+    codes = torch.arange(R * C, dtype=torch.int64, device="cuda").remainder(256).to(torch.uint8).reshape(1, R, C)
+    scales = torch.full((1, R, 4), 127, dtype=torch.uint8, device="cuda")
+    scales[0, 5:33, 2] = 255
+    bad = torch.zeros(R, C, dtype=torch.bool, device="cuda")
+    bad[5:33, 64:96] = True
+    bad |= (codes[0] & 0x7F) == 0x7F
+    for dtype in (torch.float32, torch.bfloat16):
+        y = torch.empty(R, C, dtype=dtype, device="cuda")
+        mx.checkpoint_load((codes, scales), y)
+        torch.cuda.synchronize()
+        assert torch.equal(y.isnan(), bad) and not y.isinf().any()
+    ones = torch.ones(R, C, dtype=torch.bfloat16, device="cuda")
+    for act in ACTS:
+        for x in (None, ones) if act else (None,):
+            row, total = mx.alloc_packed(R, C, mx.E4M3), torch.empty(C, device="cuda")
+            part = torch.empty(1, C, device="cuda")
+            mx.quantize_saved(R, C, mx.E4M3, mx.RCEIL, act=act, x=x, saved=(codes, scales), row=row, colsum_partials=part,
+                              colsum=total)
+            torch.cuda.synchronize()
+            assert torch.equal(total.isnan(), bad.any(0)) and not total.isinf().any()
+            assert torch.equal(row[1][0] == 255, bad.reshape(R, 4, 32).any(-1))
