@@ -588,9 +588,10 @@ int mx_gemm_act(const mx_gemm_act_args* args, void* stream);
  * mx_checkpoint_save -- x [R][ldx] (x_dtype) to its 8-bit checkpoint, the
  * rowwise MXFP8 operand [R] x K=C (E4M3, RCEIL scales; for bf16 the bytes
  * mx_quantize writes).  8.25 bits a value; also the A operand of an MXFP8
- * mx_gemm_act at any row count.  A value is off by at most 2^-4 of itself,
- * or 2^-18 of its block's largest value where that is more; a block
- * holding a NaN or Inf reads back as NaN throughout.
+ * mx_gemm_act at any row count.  A value is off by at most 2^-4 of itself
+ * or, where that is more, 2^-10 of the block's scale: less than 2^-17 of the
+ * block's largest value, or 2^-137 where that is under 2^-119 (the least scale
+ * is 2^-127).  A block holding a NaN or Inf reads back as NaN throughout.
  *
  * mx_checkpoint_load -- the values that a checkpoint stands for, into
  * y [R][ldy] (y_dtype); exact but for bf16 subnormals.  Reads any E4M3

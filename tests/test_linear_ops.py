@@ -941,3 +941,26 @@ def test_a_nan_scale_is_nan_whatever_the_codes():
             torch.cuda.synchronize()
             assert torch.equal(total.isnan(), bad.any(0)) and not total.isinf().any()
             assert torch.equal(row[1][0] == 255, bad.reshape(R, 4, 32).any(-1))
+
+
+@gpu
+def test_checkpoint_error_bound_at_its_edges():
+    """Half an E4M3 step: 2^-4 of a value, and below the format's normal range 2^-10 of the scale 2^X, with the block's
+    largest value in (224, 448] 2^X: 2^-10 / 224 < 2^-17 of it, or 2^-137 at the least scale 2^-127."""
+    rng = np.random.default_rng(2)
+    R, C = 64, 256
+    x = rng.standard_normal((R, C // 32, 32)) * 2.0 ** rng.integers(-12, 1, (R, C // 32, 32))
+    x /= np.abs(x).max(-1, keepdims=True)
+    x[..., 0] = 1                                                     # the block's largest
+    x[::2, :, 1:8] = 2.0 ** -10 / 225 * np.linspace(0.9, 0.9999, 7)   # just under half the least step
+    top = rng.choice([225.0, 224.125, 448.0, 300.0, 2.0 ** 100, 2.0 ** -100, 225 * 2.0 ** -127, 2.0 ** -121, 2.0 ** -130], (R, C // 32, 1))
+    x = (x * top).reshape(R, C).astype(np.float32)
+    p, y = mx.alloc_packed(R, C, mx.E4M3), torch.empty(R, C, device="cuda")
+    mx.checkpoint_save(torch.from_numpy(x).cuda(), p)
+    mx.checkpoint_load(p, y)
+    v, err = np.abs(x.astype(np.float64)), np.abs(f64(y) - x.astype(np.float64))
+    largest = v.reshape(R, -1, 32).max(-1, keepdims=True).repeat(32, -1).reshape(R, C)
+    bound = np.where(largest < 2.0 ** -119, 2.0 ** -137, 2.0 ** -10 / 224 * largest)
+    assert (err <= np.maximum(2.0 ** -4 * v, bound)).all()
+    assert (2.0 ** -10 / 224 * largest < 2.0 ** -17 * largest).all()
+    assert (err[::2][largest[::2] == 225] > 2.0 ** -18 * 225).any()   # no smaller power of two would do
