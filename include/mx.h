@@ -535,7 +535,10 @@ int mx_grouped_gemm(const mx_grouped_args* args, void* stream);
 /* Activations of the linear operators:
  *  GELU_TANH  x s(z), z = 2 sqrt(2/pi) (x + 0.044715 x^3);  SILU  x s(x);
  *  s(z) = 1/(1+exp(-z)).  Evaluated in binary32 with the hardware's exp2 and
- *  reciprocal: within a few ulps, not the bit-exact contract of mx_prologue. */
+ *  reciprocal, not the bit-exact contract of mx_prologue.  z log2(e) is
+ *  rounded before exp2, so the error grows with |z|: act is within
+ *  (4 |z| + 6) 2^-24 of itself, or 2^-126 |x| where s(z) is below the least
+ *  normal number; act' is within 2^-17. */
 typedef enum { MX_ACT_NONE = 0, MX_ACT_GELU_TANH = 1, MX_ACT_SILU = 2 } mx_act;
 
 /*

@@ -8,7 +8,11 @@
 //   act'(x) = s + x z'(x) s (1 - s).
 // exp2 and the reciprocal are the hardware's (each within 1 ulp), not the
 // packers' bit-exact contract (mx_device.h), which takes several times the
-// instructions; both are rounded to bf16, or to a checkpoint, once.
+// instructions.  The exponent carries at most four roundings, an error of
+// 4 |z| 2^-24 in exp(-z); the exponential, the sum, the reciprocal and the last
+// product add 6 2^-24: act is within (4 |z| + 6) 2^-24 of itself.  In act' the
+// largest error is the 2 2^-24 of s where it is next to 1, times x z' (33 for
+// GELU at z = 17): under 2^-17.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -964,3 +964,30 @@ def test_checkpoint_error_bound_at_its_edges():
     assert (err <= np.maximum(2.0 ** -4 * v, bound)).all()
     assert (2.0 ** -10 / 224 * largest < 2.0 ** -17 * largest).all()
     assert (err[::2][largest[::2] == 225] > 2.0 ** -18 * 225).any()   # no smaller power of two would do
+
+
+@gpu
+@pytest.mark.parametrize("act", [mx.ACT_GELU_TANH, mx.ACT_SILU])
+def test_activation_and_slope_error_bounds(act):
+    """The header's bounds, z to +-120: act to (4 |z| + 6) 2^-24 of itself or 2^-126 |x|, act' to 2^-17.
+
+    act: x^2 and the constants (GELU: A + B x^2 to 2.6 u, u = 2^-24; SiLU: 0.7 u), two products at most: 3.6 u of z, then
+    exp2 2 u, 1 + e u, the reciprocal 2 u, x s u.  Where 1 + e is past 2^126 its reciprocal may be flushed to 0: 2^-126 |x|.
+    act': s + x z' s (1 - s); s next to 1 is off by 2 u at most and x z' <= 33 there, elsewhere the product is smaller."""
+    top = 11.2 if act == mx.ACT_GELU_TANH else 120.0
+    x = np.linspace(-top, top, 8192).astype(np.float32)
+    x64 = x.astype(np.float64)
+    z = 2 * K0 * (x64 + K1 * x64 ** 3) if act == mx.ACT_GELU_TANH else x64
+    want = act64(x64, act)
+    for M in (1, 9600):  # the few-rows kernel and the tiles
+        c = torch.empty(M, 8192, device="cuda")
+        mx.gemm_act(None, None, M, 8192, 0, mx.E2M3, c, act=act, bias=torch.from_numpy(x).cuda())
+        assert (np.abs(f64(c[-1]) - want) <= (4 * np.abs(z) + 6) * 2.0 ** -24 * np.abs(want) + 2.0 ** -126 * np.abs(x64)).all()
+    ck = mx.alloc_packed(1, 8192, mx.E4M3)
+    t = np.exp2(np.linspace(-10, np.log2(top), 8192)) * np.where(np.arange(8192) % 2, -1, 1)  # both signs, by magnitude
+    mx.checkpoint_save(torch.from_numpy(t.astype(np.float32).reshape(1, -1)).cuda(), ck)
+    s = decode(ck, 1, 8192, mx.E4M3)[0]
+    part, slope = torch.empty(1, 8192, device="cuda"), torch.empty(8192, device="cuda")
+    mx.quantize_saved(1, 8192, mx.E4M3, mx.RCEIL, act=act, x=torch.ones(1, 8192, dtype=torch.bfloat16, device="cuda"), saved=ck,
+                      colsum_partials=part, colsum=slope)
+    assert np.abs(f64(slope) - slope64(s, act)).max() <= 2.0 ** -17
