@@ -604,8 +604,8 @@ int mx_gemm_act(const mx_gemm_act_args* args, void* stream);
  *  C            a multiple of 32.
  *  ldx, ldy     row pitches in elements, >= C, multiples of 8.
  * Errors: MX_ERR_NULL, MX_ERR_SHAPE, MX_ERR_ALIGN, MX_ERR_FORMAT (dtype),
- * MX_ERR_INDEX_OVERFLOW (more than 2^31 workgroups), MX_ERR_DEVICE,
- * MX_ERR_LAUNCH.
+ * MX_ERR_INDEX_OVERFLOW (2^24 or more tiles of 64 x 128 values),
+ * MX_ERR_DEVICE, MX_ERR_LAUNCH.
  */
 int mx_checkpoint_save(const void* x, int x_dtype, int64_t R, int64_t C, int64_t ldx, void* codes, void* scales,
                        void* stream);
@@ -631,7 +631,8 @@ int mx_checkpoint_load(const void* codes, const void* scales, int64_t R, int64_t
  *               of the binary32 values before their rounding to bf16.
  *  colsum       binary32 [C]: the partials summed in order (zeros if R = 0).
  *               Requires colsum_partials.
- * At least one of row, col and colsum_partials.  Errors as mx_quantize.
+ * At least one of row, col and colsum_partials.  Errors as mx_quantize
+ * (MX_ERR_INDEX_OVERFLOW for 2^23 or more tiles of 128 x 128 values).
  */
 typedef struct {
   int64_t R, C;

@@ -219,6 +219,9 @@ int64_t up32(int64_t n) { return (n + 31) / 32 * 32; }
 constexpr int64_t kMaxExtent = 1ll << 40;
 // row pitch of a tensor with C columns: in 8-element steps
 bool pitch_ok(int64_t ld, int64_t C) { return ld >= C && ld % 8 == 0; }
+// gx * gy workgroups of `threads` make fewer than 2^32 threads, the most one
+// launch may have
+bool threads_fit(int64_t gx, int64_t gy, int64_t threads) { return gx == 0 || gy <= ((1ll << 32) - 1) / threads / gx; }
 // the byte offset of a row fits 64 bits with room to spare
 bool rows_fit(int64_t R, int64_t ld) { return R <= kMaxExtent && ld <= (1ll << 60) / (R > 0 ? R : 1); }
 
@@ -284,8 +287,7 @@ int validate_checkpoint(const void* x, int dtype, int64_t R, int64_t C, int64_t 
   const void* ptrs[] = {x, codes, scales};
   for (const void* q : ptrs)
     if (q && !aligned16(q)) return MX_ERR_ALIGN;
-  const int64_t gx = (C + 127) / 128, gy = (R + 63) / 64;
-  if (gx > 0 && gy >= ((1ll << 31) + gx - 1) / gx) return MX_ERR_INDEX_OVERFLOW;
+  if (!threads_fit((C + 127) / 128, (R + 63) / 64, 256)) return MX_ERR_INDEX_OVERFLOW;
   if (R > 0 && C > 0 && (!x || !codes || !scales)) return MX_ERR_NULL;
   return MX_OK;
 }
@@ -303,8 +305,7 @@ int validate_quantize_saved(const mx_quantize_saved_args& a) {
                         a.col.codes, a.col.scales, a.colsum_partials, a.colsum};
   for (const void* q : ptrs)
     if (q && !aligned16(q)) return MX_ERR_ALIGN;
-  const int64_t gx = (a.C + 127) / 128, gy = (a.R + 127) / 128;
-  if (gx > 0 && gy >= ((1ll << 31) + gx - 1) / gx) return MX_ERR_INDEX_OVERFLOW;
+  if (!threads_fit((a.C + 127) / 128, (a.R + 127) / 128, 512)) return MX_ERR_INDEX_OVERFLOW;
   if (a.R == 0 || a.C == 0) return MX_OK;
   if (a.x && a.act == MX_ACT_NONE && packed_ok(a.saved)) return MX_ERR_FORMAT;
   if ((!a.x || a.act != MX_ACT_NONE) && packed_none(a.saved)) return MX_ERR_NULL;

@@ -343,11 +343,12 @@ int64_t pack_tiles(const SavedPackParams& p) {
   return ((p.C + kTile - 1) / kTile) * ((p.R + kTile - 1) / kTile);
 }
 
-// Workgroups of a save / load launch, or -1 if they do not fit a grid.
+// Workgroups of a save / load launch, or -1 for 2^32 threads or more (the
+// runtime's limit; also keeps `groups` and the block index in 31 bits).
 int64_t checkpoint_grid(int64_t R, int64_t C, int* groups) {
   const int64_t g = (C + 127) / 128, n = g * ((R + kCkptRows - 1) / kCkptRows);
   *groups = (int)g;
-  return g < (1ll << 31) && n < (1ll << 31) ? n : -1;
+  return n < (1ll << 32) / 256 ? n : -1;
 }
 
 }  // namespace
@@ -377,7 +378,7 @@ hipError_t launch_checkpoint_load(const uint8_t* codes, const uint8_t* scales, i
 hipError_t launch_quantize_saved(const SavedPackParams& p, const SavedPackParams* q, int fmt, int mode, int had,
                                  hipStream_t stream) {
   const int64_t first = pack_tiles(p), all = first + (q ? pack_tiles(*q) : 0);
-  if (all >= (1ll << 31)) return hipErrorInvalidValue;
+  if (all >= (1ll << 32) / 512) return hipErrorInvalidValue;
   if (all == 0) return hipSuccess;
   if (fmt == kE2M1 && mode == kFloor && !had) return launch_packs<kE2M1, kFloor, 0>(p, q, first, all, stream);
   if (fmt == kE2M3 && mode == kFloor && !had) return launch_packs<kE2M3, kFloor, 0>(p, q, first, all, stream);

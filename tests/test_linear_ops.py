@@ -991,3 +991,18 @@ def test_activation_and_slope_error_bounds(act):
     mx.quantize_saved(1, 8192, mx.E4M3, mx.RCEIL, act=act, x=torch.ones(1, 8192, dtype=torch.bfloat16, device="cuda"), saved=ck,
                       colsum_partials=part, colsum=slope)
     assert np.abs(f64(slope) - slope64(s, act)).max() <= 2.0 ** -17
+
+
+def test_sizes_past_the_thread_limit_of_a_launch_are_refused():
+    """2^32 threads: 2^24 workgroups of 256 (checkpoints, 64 x 128 values each), 2^23 of 512 (packs, 128 x 128)."""
+    L = mx.lib()
+    for R, C in ((1 << 30, 128), ((1 << 22) * 64 - 63, 512), (64, 1 << 31)):
+        assert L.mx_checkpoint_save(P[0], 0, R, C, C, P[1], P[2], None) == OVERFLOW
+        assert L.mx_checkpoint_load(P[1], P[2], R, C, P[0], 0, C, None) == OVERFLOW
+    for R, C in ((1 << 30, 128), ((1 << 21) * 128 - 127, 512), (128, 1 << 30)):
+        for x in (None, P[0]):
+            a = saved_args(R=R, C=C, x=x, ldx=C)
+            assert L.mx_quantize_saved(ctypes.byref(a), None) == OVERFLOW
+    if not torch.cuda.is_available():  # one tile less passes the checks of the arguments
+        assert L.mx_checkpoint_save(P[0], 0, (1 << 30) - 64, 128, 128, P[1], P[2], None) == DEVICE
+        assert L.mx_quantize_saved(ctypes.byref(saved_args(R=(1 << 30) - 128, C=128, ldx=128)), None) == DEVICE
