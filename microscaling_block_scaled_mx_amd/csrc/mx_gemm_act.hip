@@ -80,9 +80,8 @@ __global__ __launch_bounds__(tile_threads(BM, BN, kEpiAct), OCC) void gemm_act_k
 // w, w + W, ...; each stages its groups in a ring of D buffers of its own in
 // LDS, filled by direct global -> LDS loads that need no registers and no
 // barrier.  The loads take a panel's rows back to back, lane after lane, so a
-// wavefront's load is whole cache lines (loaded straight into the layout
-// above, 16 bytes of each of 16 rows at a time, 32 x 4096 x 12288 in E4M3
-// took 19.3 us); the 16-byte chunks of a row are permuted on the way so that
+// wavefront's load is whole cache lines (the layout above takes 16 bytes of
+// each of 16 rows at a time); the 16-byte chunks of a row are permuted on the way so that
 // the reads of 16 rows spread over the LDS banks.  The partial tiles meet in
 // LDS and are summed in wavefront order: the result does not depend on
 // timing.  Rows past the operands' ends are loaded as the last row and never
@@ -394,31 +393,31 @@ enum Shape {
 // column sums go beside the other product.
 constexpr bool takes_two(int shape) { return shape != kTile256x128; }
 
-// Which one (times in us, measured with one variant after the other on the
-// same operands; E2M1 / E2M3 / E4M3):
+// Which one (device times in us, measured with one variant after the other on
+// the same operands; E2M1 / E2M3 / E4M3):
 //  - M <= 32: one row of tiles, so the weights are read once.  Four
 //    wavefronts where the column panels fill the chip (1 x 12288 x 4096:
-//    6.6 / 8.5 / 9.8, eight 6.8 / 8.5 / 11.1), else eight over K
-//    (8 x 4096 x 12288: 7.2 / 8.6 / 10.2, four 8.3 / 9.8 / 9.9).
+//    6.6 / 8.4 / 9.7, eight 6.9 / 8.5 / 11.0), else eight over K
+//    (8 x 4096 x 12288: 7.0 / 8.5 / 10.2, four 7.9 / 8.9 / 10.1).
 //  - up to 320 tiles of 64 x 64 (or M <= 64, whose 128-row tiles would be half
 //    empty) the few-rows kernel with the largest tile that still gives most
-//    compute units one: 512 x 2048 x 2048 64x64 6.8 / 8.4 / 9.8, 128x128
-//    8.2 / 9.5 / 14.9; 128 x 4096 x 4096 64x32 7.0 / 8.2 / 9.7, 64x64
-//    8.1 / 8.9 / 10.3; 64 x 2048 x 12288 32x32 8.0 / 10.3 / 12.6, 64x32
-//    11.4 / 12.8 / 14.7.  With at most three K groups the four wavefronts have
-//    too little to share and the 128x128 tiles are taken (768 x 2048 x 224,
-//    GELU: 6.5 / 7.3 / 7.1, 64x64 6.1 / 9.8 / 9.6).
+//    compute units one: 512 x 2048 x 2048 64x64 7.7 / 9.3 / 10.8, 64x32
+//    6.5 / 8.3 / 11.1, 128x128 7.9 / 9.3 / 14.9; 128 x 4096 x 4096 64x32
+//    6.6 / 7.6 / 9.4, 64x64 9.1 / 10.0 / 11.2; 64 x 2048 x 12288 32x32
+//    7.9 / 10.1 / 12.7, 64x32 10.8 / 12.5 / 14.6.  With at most three K groups
+//    the four wavefronts have too little to share and the 128x128 tiles are
+//    taken (768 x 2048 x 224, GELU: 6.5 / 6.8 / 7.1, 64x64 6.2 / 9.5 / 9.7).
 //  - beyond, 256x256 tiles or, where those would leave compute units idle,
-//    128x128 at two per unit: 8191 x 2048 x 8192 256x256 66 / 79 / 112, 128x128
-//    75 / 102 / 140; 1500 x 4096 x 4096 27 / 28 / 45 against 21 / 26 / 29.
+//    128x128 at two per unit: 8191 x 2048 x 8192 256x256 64 / 78 / 111, 128x128
+//    72 / 103 / 138; 1500 x 4096 x 4096 26 / 29 / 45 against 21 / 25 / 30.
 //    Their cost per round of the chip goes by area, 128x128 15% more.
 //  - over several rounds, with a checkpoint (E2M1: or a residual, or an
 //    activation) in the epilogue and short sums, 256x128 at two per unit: one
 //    tile's epilogue then runs beside another's products, at the price of a
-//    slower main loop.  8192 x 8192 x 2048, GELU and checkpoint 118 / 143 /
-//    193, 256x256 137 / 153 / 186; residual 142 / 178 / 203 against 156 / 170 /
-//    201; 8192 x 8192 x 4096, GELU and checkpoint 178 / 222 / 320 against
-//    183 / 212 / 276; GELU alone 165 / 207 / 300 against 162 / 190 / 255.
+//    slower main loop.  8192 x 8192 x 2048, GELU and checkpoint 118 / 141 /
+//    190, 256x256 136 / 154 / 183; residual 140 / 177 / 201 against 153 / 172 /
+//    202; 8192 x 8192 x 4096, GELU and checkpoint 174 / 218 / 317 against
+//    181 / 211 / 276; GELU alone 163 / 206 / 298 against 161 / 190 / 256.
 //    overlap_k is the longest K that takes them, -1 where none does (an empty
 //    sum is no shorter than that).
 constexpr int64_t overlap_k(int fmt, bool saved, bool residual, bool act) {
@@ -472,11 +471,12 @@ hipError_t launch_fmt(int fmt, const GemmActParams& p, const Second* more, int s
 }
 
 // The variant that serves both products, or -1.  Each keeps its own where
-// those agree.  Else the smaller tile's product takes the larger's variant if
-// that costs it less than the launch it saves (about 4 us): its sums are then
-// split over fewer wavefronts, or over none, so they have to be short.
-// 200 x 2048 x 768 with 768 x 2048 x 200 in E4M3 took 9.9 us so, 13.7 in two
-// launches.
+// those agree.  Else the smaller tile's product takes the larger's variant,
+// which saves a launch and the end of one: its sums are then split over fewer
+// wavefronts, or over none, so they have to be short.  200 tokens 2048 -> 768
+// in E4M3 take 8.1 us so, 10.7 in two launches; 24 tokens 4096 -> 2048, at the
+// limit of 16 groups, 12.9 / 13.4 / 16.5 against 12.2 / 13.1 / 13.6 (E2M1 /
+// E2M3 / E4M3); 8 tokens 160 -> 128 2.9 against 5.0.
 int pair_shape(int fmt, const GemmActParams& p, const GemmActParams& q) {
   const int a = pick_shape(fmt, p), b = pick_shape(fmt, q);
   if (a == b) return takes_two(a) ? a : -1;
@@ -494,8 +494,8 @@ hipError_t launch_gemm_act(const GemmActParams& p, int fmt, hipStream_t stream) 
 }
 
 // The product with the longer sums goes first, so that the shorter tiles even
-// out the end (4095 x 2016 x 2080 with 2080 x 2016 x 4096 in E2M1: 30 us, the
-// other way round 35).
+// out the end (4095 tokens 2016 -> 2080 in E2M1: 30.4 us, the other way round
+// 32.3, in two launches 34.7).
 hipError_t launch_gemm_act_pair(const GemmActParams& p, const GemmActParams& q, const ColumnSums& sums, int fmt,
                                 hipStream_t stream) {
   if (q.K > p.K) return launch_gemm_act_pair(q, p, sums, fmt, stream);
