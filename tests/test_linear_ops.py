@@ -1006,3 +1006,38 @@ def test_sizes_past_the_thread_limit_of_a_launch_are_refused():
     if not torch.cuda.is_available():  # one tile less passes the checks of the arguments
         assert L.mx_checkpoint_save(P[0], 0, (1 << 30) - 64, 128, 128, P[1], P[2], None) == DEVICE
         assert L.mx_quantize_saved(ctypes.byref(saved_args(R=(1 << 30) - 128, C=128, ldx=128)), None) == DEVICE
+
+
+@gpu
+@pytest.mark.parametrize("fmt,mode,had", FMTS)
+def test_captured_accumulating_backward(fmt, mode, had):
+    """Every replay adds the gradient once more, as every eager call does; products in a launch each (MXFP4) or in one."""
+    M, N, K = 2100, 1952, 16352
+    g = torch.Generator(device="cuda").manual_seed(fmt)
+    t = lambda *s: torch.randn(s, generator=g, device="cuda")
+    dY, cx, cp, Wc = t(M, N).bfloat16(), mx.alloc_packed(M, K, mx.E4M3), mx.alloc_packed(M, N, mx.E4M3), mx.alloc_packed(K, N, fmt)
+    mx.checkpoint_save(t(M, K), cx)
+    mx.checkpoint_save(t(M, N), cp)
+    q = dict(fmt=fmt, scale_mode=mode, hadamard=had)
+    mx.quantize_saved(K, N, x=t(K, N).bfloat16(), row=Wc, **q)
+    sides = [(dict(dX=torch.empty(M, K, dtype=torch.bfloat16, device="cuda"), dW=torch.zeros(N, K, device="cuda"),
+                   db=torch.empty(N, device="cuda")), bwd_work(M, N, K, fmt)) for _ in range(2)]
+
+    def step(out, work):
+        mx.linear_bwd_saved(M, N, K, dY, cx, Wc, act=mx.ACT_SILU, saved_pre=cp, accumulate=True, **q, **out, **work)
+
+    step(*sides[0])  # eager first, so that nothing is loaded during the capture
+    sides[0][0]["dW"].zero_()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(*sides[1])
+    sides[1][0]["dW"].zero_()
+    for _ in range(3):
+        for out, _ in sides:
+            out["dX"].zero_(), out["db"].zero_()
+        step(*sides[0])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(sides[0][0][k], sides[1][0][k]) for k in ("dX", "dW", "db"))
+        assert sides[0][0]["dW"].any()
