@@ -702,6 +702,250 @@ typedef struct {
 
 int mx_linear_bwd_saved(const mx_linear_bwd_args* args, void* stream);
 
+/* ---------------------------------------------------------------- training operators */
+/*
+ * What a training step does around its linears: the layer norm in front of
+ * one, with its output packed as it is formed (mx_layernorm_fwd, _bwd), the
+ * loss of the projection onto a vocabulary, whose logits are never kept
+ * (mx_head_loss, _bwd), and the step over the weights (mx_adamw).
+ */
+
+/*
+ * mx_layernorm_fwd -- of every row of x [M][ldx], with mean = sum x / C and
+ * rstd = 1 / sqrt(sum (x - mean)^2 / C + eps):
+ *   y = (x - mean) rstd gamma + beta
+ * in binary32 (the variance from the differences to the mean), rounded once to
+ * y_dtype, and the operands that a linear makes of y rounded to bf16: `row`
+ * (what mx_quantize_saved packs) and `saved` (what mx_checkpoint_save writes),
+ * byte for byte, without y being read again.
+ *
+ *  M            any number >= 0; 0 enqueues nothing.
+ *  C            a multiple of 8, 8 .. MX_LAYERNORM_MAX_C; with row or saved of 32.
+ *  gamma, beta  [C] of w_dtype, or NULL (1 and 0).
+ *  eps          finite, >= 0.  A row of one value under eps = 0 gives NaN.
+ *  y            [M][ldy] of y_dtype, or NULL.
+ *  mean, rstd   binary32 [M], for the backward pass, or NULL.
+ *  row          fmt operand [M] x K=C under scale_mode and hadamard (as
+ *               mx_quantize), or {NULL, NULL} (the three are then ignored).
+ *  saved        E4M3 operand [M] x K=C, or {NULL, NULL}.
+ *  ldx, ldy     row pitches in elements, >= C, multiples of 8; elements past
+ *               C are neither read nor written.
+ * At least one output.  y may be x itself (same type and pitch); no other
+ * overlap is allowed.  Errors: MX_ERR_NULL, MX_ERR_SHAPE, MX_ERR_ALIGN,
+ * MX_ERR_FORMAT, MX_ERR_INDEX_OVERFLOW, MX_ERR_DEVICE, MX_ERR_LAUNCH.
+ *
+ * mx_layernorm_bwd -- the gradients, with h = (x - mean) rstd and g = dy gamma:
+ *   dx = rstd (g - mean(g) - h mean(g h)) + residual    (means over the row)
+ *   dgamma = sum over the rows of dy h,  dbeta = sum over the rows of dy
+ * in binary32, dx rounded once to dx_dtype.
+ *
+ *  mean, rstd   of the forward pass.
+ *  residual     [M][ldr] of dx_dtype, the gradient that reaches x past the
+ *               norm, or NULL.  It may be dx itself (ldr = lddx).
+ *  dx           [M][lddx] of dx_dtype, or NULL.  It may be dy or x itself where
+ *               type and pitch are the same.
+ *  dgamma, dbeta  binary32 [C], either or both NULL; overwritten, or added to
+ *               with accumulate = 1.
+ *  partials     binary32 [mx_layernorm_partial_rows(M, C)][2][C], needed for
+ *               dgamma and dbeta: sums of groups of rows, added in order by a
+ *               second launch.  Calls that share it must be ordered.
+ * M = 0 sets dgamma and dbeta to zero unless accumulating.
+ */
+#define MX_LAYERNORM_MAX_C 16384
+typedef struct {
+  int64_t M, C;
+  const void* x;
+  int64_t ldx;
+  const void* gamma;
+  const void* beta;
+  void* y;
+  int64_t ldy;
+  float* mean;
+  float* rstd;
+  mx_packed row;
+  mx_packed saved;
+  float eps;
+  int32_t x_dtype, y_dtype, w_dtype;
+  int32_t fmt, scale_mode, hadamard;
+  int32_t reserved;       /* 0 */
+} mx_layernorm_fwd_args;
+
+typedef struct {
+  int64_t M, C;
+  const void* dy;
+  int64_t lddy;
+  const void* x;
+  int64_t ldx;
+  const float* mean;
+  const float* rstd;
+  const void* gamma;
+  const void* residual;
+  int64_t ldr;
+  void* dx;
+  int64_t lddx;
+  float* dgamma;
+  float* dbeta;
+  float* partials;
+  int32_t dy_dtype, x_dtype, dx_dtype, w_dtype;
+  int32_t accumulate;
+  int32_t reserved;       /* 0 */
+} mx_layernorm_bwd_args;
+
+int mx_layernorm_fwd(const mx_layernorm_fwd_args* args, void* stream);
+int mx_layernorm_bwd(const mx_layernorm_bwd_args* args, void* stream);
+/* Rows of `partials` (at most 256); 0 for sizes that the call refuses. */
+int64_t mx_layernorm_partial_rows(int64_t M, int64_t C);
+
+/*
+ * mx_head_loss -- softmax cross entropy of the projection of M tokens onto V
+ * classes, l[m][v] = sum_k A[m][k] B[v][k] on packed operands (as
+ * mx_gemm_act's P):
+ *   lse[m] = log sum_v exp l[m][v],   loss[m] = lse[m] - l[m][label[m]].
+ * The logits exist in registers only: every tile of 128 or 256 classes leaves
+ * a token's largest logit and its sum of exponentials in `work`, and a second
+ * launch joins them.
+ *
+ *  M            any number >= 0; 0 enqueues nothing.
+ *  V            any number >= 1.  K: a multiple of 32, >= 32.
+ *  A, B         fmt operands [M] x K and [V] x K (rows of the hidden states
+ *               and of the weights).
+ *  labels       [M], int64.  A label outside [0, V) (-100, say) is no class:
+ *               that token's loss is 0 and so are its gradients.
+ *  loss, lse    binary32 [M].
+ *  work         mx_head_loss_work_bytes(M, V) bytes; calls that share it must be
+ *               ordered.
+ * exp is the hardware's exp2 (1 ulp).  E4M3 logits carry the error of their
+ * products (mx_gemm_act: 1.5e-5 of their norm), which is then the loss's.
+ * Errors: MX_ERR_NULL, MX_ERR_SHAPE, MX_ERR_ALIGN, MX_ERR_FORMAT,
+ * MX_ERR_INDEX_OVERFLOW, MX_ERR_DEVICE, MX_ERR_LAUNCH.
+ *
+ * mx_head_loss_bwd -- the gradients, from the forward pass's lse: the logits
+ * are formed again, a piece of the vocabulary at a time, and
+ *   G  = dloss[m] (exp(l - lse) - [v = label])   0 for a token without label
+ *   dX = Q(G) . W            [M][K] bf16
+ *   dW = Q(G^T) . Q(X^T)^T   [V][K]
+ * with G in binary32 until Q packs it to fmt along the product's inner dimension
+ * (E2M1 and E2M3 under FLOOR, E4M3 under RCEIL; hadamard as mx_quantize), so
+ * that only one piece of Q(G) is ever in memory.
+ *
+ *  dloss        binary32, the gradient of each token's loss: [M] with
+ *               dloss_step = 1, or one value for all with 0.
+ *  Wc           fmt operand [K] x K = V rounded up to 32 (columns of W); for dX.
+ *  Xc           fmt operand [K] x K = M rounded up to 32 (columns of X); for dW.
+ *               Their rows past V and M are zeros, as every pack writes them.
+ *  piece        classes a piece: a multiple of 128, >= 128.
+ *  dX           bf16 [M][lddx], or NULL.
+ *  dW           dw_dtype [V][lddw], or NULL; accumulate = 1 adds into it.
+ *  Gr           work operand [M] x K = min(piece, V) rounded up to 32; for dX.
+ *  Gc           work operand [min(piece, V)] x K = M rounded up to 32; for dW.
+ *  sums         binary32 [M][K], the sum of dX over the pieces; for dX where V >
+ *               piece.
+ * M = 0 sets dW to zero unless accumulating.  No output or work buffer may
+ * overlap another or an input; calls that share work buffers must be ordered.
+ * Errors: as above and as mx_gemm_act's; every argument is checked before
+ * anything is enqueued.
+ */
+typedef struct {
+  int64_t M, V, K;
+  int32_t fmt;
+  int32_t reserved;       /* 0 */
+  mx_packed A, B;
+  const int64_t* labels;
+  float* loss;
+  float* lse;
+  float* work;
+} mx_head_loss_args;
+
+typedef struct {
+  int64_t M, V, K;
+  int32_t fmt, scale_mode, hadamard;
+  int32_t accumulate;
+  mx_packed A, B, Wc, Xc;
+  const int64_t* labels;
+  const float* lse;
+  const float* dloss;
+  int64_t dloss_step;
+  void* dX;
+  int64_t lddx;
+  void* dW;
+  int64_t lddw;
+  int32_t dw_dtype;
+  int32_t reserved;       /* 0 */
+  mx_packed Gr, Gc;
+  int64_t piece;
+  float* sums;
+} mx_head_loss_bwd_args;
+
+int mx_head_loss(const mx_head_loss_args* args, void* stream);
+int mx_head_loss_bwd(const mx_head_loss_bwd_args* args, void* stream);
+/* 0 for sizes that the call refuses. */
+int64_t mx_head_loss_work_bytes(int64_t M, int64_t V);
+
+/*
+ * mx_adamw -- one AdamW step over n tensors, in place:
+ *   g = grad_scale grad
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay)
+ *       - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * in binary32, the factors formed in binary64.
+ *
+ *  items        host array; read before the call returns.  Each:
+ *    p          binary32 [n], the master weights.
+ *    g          [n] of g_dtype.
+ *    m, v       state_bits 32: `codes` is binary32 [n], `scales` NULL.
+ *               state_bits 8: E4M3 operands [1] x K = n rounded up to 32 under
+ *               RCEIL scales (mx_checkpoint_load reads them): m, and for v the
+ *               values of sqrt(v).  All zero bytes is the state before the first
+ *               step.  The update takes m and v before they are rounded.
+ *    copy       bf16 [n], p after the step, rounded; or NULL.
+ *    n          any number >= 0, at most 2^34.
+ *  States in 8 bits are rounded stochastically (the nearest code would never
+ *  move: a step changes a mean by less than half a code).  With neighbours
+ *  lo <= |x| / 2^X < hi in E4M3 and t = (|x| / 2^X - lo) / (hi - lo), the
+ *  magnitude is hi iff r < floor(t 2^16); r is the low half (m) or the high half
+ *  (v) of word i % 4 of Philox4x32-10 at counter (i/4 mod 2^32, i/4 div 2^32,
+ *  tensor's place in `items`, t mod 2^32), key `seed` (low, high half), for
+ *  element i: the same bits on every run, others on every step.  A block of 32
+ *  that holds a NaN or Inf reads back as NaN throughout.
+ *  lr, beta1, beta2, eps, weight_decay   0 <= beta < 1, the others finite and
+ *               >= 0.
+ *  step         t, >= 1.  Ignored where `state` is given.
+ *  state        device buffer of MX_ADAMW_STATE_BYTES that holds the step count,
+ *               all zero bytes before the first step, or NULL: each call first
+ *               advances it (one more launch), so that a call captured into a
+ *               graph makes a new step on every replay.  Calls that share it
+ *               must be ordered.
+ *  lr_device    binary32 on the device, in place of lr (with `state` only), or
+ *               NULL.
+ *  grad_scale   binary32 on the device (gradient clipping, loss scaling), or
+ *               NULL for 1.
+ * One launch for every 40 tensors that are not empty.  No two tensors may
+ * overlap.  Errors: MX_ERR_NULL, MX_ERR_SHAPE (a size, rate or step out of range,
+ * more than MX_ADAMW_MAX_ITEMS tensors), MX_ERR_ALIGN (grad_scale and lr_device:
+ * 4 bytes), MX_ERR_FORMAT, MX_ERR_INDEX_OVERFLOW, MX_ERR_DEVICE, MX_ERR_LAUNCH.
+ */
+#define MX_ADAMW_STATE_BYTES 64
+#define MX_ADAMW_MAX_ITEMS 1000000
+typedef struct {
+  float* p;
+  const void* g;
+  mx_packed m, v;
+  void* copy;
+  int64_t n;
+  int32_t g_dtype, state_bits;
+} mx_adamw_item;
+
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;
+  int64_t step;
+  uint64_t seed;
+  void* state;
+  const float* lr_device;
+  const float* grad_scale;
+} mx_adamw_args;
+
+int mx_adamw(const mx_adamw_item* items, int64_t n, const mx_adamw_args* args, void* stream);
+
 /* ---------------------------------------------------------------- misc */
 /* Human-readable name of a status code (static string). */
 const char* mx_status_str(int status);

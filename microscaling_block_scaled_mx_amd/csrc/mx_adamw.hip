@@ -1,0 +1,220 @@
+// The AdamW step over many tensors in one launch, its states in binary32 or in
+// 8 bits:
+//   g = s g,  m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2,
+//   p = p (1 - lr wd) - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps).
+//
+// States in 8 bits are E4M3 operands [1] x K = n: m, and sqrt(v), whose range
+// is half of v's in the exponent (E4M3 under one scale reaches from 448 down to
+// 2^-9; of v itself a block would lose everything below 2^-17 of its largest).
+// They are rounded stochastically: the nearest code would never move, as one
+// step changes a mean by 0.1% to 10% and half a step of E4M3 is 3% to 6%.
+// Everything else is binary32, and the update takes m and v before they are
+// rounded.
+//
+// Bound by HBM: 16 bytes an element with bf16 gradients and 8-bit states (28
+// with binary32 states), each read and written once.  A thread takes eight
+// consecutive elements a step, four lanes a block.  The tensors' addresses
+// travel in the launch's arguments, so no table has to be copied and a launch
+// can be captured into a graph.
+#include <limits.h>
+#include <math.h>
+#include <string.h>
+
+#include "mx_lanes.h"
+#include "mx_train.h"
+
+namespace mx {
+
+namespace {
+
+__host__ __device__ AdamFactors factors_of(const AdamHyper& h, double lr, int64_t step) {
+  const double t = (double)step;
+  AdamFactors f;
+  f.decay = (float)(1.0 - lr * h.weight_decay);
+  // 1 - beta^t; log(0) gives exp(-inf) = 0
+  f.rate = (float)(lr / -expm1(t * log(h.beta1)));
+  f.inv_root = (float)(1.0 / sqrt(-expm1(t * log(h.beta2))));
+  f.eps = (float)h.eps;
+  f.b1 = (float)h.beta1;
+  f.g1 = (float)(1.0 - h.beta1);
+  f.b2 = (float)h.beta2;
+  f.g2 = (float)(1.0 - h.beta2);
+  return f;
+}
+
+__global__ void adam_advance_kernel(AdamState* state, AdamHyper h, const float* lr) {
+  const int64_t step = state->step + 1;
+  state->step = step;
+  state->f = factors_of(h, lr != nullptr ? (double)*lr : h.lr, step);
+}
+
+// E4M3 code of x / 2^X given 2^-X (|x| <= 448 2^X), rounded by 16 random bits:
+// with neighbours lo <= |x| / 2^X < hi a step apart, hi iff r < floor(t 2^16),
+// t the share of the step above lo.  Exact: normal codes are the upper bits of
+// the binary32 pattern, below 2^-6 the steps are 2^-9.
+__device__ __forceinline__ uint32_t e4m3_sr_code(float x, float inv, uint32_t r) {
+  const float a = __builtin_fabsf(x) * inv;
+  const uint32_t b = __float_as_uint(a);
+  const float u = a * 512.0f, low = __builtin_floorf(u);
+  const bool normal = a >= 0x1p-6f;
+  const uint32_t code = normal ? (b >> 20) - (120u << 3) : (uint32_t)low;
+  const uint32_t k = normal ? (b & 0xfffffu) >> 4 : (uint32_t)((u - low) * 65536.0f);
+  return code + (r < k ? 1u : 0u) + ((__float_as_uint(x) >> 24) & 0x80u);
+}
+
+// Eight values at element c of a tensor of n (zeros past its end), binary32 or
+// bf16, and the same written.
+__device__ __forceinline__ void read8(const void* base, int64_t c, int64_t n, int f32, float (&v)[8]) {
+  if (c + 8 <= n) {
+    lane8_read(base, c, f32, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      v[e] = 0.0f;
+      if (c + e < n)
+        v[e] = f32 ? reinterpret_cast<const float*>(base)[c + e] : bf16_to_f32(reinterpret_cast<const uint16_t*>(base)[c + e]);
+    }
+  }
+}
+__device__ __forceinline__ void write8(void* base, int64_t c, int64_t n, int f32, const float (&v)[8]) {
+  if (c + 8 <= n) {
+    lane8_store(base, c, f32, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (c + e < n) {
+        if (f32) reinterpret_cast<float*>(base)[c + e] = v[e];
+        else reinterpret_cast<uint16_t*>(base)[c + e] = (uint16_t)f32_to_bf16(v[e]);
+      }
+    }
+  }
+}
+
+// Eight values of a state in 8 bits, four lanes a block; `in`: inside the
+// operand's whole groups of 128.
+__device__ __forceinline__ void read_state8(const void* codes, const uint8_t* scales, int64_t c, bool in, float (&v)[8]) {
+  uint2 w = make_uint2(0u, 0u);
+  uint32_t s = 0u;
+  if (in) {
+    w = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(codes) + c);
+    s = scales[c >> 5];
+  }
+  const float sc = e8m0_value(s);
+  float lo[4], hi[4];
+  e4m3_decode4(w.x, sc, lo);
+  e4m3_decode4(w.y, sc, hi);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[e] = lo[e];
+    v[4 + e] = hi[e];
+  }
+}
+__device__ __forceinline__ void write_state8(void* codes, uint8_t* scales, int64_t c, bool in, const float (&v)[8],
+                                             const uint32_t (&r)[8]) {
+  const int ch = threadIdx.x & 15;
+  const uint32_t s = scale_byte<kE4M3, kRceil>(max_over4(abs_max(v)));
+  const float inv = __uint_as_float((254u - (s == 0xffu ? 127u : s)) << 23);  // 2^-X (X is at most 120)
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) w[e >> 2] |= e4m3_sr_code(v[e], inv, r[e]) << (8 * (e & 3));
+  if (s == 0xffu) w[0] = w[1] = 0u;
+  uint32_t d = s << (8 * (ch >> 2));
+  d |= dpp_move<kDppRor8>(d);
+  d |= dpp_move<kDppRor4>(d);
+  if (in) {
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(codes) + c) = make_uint2(w[0], w[1]);
+    if (ch == 0) *reinterpret_cast<uint32_t*>(scales + (c >> 5)) = d;
+  }
+}
+
+__global__ __launch_bounds__(256) void adamw_kernel(AdamParams all) {
+  // this workgroup's tensor: the last that starts at or before it
+  const int block = blockIdx.x;
+  int k = -1;
+#pragma unroll
+  for (int i = 0; i < kAdamItems; ++i) k += block >= all.first[i] ? 1 : 0;
+  const AdamItem& it = all.item[k];
+  const AdamFactors f = all.state != nullptr ? all.state->f : all.f;
+  const uint32_t step = all.state != nullptr ? (uint32_t)all.state->step : all.step;
+  const float gs = all.grad_scale != nullptr ? *all.grad_scale : 1.0f;
+  const bool eight = it.m_scales != nullptr;
+  const int64_t n = it.n, padded = (n + 127) & ~(int64_t)127;
+  const int64_t c0 = (int64_t)(block - all.first[k]) * kAdamChunk;
+#pragma unroll 1
+  for (int64_t c = c0 + 8 * (int64_t)threadIdx.x; c - 8 * (int64_t)threadIdx.x < c0 + kAdamChunk; c += 8 * 256) {
+    float p[8], g[8], m[8], v[8];
+    read8(it.p, c, n, 1, p);
+    read8(it.g, c, n, it.g_f32, g);
+    if (eight) {
+      read_state8(it.m, it.m_scales, c, c < padded, m);
+      read_state8(it.v, it.v_scales, c, c < padded, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = v[e] * v[e];
+    } else {
+      read8(it.m, c, n, 1, m);
+      read8(it.v, c, n, 1, v);
+    }
+    float root[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const bool in = c + e < n;
+      const float x = g[e] * gs;
+      m[e] = in ? __builtin_fmaf(f.b1, m[e], f.g1 * x) : 0.0f;
+      v[e] = in ? __builtin_fmaf(f.b2, v[e], f.g2 * x * x) : 0.0f;
+      root[e] = __builtin_sqrtf(v[e]);
+      p[e] = __builtin_fmaf(-f.rate, m[e] / __builtin_fmaf(root[e], f.inv_root, f.eps), p[e] * f.decay);
+    }
+    write8(it.p, c, n, 1, p);
+    if (it.copy != nullptr) write8(it.copy, c, n, 0, p);
+    if (eight) {
+      uint32_t w[8], rm[8], rv[8];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const uint64_t i = ((uint64_t)c >> 2) + q;
+        uint32_t x[4] = {(uint32_t)i, (uint32_t)(i >> 32), it.index, step};
+        philox4x32_10(x, (uint32_t)all.seed, (uint32_t)(all.seed >> 32));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[4 * q + e] = x[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        rm[e] = w[e] & 0xffffu;
+        rv[e] = w[e] >> 16;
+      }
+      write_state8(it.m, it.m_scales, c, c < padded, m, rm);
+      write_state8(it.v, it.v_scales, c, c < padded, root, rv);
+    } else {
+      write8(it.m, c, n, 1, m);
+      write8(it.v, c, n, 1, v);
+    }
+  }
+}
+
+}  // namespace
+
+AdamFactors adam_factors(const AdamHyper& h, int64_t step) { return factors_of(h, h.lr, step); }
+
+hipError_t launch_adam_advance(AdamState* state, const AdamHyper& h, const float* lr, hipStream_t stream) {
+  hipLaunchKernelGGL(adam_advance_kernel, dim3(1), dim3(1), 0, stream, state, h, lr);
+  return hipGetLastError();
+}
+
+hipError_t launch_adam(AdamParams& p, int count, hipStream_t stream) {
+  int64_t blocks = 0;
+  for (int i = 0; i < kAdamItems; ++i) {
+    if (i < count) {
+      if (blocks >= INT_MAX) return hipErrorInvalidValue;
+      p.first[i] = (int)blocks;
+      blocks += (p.item[i].n + kAdamChunk - 1) / kAdamChunk;
+    } else {
+      p.first[i] = INT_MAX;
+      memset(&p.item[i], 0, sizeof p.item[i]);
+    }
+  }
+  if (blocks >= (1ll << 32) / 256) return hipErrorInvalidValue;
+  if (blocks == 0) return hipSuccess;
+  hipLaunchKernelGGL(adamw_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, p);
+  return hipGetLastError();
+}
+
+}  // namespace mx

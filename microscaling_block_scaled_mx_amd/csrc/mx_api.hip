@@ -2,6 +2,8 @@
 // Declarations and the contract of every entry point are in include/mx.h.
 #include <hip/hip_runtime.h>
 
+#include <math.h>
+#include <initializer_list>
 #include <mutex>
 #include <string.h>
 #include <vector>
@@ -9,6 +11,7 @@
 #include "mx.h"
 #include "mx_kernels.h"
 #include "mx_linear.h"
+#include "mx_train.h"
 
 namespace {
 
@@ -340,6 +343,80 @@ int quantize_saved_launch(const mx_quantize_saved_args& a, const mx_quantize_sav
 int finish_sums_launch(const mx_quantize_saved_args& a, hipStream_t s) {
   if (!a.colsum || a.C == 0) return MX_OK;
   return launched(mx::launch_colsum_finish(a.colsum_partials, (a.R + 127) / 128, a.C, a.colsum, 1, s));
+}
+
+// ---------------------------------------------------------------- training operators
+bool all_aligned(std::initializer_list<const void*> ptrs) {
+  for (const void* q : ptrs)
+    if (!aligned16(q)) return false;  // (NULL is aligned)
+  return true;
+}
+
+// Sizes of a layer norm's tensors: rows in 16-byte steps of bf16, held by at
+// most 1024 threads.
+int validate_norm_size(int64_t M, int64_t C) {
+  if (M < 0 || C < 8 || C % 8 || C > MX_LAYERNORM_MAX_C) return MX_ERR_SHAPE;
+  return M > kMaxExtent ? MX_ERR_INDEX_OVERFLOW : MX_OK;
+}
+// [M][ld] of a layer norm, or NULL
+int validate_norm_rows(const void* t, int64_t M, int64_t C, int64_t ld) {
+  if (t && !pitch_ok(ld, C)) return MX_ERR_SHAPE;
+  return t && !rows_fit(M, ld) ? MX_ERR_INDEX_OVERFLOW : MX_OK;
+}
+
+int validate_layernorm_fwd(const mx_layernorm_fwd_args& a) {
+  if (!dtype_ok(a.x_dtype) || !dtype_ok(a.y_dtype) || !dtype_ok(a.w_dtype)) return MX_ERR_FORMAT;
+  if (packed_ok(a.row) == packed_none(a.row) || packed_ok(a.saved) == packed_none(a.saved)) return MX_ERR_NULL;
+  if (packed_ok(a.row) && !combo_ok(a.fmt, a.scale_mode, a.hadamard)) return MX_ERR_FORMAT;
+  int st = validate_norm_size(a.M, a.C);
+  if (st != MX_OK) return st;
+  if ((packed_ok(a.row) || packed_ok(a.saved)) && a.C % 32) return MX_ERR_SHAPE;
+  if (!(a.eps >= 0.0f) || isinf(a.eps)) return MX_ERR_SHAPE;
+  if ((st = validate_norm_rows(a.x, a.M, a.C, a.ldx)) != MX_OK) return st;
+  if ((st = validate_norm_rows(a.y, a.M, a.C, a.ldy)) != MX_OK) return st;
+  if (!all_aligned({a.x, a.y, a.gamma, a.beta, a.mean, a.rstd, a.row.codes, a.row.scales, a.saved.codes, a.saved.scales}))
+    return MX_ERR_ALIGN;
+  if (a.M == 0) return MX_OK;
+  if (!a.x) return MX_ERR_NULL;
+  if (!a.y && !a.mean && !a.rstd && packed_none(a.row) && packed_none(a.saved)) return MX_ERR_NULL;
+  return MX_OK;
+}
+
+int validate_layernorm_bwd(const mx_layernorm_bwd_args& a) {
+  if (!dtype_ok(a.dy_dtype) || !dtype_ok(a.x_dtype) || !dtype_ok(a.dx_dtype) || !dtype_ok(a.w_dtype)) return MX_ERR_FORMAT;
+  if (a.accumulate != 0 && a.accumulate != 1) return MX_ERR_FORMAT;
+  int st = validate_norm_size(a.M, a.C);
+  if (st != MX_OK) return st;
+  if ((st = validate_norm_rows(a.dy, a.M, a.C, a.lddy)) != MX_OK) return st;
+  if ((st = validate_norm_rows(a.x, a.M, a.C, a.ldx)) != MX_OK) return st;
+  if ((st = validate_norm_rows(a.residual, a.M, a.C, a.ldr)) != MX_OK) return st;
+  if ((st = validate_norm_rows(a.dx, a.M, a.C, a.lddx)) != MX_OK) return st;
+  if (a.residual && a.residual == a.dx && a.ldr != a.lddx) return MX_ERR_SHAPE;
+  if (!all_aligned({a.dy, a.x, a.mean, a.rstd, a.gamma, a.residual, a.dx, a.dgamma, a.dbeta, a.partials}))
+    return MX_ERR_ALIGN;
+  if (!a.dx && !a.dgamma && !a.dbeta) return MX_ERR_NULL;
+  if (a.M == 0) return MX_OK;
+  if (!a.dy || !a.x || !a.mean || !a.rstd) return MX_ERR_NULL;
+  if (a.residual && !a.dx) return MX_ERR_NULL;
+  if ((a.dgamma || a.dbeta) && !a.partials) return MX_ERR_NULL;
+  return MX_OK;
+}
+
+// What the two passes of the cross entropy share.
+int validate_head(int64_t M, int64_t V, int64_t K, int fmt) {
+  if (bits_of(fmt) == 0) return MX_ERR_FORMAT;
+  if (M < 0 || V < 1 || K < 32 || K % 32) return MX_ERR_SHAPE;
+  const int64_t kp = (K + 127) / 128 * 128;
+  if (K > kMaxOperandBytes) return MX_ERR_INDEX_OVERFLOW;
+  for (int64_t rows : {M, V})
+    if (rows > kMaxOperandBytes || (rows > 0 && kp * bits_of(fmt) / 8 > kMaxOperandBytes / rows)) return MX_ERR_INDEX_OVERFLOW;
+  // tiles of 128 x 128 with 256 threads, of 256 x 256 with 512
+  return threads_fit((V + 127) / 128, (M + 127) / 128, 512) ? MX_OK : MX_ERR_INDEX_OVERFLOW;
+}
+
+mx::HeadParams head_params(const mx_packed& A, const mx_packed& B, int64_t M, int64_t V, int64_t K,
+                           const int64_t* labels) {
+  return mx::HeadParams{bytes(A.codes), bytes(A.scales), bytes(B.codes), bytes(B.scales), M, V, K, labels};
 }
 
 }  // namespace
@@ -927,6 +1004,250 @@ int mx_linear_bwd_saved(const mx_linear_bwd_args* args, void* stream) {
   if ((st = finish_sums_launch(g, s)) != MX_OK) return st;
   if (want_dx) return gemm_act_launch(d, s);
   return want_dw ? gemm_act_launch(w, s) : MX_OK;
+}
+
+int64_t mx_layernorm_partial_rows(int64_t M, int64_t C) {
+  return validate_norm_size(M, C) == MX_OK ? mx::norm_partial_rows(M, C) : 0;
+}
+
+int mx_layernorm_fwd(const mx_layernorm_fwd_args* args, void* stream) {
+  if (!args) return MX_ERR_NULL;
+  const mx_layernorm_fwd_args& a = *args;
+  int st = validate_layernorm_fwd(a);
+  if (st != MX_OK) return st;
+  if ((st = check_device()) != MX_OK) return st;
+  if (a.M == 0) return MX_OK;
+  mx::NormFwdParams p;
+  memset(&p, 0, sizeof p);
+  p.x = a.x;
+  p.ldx = a.ldx;
+  p.gamma = a.gamma;
+  p.beta = a.beta;
+  p.y = a.y;
+  p.ldy = a.ldy;
+  p.mean = a.mean;
+  p.rstd = a.rstd;
+  p.row_codes = bytes(a.row.codes);
+  p.row_scales = bytes(a.row.scales);
+  p.saved_codes = bytes(a.saved.codes);
+  p.saved_scales = bytes(a.saved.scales);
+  p.M = a.M;
+  p.C = a.C;
+  p.eps = a.eps;
+  p.inv_c = (float)(1.0 / (double)a.C);
+  p.w_f32 = a.w_dtype == MX_F32;
+  p.y_f32 = a.y_dtype == MX_F32;
+  p.fmt = a.fmt;
+  p.mode = a.scale_mode;
+  p.had = a.hadamard;
+  return launched(mx::launch_norm_fwd(p, a.x_dtype == MX_F32, static_cast<hipStream_t>(stream)));
+}
+
+int mx_layernorm_bwd(const mx_layernorm_bwd_args* args, void* stream) {
+  if (!args) return MX_ERR_NULL;
+  const mx_layernorm_bwd_args& a = *args;
+  int st = validate_layernorm_bwd(a);
+  if (st != MX_OK) return st;
+  if ((st = check_device()) != MX_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const bool weights = a.dgamma || a.dbeta;
+  if (a.M > 0) {
+    mx::NormBwdParams p;
+    memset(&p, 0, sizeof p);
+    p.dy = a.dy;
+    p.lddy = a.lddy;
+    p.x = a.x;
+    p.ldx = a.ldx;
+    p.mean = a.mean;
+    p.rstd = a.rstd;
+    p.gamma = a.gamma;
+    p.residual = a.residual;
+    p.ldr = a.ldr;
+    p.dx = a.dx;
+    p.lddx = a.lddx;
+    p.partials = weights ? a.partials : nullptr;
+    p.M = a.M;
+    p.C = a.C;
+    p.inv_c = (float)(1.0 / (double)a.C);
+    p.w_f32 = a.w_dtype == MX_F32;
+    p.dx_f32 = a.dx_dtype == MX_F32;
+    st = launched(mx::launch_norm_bwd(p, a.x_dtype == MX_F32, a.dy_dtype == MX_F32, s));
+    if (st != MX_OK) return st;
+  }
+  if (!weights || (a.M == 0 && a.accumulate)) return MX_OK;
+  return launched(mx::launch_norm_weights(a.partials, mx::norm_partial_rows(a.M, a.C), a.C, a.dgamma, a.dbeta,
+                                          a.accumulate, s));
+}
+
+int64_t mx_head_loss_work_bytes(int64_t M, int64_t V) {
+  if (M < 0 || V < 1 || M > kMaxOperandBytes || V > kMaxOperandBytes) return 0;
+  return 4 * mx::head_work_floats(M, V);
+}
+
+int mx_head_loss(const mx_head_loss_args* args, void* stream) {
+  if (!args) return MX_ERR_NULL;
+  const mx_head_loss_args& a = *args;
+  int st = validate_head(a.M, a.V, a.K, a.fmt);
+  if (st != MX_OK) return st;
+  if (!all_aligned({a.A.codes, a.A.scales, a.B.codes, a.B.scales, a.labels, a.loss, a.lse, a.work})) return MX_ERR_ALIGN;
+  if (a.M > 0 && (!packed_ok(a.A) || !packed_ok(a.B) || !a.labels || !a.loss || !a.lse || !a.work)) return MX_ERR_NULL;
+  if ((st = check_device()) != MX_OK) return st;
+  if (a.M == 0) return MX_OK;
+  return launched(mx::launch_head_loss(head_params(a.A, a.B, a.M, a.V, a.K, a.labels), a.fmt, a.loss, a.lse, a.work,
+                                       static_cast<hipStream_t>(stream)));
+}
+
+int mx_head_loss_bwd(const mx_head_loss_bwd_args* args, void* stream) {
+  if (!args) return MX_ERR_NULL;
+  const mx_head_loss_bwd_args& a = *args;
+  if (a.accumulate != 0 && a.accumulate != 1) return MX_ERR_FORMAT;
+  if (!combo_ok(a.fmt, a.scale_mode, a.hadamard)) return MX_ERR_FORMAT;
+  if (a.scale_mode != (a.fmt == MX_E4M3 ? MX_SCALE_RCEIL : MX_SCALE_FLOOR)) return MX_ERR_FORMAT;
+  int st = validate_head(a.M, a.V, a.K, a.fmt);
+  if (st != MX_OK) return st;
+  if (a.piece < 128 || a.piece % 128 || (a.dloss_step != 0 && a.dloss_step != 1)) return MX_ERR_SHAPE;
+  if (!all_aligned({a.A.codes, a.A.scales, a.B.codes, a.B.scales, a.labels, a.lse})) return MX_ERR_ALIGN;
+  if ((uintptr_t)a.dloss & 3u) return MX_ERR_ALIGN;
+  if (!a.dX && !a.dW) return MX_ERR_NULL;
+  const int64_t piece = a.piece < a.V ? a.piece : a.V, pieces = (a.V + piece - 1) / piece, Mp = up32(a.M);
+  const bool want_dx = a.dX && a.M > 0, want_dw = a.dW != nullptr, many = want_dx && pieces > 1;
+  if (a.M > 0) {
+    if (!packed_ok(a.A) || !packed_ok(a.B) || !a.labels || !a.lse || !a.dloss) return MX_ERR_NULL;
+    if (want_dx && !packed_ok(a.Gr)) return MX_ERR_NULL;
+    if (want_dw && !packed_ok(a.Gc)) return MX_ERR_NULL;
+    if (many && !a.sums) return MX_ERR_NULL;
+  }
+  // dX (+)= Q(G) . W over a piece, dW of a piece = Q(G^T) . Q(X^T)^T
+  mx_gemm_act_args d;
+  memset(&d, 0, sizeof d);
+  d.M = a.M;
+  d.N = a.K;
+  d.K = up32(piece);
+  d.fmt = a.fmt;
+  d.act = MX_ACT_NONE;
+  d.A = a.Gr;
+  d.B = a.Wc;
+  d.C = a.dX;
+  d.ldc = a.lddx;
+  mx_gemm_act_args w = d;
+  w.M = a.V;  // (validated whole; launched piece by piece)
+  w.N = a.K;
+  w.K = Mp;
+  w.A = a.Gc;
+  w.B = a.Xc;
+  w.C = a.dW;
+  w.ldc = a.lddw;
+  w.c_dtype = a.dw_dtype;
+  w.residual = a.accumulate ? a.dW : nullptr;
+  w.ldr = a.lddw;
+  if (want_dx) {
+    mx_gemm_act_args whole = d;
+    whole.K = up32(a.V);  // W's columns are one operand
+    if ((st = validate_gemm_act(whole)) != MX_OK || (st = validate_gemm_act(d)) != MX_OK) return st;
+  }
+  if (want_dw && (st = validate_gemm_act(w)) != MX_OK) return st;
+  if (many && !aligned16(a.sums)) return MX_ERR_ALIGN;
+  if (many && !threads_fit((a.M * (a.K / 8) + 255) / 256, 1, 256)) return MX_ERR_INDEX_OVERFLOW;
+  if ((st = check_device()) != MX_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (a.M == 0) {  // the empty sum: K = 0
+    if (!want_dw || a.accumulate) return MX_OK;
+    w.K = 0;
+    return gemm_act_launch(w, s);
+  }
+  const mx::HeadParams h = head_params(a.A, a.B, a.M, a.V, a.K, a.labels);
+  const int bits = bits_of(a.fmt), dw_bytes = a.dw_dtype == MX_F32 ? 4 : 2;
+  if (many) {
+    d.C = a.sums;
+    d.ldc = d.ldr = a.K;
+    d.c_dtype = MX_F32;
+  }
+  for (int64_t first = 0; first < a.V; first += piece) {
+    const int64_t count = a.V - first < piece ? a.V - first : piece;
+    mx::HeadGradOut o;
+    memset(&o, 0, sizeof o);
+    o.lse = a.lse;
+    o.dloss = a.dloss;
+    o.dloss_step = a.dloss_step;
+    o.first = first;
+    o.count = count;
+    if (want_dx) {
+      o.row_codes = bytes(a.Gr.codes);
+      o.row_scales = bytes(a.Gr.scales);
+    }
+    if (want_dw) {
+      o.col_codes = bytes(a.Gc.codes);
+      o.col_scales = bytes(a.Gc.scales);
+    }
+    o.had = a.hadamard;
+    if ((st = launched(mx::launch_head_grad(h, o, a.fmt, s))) != MX_OK) return st;
+    d.K = up32(count);
+    d.B.codes = bytes(a.Wc.codes) + first / 128 * a.K * 16 * bits;
+    d.B.scales = bytes(a.Wc.scales) + first / 128 * a.K * 4;
+    d.residual = many && first > 0 ? a.sums : nullptr;
+    w.M = count;
+    w.C = bytes(a.dW) + first * a.lddw * dw_bytes;
+    w.residual = a.accumulate ? w.C : nullptr;
+    if (want_dx && want_dw)
+      st = launched(mx::launch_gemm_act_pair(gemm_act_params(d), gemm_act_params(w), mx::ColumnSums{nullptr, 0, 0, nullptr},
+                                             a.fmt, s));
+    else
+      st = gemm_act_launch(want_dx ? d : w, s);
+    if (st != MX_OK) return st;
+  }
+  if (!many) return MX_OK;
+  return launched(mx::launch_to_bf16(a.sums, a.M, a.K, static_cast<uint16_t*>(a.dX), a.lddx, s));
+}
+
+int mx_adamw(const mx_adamw_item* items, int64_t n, const mx_adamw_args* args, void* stream) {
+  if (!args || (n > 0 && !items)) return MX_ERR_NULL;
+  if (n < 0 || n > MX_ADAMW_MAX_ITEMS) return MX_ERR_SHAPE;
+  const mx_adamw_args& a = *args;
+  const auto unit = [](double b) { return b >= 0.0 && b < 1.0; };
+  const auto plain = [](double x) { return x >= 0.0 && !isinf(x); };
+  if (!unit(a.beta1) || !unit(a.beta2) || !plain(a.eps) || !plain(a.weight_decay) || !plain(a.lr)) return MX_ERR_SHAPE;
+  if (!a.state && a.step < 1) return MX_ERR_SHAPE;
+  if (!all_aligned({a.state}) || ((uintptr_t)a.grad_scale & 3u) || ((uintptr_t)a.lr_device & 3u)) return MX_ERR_ALIGN;
+  if (a.lr_device && !a.state) return MX_ERR_NULL;
+  for (int64_t i = 0; i < n; ++i) {
+    const mx_adamw_item& q = items[i];
+    if (!dtype_ok(q.g_dtype) || (q.state_bits != 8 && q.state_bits != 32)) return MX_ERR_FORMAT;
+    if (q.n < 0) return MX_ERR_SHAPE;
+    if (q.n > (1ll << 34)) return MX_ERR_INDEX_OVERFLOW;
+    if (!all_aligned({q.p, q.g, q.m.codes, q.m.scales, q.v.codes, q.v.scales, q.copy})) return MX_ERR_ALIGN;
+    if (q.n == 0) continue;
+    if (!q.p || !q.g || !q.m.codes || !q.v.codes) return MX_ERR_NULL;
+    // states in binary32 have no scales
+    if (q.state_bits == 8 ? !q.m.scales || !q.v.scales : q.m.scales || q.v.scales) return MX_ERR_NULL;
+  }
+  int st = check_device();
+  if (st != MX_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const mx::AdamHyper h = {a.lr, a.beta1, a.beta2, a.eps, a.weight_decay};
+  mx::AdamParams p;
+  memset(&p, 0, sizeof p);
+  p.grad_scale = a.grad_scale;
+  p.seed = a.seed;
+  if (a.state) {
+    p.state = static_cast<const mx::AdamState*>(a.state);
+    if ((st = launched(mx::launch_adam_advance(static_cast<mx::AdamState*>(a.state), h, a.lr_device, s))) != MX_OK) return st;
+  } else {
+    p.f = mx::adam_factors(h, a.step);
+    p.step = (uint32_t)a.step;
+  }
+  int count = 0;
+  for (int64_t i = 0; i < n; ++i) {
+    const mx_adamw_item& q = items[i];
+    if (q.n > 0) {
+      p.item[count++] = mx::AdamItem{q.p, q.g, q.m.codes, q.v.codes, bytes(q.m.scales), bytes(q.v.scales),
+                                     static_cast<uint16_t*>(q.copy), q.n, q.g_dtype == MX_F32, (uint32_t)i};
+    }
+    if (count == mx::kAdamItems || (i == n - 1 && count > 0)) {
+      if ((st = launched(mx::launch_adam(p, count, s))) != MX_OK) return st;
+      count = 0;
+    }
+  }
+  return MX_OK;
 }
 
 const char* mx_status_str(int status) {

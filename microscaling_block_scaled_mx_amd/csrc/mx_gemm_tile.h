@@ -25,7 +25,9 @@
 
 // The epilogue kEpiAct (GemmActParams) adds a bias, applies an activation,
 // writes the 8-bit checkpoint of the pre-activation and adds a residual, for
-// any number of rows.
+// any number of rows.  kEpiOwn is an epilogue that the parameter type brings
+// along (its members pin() and finish()), for any number of rows and columns,
+// with B a run of b_group_rows' rows.
 
 // Dense tiles are ordered for cache reuse: workgroups are dealt round-robin
 // to the 8 XCDs (each with its own L2), so consecutive workgroup ids are
@@ -138,8 +140,10 @@ struct Cfg {
   static constexpr int kCPitch = kWN * 2 + 8;         // bf16 store: per-wave kWM x kWN tile
   static constexpr int kZPitch = BN * 2 + 16;         // SwiGLU: gate | up tile BM x BN, then z in its gate half
   static constexpr int kDPitch = BN * 2 + 16;         // dSwiGLU: two BM x BN tiles, 16-byte rows
+  static constexpr int kOwnPitch = kWN + 4;           // own epilogue: a wavefront's 32 x kWN floats
   static constexpr int kEpiBytes = EPI == kEpiSwiglu    ? BM * kZPitch
                                    : EPI == kEpiDSwiglu ? 2 * BM * kDPitch
+                                   : EPI == kEpiOwn     ? kWaves * 32 * kOwnPitch * 4
                                                         : kWaves * kWM * kCPitch;
   static constexpr int kBiasAt = (kJOff + kJunk > kEpiBytes) ? kJOff + kJunk : kEpiBytes;
   static constexpr int kSmem = kBiasAt + (EPI == kEpiAct ? BN * 4 : 0);  // kEpiAct: the tile's bias beside the ring
@@ -327,13 +331,14 @@ __device__ __forceinline__ uint32_t checkpoint_block(float (&v)[16], uint4& code
 #endif
 }
 
-// P: GemmParams, or GemmActParams for kEpiAct, whose M and N need not be
-// whole tiles: operand rows past the end are loaded as the last row and
-// never stored.
+// P: GemmParams; GemmActParams for kEpiAct or a type with an epilogue of its
+// own for kEpiOwn, whose M and N need not be whole tiles: operand rows past the
+// end are loaded as the last row and never stored.
 template <int FMT, int BM, int BN, int MODE, int EPI, int OCC = 1, class P = GemmParams>
 __device__ __forceinline__ void gemm_tile(const P& p, int bx, int by, int bz, uint8_t* smem) {
   using CF = Cfg<FMT, BM, BN, MODE, EPI, OCC>;
   constexpr int kBits = CF::kBits;
+  constexpr bool kAnyRows = EPI == kEpiAct || EPI == kEpiOwn;
 
   const int t = threadIdx.x;
   const int lane = t & 63, wave = t >> 6;
@@ -345,7 +350,7 @@ __device__ __forceinline__ void gemm_tile(const P& p, int bx, int by, int bz, ui
   int tm, tn;
   int split = 0;  // split K: this workgroup's part of the K range
   if constexpr (MODE == kDense) {
-    constexpr int kUp = EPI == kEpiAct ? 1 : 0;  // whole tiles, or a partial one at each end
+    constexpr int kUp = kAnyRows ? 1 : 0;  // whole tiles, or a partial one at each end
     const int tiles_m = (int)((p.M + kUp * (BM - 1)) / BM), tiles_n = (int)((p.N + kUp * (BN - 1)) / BN);
     int local = bx;
     if constexpr (EPI == kEpiSplit) {  // workgroups [s * T, (s + 1) * T) compute part s
@@ -424,11 +429,11 @@ __device__ __forceinline__ void gemm_tile(const P& p, int bx, int by, int bz, ui
     if (kend < kbeg) kend = kbeg;
     c_off = (int64_t)gi * p.M * p.N;
   }
-  if constexpr (EPI == kEpiAct) kend = (p.K + 127) & ~(int64_t)127;  // pad codes and scales are zero
+  if constexpr (kAnyRows) kend = (p.K + 127) & ~(int64_t)127;  // pad codes and scales are zero
   // rows of the A / B operands (of one group's B): the stride between K
   // groups of their codes and scales
   const int64_t a_rows = p.M;
-  const int64_t b_rows = MODE == kRaggedM ? p.b_group_rows : p.N;
+  const int64_t b_rows = MODE == kRaggedM || EPI == kEpiOwn ? p.b_group_rows : p.N;
   constexpr int kGB = 16 * kBits;  // code bytes of one row in one 128-element K group
   const int nk = (int)((kend - kbeg) / CF::kBK);
 
@@ -437,7 +442,7 @@ __device__ __forceinline__ void gemm_tile(const P& p, int bx, int by, int bz, ui
     if constexpr (EPI == kEpiSwiglu) {
       const int64_t zb = (int64_t)tn * (BN / 2);
       return b_row0 + (r < BN / 2 ? zb + r : p.F + zb + (r - BN / 2));
-    } else if constexpr (EPI == kEpiAct) {
+    } else if constexpr (kAnyRows) {
       return n0 + r < p.N ? n0 + r : p.N - 1;
     } else {
       return b_row0 + n0 + r;
@@ -459,7 +464,7 @@ __device__ __forceinline__ void gemm_tile(const P& p, int bx, int by, int bz, ui
     const int rr = r < BM ? r : 0;  // junk slots read a valid chunk
     const int c = chunk_at<CF::kChunks>(rr, pos);
     int64_t ar = MODE == kRaggedM && m0 + rr >= m_end ? m_end - 1 : m0 + rr;
-    if constexpr (EPI == kEpiAct) ar = ar < p.M ? ar : p.M - 1;
+    if constexpr (kAnyRows) ar = ar < p.M ? ar : p.M - 1;
     a_off[i] = (uint32_t)(ar * kGB + 16 * c);
   }
 #pragma unroll
@@ -486,7 +491,7 @@ __device__ __forceinline__ void gemm_tile(const P& p, int bx, int by, int bz, ui
     const int rw = wave_uniform(r);  // the wavefront's first slot
     const bool is_b = rw >= BM && rw < BM + BN;
     int64_t ar = MODE == kRaggedM && m0 + (r < BM ? r : 0) >= m_end ? m_end - 1 : m0 + (r < BM ? r : 0);
-    if constexpr (EPI == kEpiAct) ar = ar < p.M ? ar : p.M - 1;
+    if constexpr (kAnyRows) ar = ar < p.M ? ar : p.M - 1;
     s_base[j] = is_b ? p.b_scales + b_soff : p.a_scales;
     s_off[j] = (uint32_t)(is_b ? (b_row(r - BM) - b_row0) * 4 : ar * 4);
     s_step[j] = (uint32_t)((is_b ? b_rows : a_rows) * 4);
@@ -693,6 +698,8 @@ __device__ __forceinline__ void gemm_tile(const P& p, int bx, int by, int bz, ui
     pin_arg(p.saved_scales);
     pin_arg(p.M);
     pin_arg(p.N);
+  } else if constexpr (EPI == kEpiOwn) {
+    p.pin();
   } else {
     pin_arg(p.F);
     pin_arg(p.R);
@@ -1079,6 +1086,8 @@ __device__ __forceinline__ void gemm_tile(const P& p, int bx, int by, int bz, ui
         }
       }
     }
+  } else if constexpr (EPI == kEpiOwn) {
+    p.template finish<FMT, CF>(acc, m0, n0, tn, smem);
   } else if constexpr (EPI == kEpiSwiglu) {
     // A lane holds gate (j < NJ/2) and up (j + NJ/2) of the same (row, z
     // columns).  Both are staged in LDS as bf16, the gate half in columns

@@ -1,0 +1,407 @@
+// Softmax cross entropy of a vocabulary projection, l = A . B^T on packed
+// operands, without keeping the logits.
+//
+// Forward: each output tile of the block-scaled GEMM (mx_gemm_tile.h) leaves,
+// of every token, the largest of its logits and the sum of their exponentials
+// below it (8 bytes for a tile's 128 or 256 logits); a second kernel joins a
+// token's tiles:
+//   lse = log sum exp l,  loss = lse - l[label].
+// Backward: the logits are formed again, of one piece of the vocabulary at a
+// time, and become
+//   G = dloss (exp(l - lse) - [class = label])
+// in the accumulators; from there G is packed, rowwise for dX = Q(G) . W and
+// columnwise for dW = Q(G^T) . Q(X^T)^T, as the grouped GEMM's epilogues do.
+// Exponentials are the hardware's exp2 (1 ulp) of l log2(e); sums are binary32.
+#include <string.h>
+
+#include "mx_device.h"
+#include "mx_gemm_tile.h"
+#include "mx_kernels.h"
+#include "mx_linear.h"
+#include "mx_train.h"
+
+namespace mx {
+
+namespace {
+
+constexpr float kLog2e = 0x1.715476p+0f, kLn2 = 0x1.62e43p-1f;
+
+__device__ __forceinline__ float exp2_hw(float x) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  return __builtin_amdgcn_exp2f(x);
+#else
+  return x;
+#endif
+}
+__device__ __forceinline__ float log2_hw(float x) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  return __builtin_amdgcn_logf(x);
+#else
+  return x;
+#endif
+}
+
+// Order of a wavefront's own LDS writes and reads across lanes (its LDS
+// instructions execute in order; the compiler must not move them).
+__device__ __forceinline__ void wave_lds_fence() {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_wave_barrier();
+  asm volatile("" ::: "memory");
+#endif
+}
+
+// ------------------------------------------------------------------ forward
+// A token's logits of one tile: `top` = log2(e) max l (rounded), sum of
+// 2^(log2(e) l - top).  The rounding of top cancels, as the same number is added
+// again in the end.
+struct Part {
+  float top, sum;
+};
+// An empty part (no class) has top = -inf, sum = 0.
+__device__ __forceinline__ Part joined(const Part& a, const Part& b) {
+  const float top = __builtin_fmaxf(a.top, b.top), base = top == -__builtin_inff() ? 0.0f : top;
+  return Part{top, a.sum * exp2_hw(a.top - base) + b.sum * exp2_hw(b.top - base)};
+}
+
+struct HeadLossParams : GemmParams {
+  const int64_t* labels;
+  Part* parts;        // [tiles of classes][M]
+  float* label_logit; // [M], written where the label is a class
+
+  __device__ __forceinline__ void pin() const {
+    pin_arg(labels);
+    pin_arg(parts);
+    pin_arg(label_logit);
+    pin_arg(M);
+    pin_arg(N);
+  }
+
+  template <int FMT, class CF, class Acc>
+  __device__ __forceinline__ void finish(Acc& acc, int64_t m0, int64_t n0, int tn, uint8_t* smem) const {
+#if defined(__HIP_DEVICE_COMPILE__)
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6, wm = wave / CF::kWavesN, wn = wave % CF::kWavesN;
+    const int lrow = lane & 31, g = lane >> 5;
+    const int64_t mw = m0 + wm * CF::kWM, nw = n0 + wn * CF::kWN;
+    Part* const red = reinterpret_cast<Part*>(smem);  // [kWavesN][2 kWM]
+    if (nw + CF::kWN > N) {  // (uniform) classes past the end count nothing
+#pragma unroll
+      for (int i = 0; i < CF::kMI; ++i)
+#pragma unroll
+        for (int j = 0; j < CF::kNJ; ++j)
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            acc[i][j][e] = nw + 32 * j + 8 * (e / 4) + 4 * g + e % 4 < N ? acc[i][j][e] : -__builtin_inff();
+    }
+#pragma unroll
+    for (int i = 0; i < CF::kMI; ++i) {
+      const int64_t m = mw + 32 * i + lrow;
+      float top = -__builtin_inff();
+#pragma unroll
+      for (int j = 0; j < CF::kNJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) top = __builtin_fmaxf(top, acc[i][j][e]);
+      // a token's logits lie in lanes l and l ^ 32: one maximum for both
+      const uint32_t tb = __float_as_uint(top);
+      const auto tt = __builtin_amdgcn_permlane32_swap(tb, tb, false, false);
+      top = __builtin_fmaxf(__uint_as_float(tt[0]), __uint_as_float(tt[1])) * kLog2e;
+      const float base = top == -__builtin_inff() ? 0.0f : top;
+      float sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < CF::kNJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sum = sum + exp2_hw(__builtin_fmaf(acc[i][j][e], kLog2e, -base));
+      const uint32_t sb = __float_as_uint(sum);
+      const auto ss = __builtin_amdgcn_permlane32_swap(sb, sb, false, false);
+      sum = __uint_as_float(ss[0]) + __uint_as_float(ss[1]);
+      if (g == 0) red[wn * 2 * CF::kWM + wm * CF::kWM + 32 * i + lrow] = Part{top, sum};
+      // the label's logit, from the lane that holds it
+      const int64_t y = m < M ? labels[m] : -1;
+      const int at = y >= nw && y < nw + CF::kWN && y < N ? (int)(y - nw) : -1;
+      if (__builtin_amdgcn_ballot_w64(at >= 0) != 0) {
+        float logit = 0.0f;
+        bool here = false;
+#pragma unroll
+        for (int j = 0; j < CF::kNJ; ++j)
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (at == 32 * j + 8 * (e / 4) + 4 * g + e % 4) {
+              logit = acc[i][j][e];
+              here = true;
+            }
+        if (here) label_logit[m] = logit;
+      }
+    }
+    __syncthreads();
+    if (t < 2 * CF::kWM && m0 + t < M) {
+      Part all = red[t];
+#pragma unroll
+      for (int w = 1; w < CF::kWavesN; ++w) all = joined(all, red[w * 2 * CF::kWM + t]);
+      parts[(int64_t)tn * M + m0 + t] = all;
+    }
+#endif
+  }
+};
+
+// Joins the parts of ROWS tokens a workgroup: 256 / ROWS threads a token take
+// every so manieth tile, then meet in LDS in a fixed order.
+template <int ROWS>
+__global__ __launch_bounds__(256) void head_join_kernel(const Part* __restrict__ parts, int64_t tiles, int64_t M,
+                                                        int64_t V, const int64_t* __restrict__ labels,
+                                                        const float* __restrict__ label_logit,
+                                                        float* __restrict__ loss, float* __restrict__ lse) {
+  constexpr int kSides = 256 / ROWS;
+  __shared__ Part red[256];
+  const int t = threadIdx.x, row = t % ROWS, side = t / ROWS;
+  const int64_t m = (int64_t)blockIdx.x * ROWS + row;
+  Part all = {-__builtin_inff(), 0.0f};
+  if (m < M) {
+#pragma unroll 4
+    for (int64_t q = side; q < tiles; q += kSides) all = joined(all, parts[q * M + m]);
+  }
+  red[t] = all;
+  __syncthreads();
+#pragma unroll
+  for (int half = kSides / 2; half > 0; half /= 2) {
+    if (side < half) red[t] = joined(red[t], red[t + half * ROWS]);
+    __syncthreads();
+  }
+  if (side != 0 || m >= M) return;
+  all = red[t];
+  const float total = (all.top + log2_hw(all.sum)) * kLn2;
+  lse[m] = total;
+  const int64_t y = labels[m];
+  loss[m] = y >= 0 && y < V ? total - label_logit[m] : 0.0f;
+}
+
+// ------------------------------------------------------------------ gradient
+struct HeadGradParams : GemmParams {
+  const int64_t* labels;
+  const float* lse;
+  const float* dloss;
+  int64_t dloss_step;
+  int64_t first;      // of the piece: column n is class first + n
+  int64_t classes;    // V
+  int had;
+
+  __device__ __forceinline__ void pin() const {
+    pin_arg(labels);
+    pin_arg(lse);
+    pin_arg(dloss);
+    pin_arg(dloss_step);
+    pin_arg(first);
+    pin_arg(classes);
+    pin_arg(had);
+    pin_arg(q_row_codes);
+    pin_arg(q_row_scales);
+    pin_arg(q_col_codes);
+    pin_arg(q_col_scales);
+    pin_arg(M);
+    pin_arg(N);
+  }
+
+  // 32 values to the format's block, under the scale selection that goes with
+  // the format.
+  template <int FMT>
+  __device__ __forceinline__ void store(float (&v)[32], uint8_t* g, int blk, int64_t row, uint8_t* scale) const {
+    if constexpr (FMT == kE4M3) {
+      quant_store<FMT, kRceil, 0>(v, g, blk, row, scale);
+    } else {
+      if constexpr (FMT == kE2M3) {
+        if (had) hadamard32(v);
+      }
+      quant_store<FMT, kFloor, 0>(v, g, blk, row, scale);
+    }
+  }
+
+  // A wavefront turns its 32 x 64 pieces into G in an LDS tile of its own
+  // (binary32, pitch 68: rows start four banks apart, so 16-byte row reads and
+  // 4-byte column reads are both free of conflicts); each lane then packs one
+  // row's and one column's block of 32.
+  template <int FMT, class CF, class Acc>
+  __device__ __forceinline__ void finish(Acc& acc, int64_t m0, int64_t n0, int, uint8_t* smem) const {
+#if defined(__HIP_DEVICE_COMPILE__)
+    static_assert(CF::kWN == 64, "a lane a block");
+    constexpr int kBits = FmtTraits<FMT>::kBits, kPitch = CF::kOwnPitch;
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6, wm = wave / CF::kWavesN, wn = wave % CF::kWavesN;
+    const int lrow = lane & 31, g = lane >> 5;
+    const int64_t mw = m0 + wm * CF::kWM, nw = n0 + wn * CF::kWN;
+    const int64_t packed_n = (N + 127) & ~(int64_t)127, packed_m = (M + 127) & ~(int64_t)127;
+    float* const tile = reinterpret_cast<float*>(smem) + wave * 32 * kPitch;
+    const int limit = N - nw < CF::kWN ? (int)(N - nw) : CF::kWN;  // columns of this wavefront (may be <= 0)
+    float top[CF::kMI], d[CF::kMI];
+    int at[CF::kMI];
+#pragma unroll
+    for (int i = 0; i < CF::kMI; ++i) {
+      const int64_t m = mw + 32 * i + lrow;
+      const int64_t mc = m < M ? m : M - 1;
+      const int64_t y = labels[mc];
+      const bool counts = m < M && y >= 0 && y < classes;
+      top[i] = counts ? -lse[mc] * kLog2e : -__builtin_inff();  // no label: every exponential is 0
+      d[i] = counts ? dloss[mc * dloss_step] : 0.0f;
+      const int64_t c = y - first - nw;
+      at[i] = counts && c >= 0 && c < CF::kWN ? (int)c : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < CF::kMI; ++i) {
+#pragma unroll
+      for (int j = 0; j < CF::kNJ; ++j)
+#pragma unroll
+        for (int e4 = 0; e4 < 4; ++e4) {
+          const int c = 32 * j + 8 * e4 + 4 * g;
+          float v[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float p = exp2_hw(__builtin_fmaf(acc[i][j][4 * e4 + q], kLog2e, top[i]));
+            const float x = d[i] * (p - (at[i] == c + q ? 1.0f : 0.0f));
+            v[q] = c + q < limit ? x : 0.0f;
+          }
+          *reinterpret_cast<float4*>(tile + lrow * kPitch + c) = make_float4(v[0], v[1], v[2], v[3]);
+        }
+      wave_lds_fence();
+      const int64_t m = mw + 32 * i + lrow, n = nw + 32 * g;
+      if (q_row_codes != nullptr && m < M && n < packed_n) {
+        float v[32];
+        const float4* src = reinterpret_cast<const float4*>(tile + lrow * kPitch + 32 * g);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float4 x = src[k];
+          v[4 * k] = x.x;
+          v[4 * k + 1] = x.y;
+          v[4 * k + 2] = x.z;
+          v[4 * k + 3] = x.w;
+        }
+        store<FMT>(v, q_row_codes + code_group(m, n, M, kBits), (int)((n >> 5) & 3), m,
+                   q_row_scales + scale_offset(m, n >> 5, M));
+      }
+      const int64_t mb = mw + 32 * i, nc = nw + lane;
+      if (q_col_codes != nullptr && nc < N && mb < packed_m) {
+        float v[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] = tile[k * kPitch + lane];
+        store<FMT>(v, q_col_codes + code_group(nc, mb, N, kBits), (int)((mb >> 5) & 3), nc,
+                   q_col_scales + scale_offset(nc, mb >> 5, N));
+      }
+      wave_lds_fence();
+    }
+#endif
+  }
+};
+
+// ------------------------------------------------------------------ kernels
+template <int FMT, int BM, int BN, int OCC, class P>
+__global__ __launch_bounds__(tile_threads(BM, BN, kEpiOwn), OCC) void head_kernel(P p) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[Cfg<FMT, BM, BN, kDense, kEpiOwn, OCC>::kSmem];
+  gemm_tile<FMT, BM, BN, kDense, kEpiOwn, OCC>(p, blockIdx.x, 0, 0, smem);
+}
+
+template <int FMT, int BM, int BN, int OCC, class P>
+hipError_t launch_tiles(const P& p, hipStream_t stream) {
+  const int64_t tiles = ((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
+  if (tiles >= (1ll << 31) / 512) return hipErrorInvalidValue;
+  constexpr int kThreads = Cfg<FMT, BM, BN, kDense, kEpiOwn, OCC>::kThreads;
+  hipLaunchKernelGGL((head_kernel<FMT, BM, BN, OCC, P>), dim3((unsigned)tiles), dim3(kThreads), 0, stream, p);
+  return hipGetLastError();
+}
+
+// Classes a tile: 256 x 256 where such tiles fill the chip, else 128 x 128, two
+// a compute unit.
+int tile_classes(int64_t M, int64_t N) {
+  const int64_t t256 = ((M + 255) / 256) * ((N + 255) / 256);
+  return M > 128 && t256 >= cu_count() ? 256 : 128;
+}
+
+template <int FMT, class P>
+hipError_t launch_of(const P& p, hipStream_t stream) {
+  return tile_classes(p.M, p.N) == 256 ? launch_tiles<FMT, 256, 256, 1>(p, stream)
+                                       : launch_tiles<FMT, 128, 128, 2>(p, stream);
+}
+
+template <class P>
+hipError_t launch_fmt(const P& p, int fmt, hipStream_t stream) {
+  switch (fmt) {
+    case kE2M1: return launch_of<kE2M1>(p, stream);
+    case kE2M3: return launch_of<kE2M3>(p, stream);
+    case kE4M3: return launch_of<kE4M3>(p, stream);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+// Eight values a thread.
+__global__ __launch_bounds__(256) void to_bf16_kernel(const float* __restrict__ x, int64_t R, int64_t chunks,
+                                                      uint16_t* __restrict__ y, int64_t ldy) {
+  const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x, r = q / chunks, c = 8 * (q - r * chunks);
+  if (r >= R) return;
+  const float4* src = reinterpret_cast<const float4*>(x + 8 * q);
+  const float4 a = src[0], b = src[1];
+  *reinterpret_cast<uint4*>(y + r * ldy + c) =
+      make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
+}
+
+template <class P>
+P head_params(const HeadParams& h) {
+  P p;
+  memset(&p, 0, sizeof p);
+  p.a_codes = h.a_codes;
+  p.a_scales = h.a_scales;
+  p.b_codes = h.b_codes;
+  p.b_scales = h.b_scales;
+  p.M = h.M;
+  p.N = h.V;
+  p.K = p.ktot = h.K;
+  p.b_group_rows = h.V;
+  p.labels = h.labels;
+  return p;
+}
+
+}  // namespace
+
+int64_t head_work_floats(int64_t M, int64_t V) { return (V + 127) / 128 * 2 * M + M; }
+
+hipError_t launch_head_loss(const HeadParams& h, int fmt, float* loss, float* lse, float* work, hipStream_t stream) {
+  HeadLossParams p = head_params<HeadLossParams>(h);
+  p.parts = reinterpret_cast<Part*>(work);
+  p.label_logit = work + (h.V + 127) / 128 * 2 * h.M;
+  const hipError_t e = launch_fmt(p, fmt, stream);
+  if (e != hipSuccess) return e;
+  const int width = tile_classes(h.M, h.V);
+  const int64_t tiles = (h.V + width - 1) / width;
+  // 16 tokens a workgroup read whole 128-byte lines of a tile's parts, where
+  // that leaves enough workgroups
+  if (h.M >= 2048)
+    hipLaunchKernelGGL(head_join_kernel<16>, dim3((unsigned)((h.M + 15) / 16)), dim3(256), 0, stream, p.parts, tiles,
+                       h.M, h.V, h.labels, p.label_logit, loss, lse);
+  else
+    hipLaunchKernelGGL(head_join_kernel<1>, dim3((unsigned)h.M), dim3(256), 0, stream, p.parts, tiles, h.M, h.V,
+                       h.labels, p.label_logit, loss, lse);
+  return hipGetLastError();
+}
+
+hipError_t launch_head_grad(const HeadParams& h, const HeadGradOut& o, int fmt, hipStream_t stream) {
+  HeadGradParams p = head_params<HeadGradParams>(h);
+  const int bits = fmt == kE2M1 ? 4 : fmt == kE2M3 ? 6 : 8;
+  p.b_codes = h.b_codes + o.first * 16 * bits;
+  p.b_scales = h.b_scales + o.first * 4;
+  p.N = o.count;
+  p.lse = o.lse;
+  p.dloss = o.dloss;
+  p.dloss_step = o.dloss_step;
+  p.first = o.first;
+  p.classes = h.V;
+  p.had = o.had;
+  p.q_row_codes = o.row_codes;
+  p.q_row_scales = o.row_scales;
+  p.q_col_codes = o.col_codes;
+  p.q_col_scales = o.col_scales;
+  return launch_fmt(p, fmt, stream);
+}
+
+hipError_t launch_to_bf16(const float* x, int64_t R, int64_t C, uint16_t* y, int64_t ldy, hipStream_t stream) {
+  const int64_t blocks = (R * (C / 8) + 255) / 256;
+  if (blocks >= (1ll << 32) / 256) return hipErrorInvalidValue;
+  if (blocks == 0) return hipSuccess;
+  hipLaunchKernelGGL(to_bf16_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, x, R, C / 8, y, ldy);
+  return hipGetLastError();
+}
+
+}  // namespace mx

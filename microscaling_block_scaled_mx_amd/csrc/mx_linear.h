@@ -12,6 +12,8 @@ namespace mx {
 
 // Dense GEMM epilogue of mx_gemm_act (beside those of mx_kernels.h).
 constexpr int kEpiAct = 5;
+// ... and one that the kernel's parameter type brings along.
+constexpr int kEpiOwn = 6;
 
 // C = act(A . B^T + bias) + residual for any M, N a multiple of 32 and K a
 // multiple of 32 (operands padded to whole K groups); c may be null when the

@@ -1,0 +1,144 @@
+// Internal launch interface of the training operators around the linears:
+// layer norm (mx_norm.hip), the vocabulary projection's cross entropy
+// (mx_head.hip) and the AdamW step (mx_adamw.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "mx_kernels.h"
+
+namespace mx {
+
+// ------------------------------------------------------------------ layer norm
+constexpr int64_t kNormMaxC = 16384;
+
+struct NormFwdParams {
+  const void* x;          // [M][ldx]
+  int64_t ldx;
+  const void* gamma;      // [C] or nullptr, both of one type
+  const void* beta;
+  void* y;                // [M][ldy] or nullptr
+  int64_t ldy;
+  float* mean;            // [M] or nullptr
+  float* rstd;
+  uint8_t* row_codes;     // [M] x K=C, or nullptr
+  uint8_t* row_scales;
+  uint8_t* saved_codes;   // E4M3 [M] x K=C, or nullptr
+  uint8_t* saved_scales;
+  int64_t M, C;
+  float eps, inv_c;
+  int w_f32, y_f32;
+  int fmt, mode, had;     // of the row operand
+};
+hipError_t launch_norm_fwd(const NormFwdParams& p, int x_f32, hipStream_t stream);
+
+struct NormBwdParams {
+  const void* dy;         // [M][lddy]
+  int64_t lddy;
+  const void* x;          // [M][ldx]
+  int64_t ldx;
+  const float* mean;
+  const float* rstd;
+  const void* gamma;      // [C] or nullptr
+  const void* residual;   // [M][ldr] of dx's type, or nullptr
+  int64_t ldr;
+  void* dx;               // [M][lddx] or nullptr
+  int64_t lddx;
+  float* partials;        // [norm_partial_rows][2][C], or nullptr: no weight gradients
+  int64_t M, C;
+  float inv_c;
+  int w_f32, dx_f32;
+};
+// Rows of partial weight gradients that the backward pass of M x C writes.
+int64_t norm_partial_rows(int64_t M, int64_t C);
+hipError_t launch_norm_bwd(const NormBwdParams& p, int x_f32, int dy_f32, hipStream_t stream);
+// dgamma, dbeta [C] (either nullptr) from `rows` partials, in order; added to
+// what they hold where `accumulate`.
+hipError_t launch_norm_weights(const float* partials, int64_t rows, int64_t C, float* dgamma, float* dbeta,
+                               int accumulate, hipStream_t stream);
+
+// ------------------------------------------------------------------ cross entropy
+// Logits l = A . B^T of M tokens and V classes, formed and consumed tile by
+// tile.
+struct HeadParams {
+  const uint8_t* a_codes;      // [M] x K
+  const uint8_t* a_scales;
+  const uint8_t* b_codes;      // [V] x K
+  const uint8_t* b_scales;
+  int64_t M, V, K;
+  const int64_t* labels;       // [M]; outside [0, V): the token has none
+};
+// loss and lse [M]; `work`: head_work_floats(M, V) floats.
+int64_t head_work_floats(int64_t M, int64_t V);
+hipError_t launch_head_loss(const HeadParams& p, int fmt, float* loss, float* lse, float* work, hipStream_t stream);
+
+// G = dloss (exp(l - lse) - [class = label]) of classes [first, first + count),
+// packed: rows [M] x K = count, columns [count] x K = M (either may be absent).
+struct HeadGradOut {
+  const float* lse;            // [M]
+  const float* dloss;          // [M] at dloss_step, or one value (0)
+  int64_t dloss_step;
+  int64_t first, count;
+  uint8_t* row_codes;
+  uint8_t* row_scales;
+  uint8_t* col_codes;
+  uint8_t* col_scales;
+  int had;
+};
+hipError_t launch_head_grad(const HeadParams& p, const HeadGradOut& o, int fmt, hipStream_t stream);
+// y [R][ldy] (bf16) = x [R][C] (binary32), C a multiple of 8.
+hipError_t launch_to_bf16(const float* x, int64_t R, int64_t C, uint16_t* y, int64_t ldy, hipStream_t stream);
+
+// ------------------------------------------------------------------ AdamW
+// What a step multiplies with, formed in binary64 and rounded once.
+struct AdamFactors {
+  float decay;      // 1 - lr weight_decay
+  float rate;       // lr / (1 - beta1^t)
+  float inv_root;   // 1 / sqrt(1 - beta2^t)
+  float eps;
+  float b1, g1;     // beta1, 1 - beta1
+  float b2, g2;     // beta2, 1 - beta2
+};
+// The step count on the device and the factors of the step under way.
+struct AdamState {
+  int64_t step;
+  AdamFactors f;
+};
+struct AdamHyper {
+  double lr, beta1, beta2, eps, weight_decay;
+};
+AdamFactors adam_factors(const AdamHyper& h, int64_t step);
+
+struct AdamItem {
+  float* p;
+  const void* g;
+  void* m;          // binary32 [n], or E4M3 codes [1] x K = n
+  void* v;
+  uint8_t* m_scales;
+  uint8_t* v_scales;
+  uint16_t* copy;   // bf16 [n] or nullptr
+  int64_t n;
+  int32_t g_f32;
+  uint32_t index;   // of the tensor, for its random words
+};
+// As many as the launch's arguments hold.
+constexpr int kAdamItems = 40;
+struct AdamParams {
+  AdamItem item[kAdamItems];
+  int first[kAdamItems];        // first workgroup of each; past the last item: INT_MAX
+  AdamFactors f;
+  const AdamState* state;       // on the device, or nullptr: f and step
+  const float* grad_scale;      // on the device, or nullptr
+  uint64_t seed;
+  uint32_t step;
+};
+static_assert(sizeof(AdamParams) <= 4096, "kernel arguments");
+constexpr int64_t kAdamChunk = 4096;  // elements a workgroup
+// Advances the device's step count and forms its factors; lr from the device
+// where given.
+hipError_t launch_adam_advance(AdamState* state, const AdamHyper& h, const float* lr, hipStream_t stream);
+// items: `count` <= kAdamItems filled in; `first` is filled in here.
+hipError_t launch_adam(AdamParams& p, int count, hipStream_t stream);
+
+}  // namespace mx

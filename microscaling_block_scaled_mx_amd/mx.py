@@ -111,6 +111,57 @@ class LinearBwdArgs(ctypes.Structure):
                 ("dw_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32), ("db", ctypes.c_void_p),
                 ("db_partials", ctypes.c_void_p), ("dPr", Packed), ("dPc", Packed), ("Xc", Packed)]
 
+
+class LayernormFwdArgs(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("C", ctypes.c_int64), ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("gamma", ctypes.c_void_p), ("beta", ctypes.c_void_p), ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+                ("mean", ctypes.c_void_p), ("rstd", ctypes.c_void_p), ("row", Packed), ("saved", Packed),
+                ("eps", ctypes.c_float), ("x_dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32),
+                ("w_dtype", ctypes.c_int32), ("fmt", ctypes.c_int32), ("scale_mode", ctypes.c_int32),
+                ("hadamard", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class LayernormBwdArgs(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("C", ctypes.c_int64), ("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64),
+                ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("mean", ctypes.c_void_p), ("rstd", ctypes.c_void_p),
+                ("gamma", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+                ("dx", ctypes.c_void_p), ("lddx", ctypes.c_int64), ("dgamma", ctypes.c_void_p),
+                ("dbeta", ctypes.c_void_p), ("partials", ctypes.c_void_p), ("dy_dtype", ctypes.c_int32),
+                ("x_dtype", ctypes.c_int32), ("dx_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
+                ("accumulate", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class HeadLossArgs(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("V", ctypes.c_int64), ("K", ctypes.c_int64), ("fmt", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("A", Packed), ("B", Packed), ("labels", ctypes.c_void_p),
+                ("loss", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("work", ctypes.c_void_p)]
+
+
+class HeadLossBwdArgs(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("V", ctypes.c_int64), ("K", ctypes.c_int64), ("fmt", ctypes.c_int32),
+                ("scale_mode", ctypes.c_int32), ("hadamard", ctypes.c_int32), ("accumulate", ctypes.c_int32),
+                ("A", Packed), ("B", Packed), ("Wc", Packed), ("Xc", Packed), ("labels", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p), ("dloss", ctypes.c_void_p), ("dloss_step", ctypes.c_int64),
+                ("dX", ctypes.c_void_p), ("lddx", ctypes.c_int64), ("dW", ctypes.c_void_p), ("lddw", ctypes.c_int64),
+                ("dw_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32), ("Gr", Packed), ("Gc", Packed),
+                ("piece", ctypes.c_int64), ("sums", ctypes.c_void_p)]
+
+
+class AdamwItem(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("g", ctypes.c_void_p), ("m", Packed), ("v", Packed),
+                ("copy", ctypes.c_void_p), ("n", ctypes.c_int64), ("g_dtype", ctypes.c_int32),
+                ("state_bits", ctypes.c_int32)]
+
+
+class AdamwArgs(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64),
+                ("seed", ctypes.c_uint64), ("state", ctypes.c_void_p), ("lr_device", ctypes.c_void_p),
+                ("grad_scale", ctypes.c_void_p)]
+
+
+ADAMW_STATE_BYTES = 64  # MX_ADAMW_STATE_BYTES
+
 _lib = None
 
 
@@ -160,6 +211,20 @@ def lib():
         L.mx_quantize_saved.argtypes = [vp, vp]
         L.mx_linear_bwd_saved.restype = ci
         L.mx_linear_bwd_saved.argtypes = [vp, vp]
+        L.mx_layernorm_fwd.restype = ci
+        L.mx_layernorm_fwd.argtypes = [vp, vp]
+        L.mx_layernorm_bwd.restype = ci
+        L.mx_layernorm_bwd.argtypes = [vp, vp]
+        L.mx_layernorm_partial_rows.restype = i64
+        L.mx_layernorm_partial_rows.argtypes = [i64, i64]
+        L.mx_head_loss.restype = ci
+        L.mx_head_loss.argtypes = [vp, vp]
+        L.mx_head_loss_bwd.restype = ci
+        L.mx_head_loss_bwd.argtypes = [vp, vp]
+        L.mx_head_loss_work_bytes.restype = i64
+        L.mx_head_loss_work_bytes.argtypes = [i64, i64]
+        L.mx_adamw.restype = ci
+        L.mx_adamw.argtypes = [vp, i64, vp, vp]
         L.mx_status_str.restype = ctypes.c_char_p
         L.mx_status_str.argtypes = [ci]
         L.mx_device_supported.restype = ci
@@ -493,7 +558,8 @@ def device_supported(device: int = 0) -> bool:
 def _packer(cls):
     """struct.pack of the fields of an argument struct (Packed as two
     addresses), with the C layout."""
-    code = {ctypes.c_int64: "q", ctypes.c_int32: "i", ctypes.c_void_p: "P", Packed: "PP"}
+    code = {ctypes.c_int64: "q", ctypes.c_uint64: "Q", ctypes.c_int32: "i", ctypes.c_float: "f", ctypes.c_double: "d",
+            ctypes.c_void_p: "P", Packed: "PP"}
     s = struct.Struct("@" + "".join(code[t] for _, t in cls._fields_) + "0q")
     assert s.size == ctypes.sizeof(cls)
     return s.pack
@@ -502,6 +568,11 @@ def _packer(cls):
 _pack_gemm_act = _packer(GemmActArgs)
 _pack_quantize_saved = _packer(QuantizeSavedArgs)
 _pack_linear_bwd = _packer(LinearBwdArgs)
+_pack_layernorm_fwd = _packer(LayernormFwdArgs)
+_pack_layernorm_bwd = _packer(LayernormBwdArgs)
+_pack_head_loss = _packer(HeadLossArgs)
+_pack_head_loss_bwd = _packer(HeadLossBwdArgs)
+_pack_adamw = _packer(AdamwArgs)
 
 
 def _current():
@@ -647,6 +718,182 @@ def linear_bwd_saved(M: int, N: int, K: int, dY, saved_x, Wc, fmt: int, scale_mo
                             *_operand(dPc, N, Mp, fmt, dev, "linear_bwd_saved dPc"),
                             *_operand(Xc, K, Mp, fmt, dev, "linear_bwd_saved Xc"))
     _check(lib().mx_linear_bwd_saved(args, _handle(stream, here)), "mx_linear_bwd_saved")
+
+
+# ---------------------------------------------------------------- training operators
+def layernorm_fwd(x, y=None, gamma=None, beta=None, eps: float = 1e-5, mean=None, rstd=None, row=None, fmt: int = E4M3,
+                  scale_mode: int = RCEIL, hadamard: bool = False, saved=None, stream=None):
+    """mx_layernorm_fwd: y [M][C] = (x - mean) rstd gamma + beta (x, y each
+    bf16 or float32, rows dense; gamma and beta [C] of one type), mean and rstd
+    float32 [M]; row = (codes, scales) of alloc_packed(M, C, fmt), saved of
+    alloc_packed(M, C, E4M3).  Any of the outputs may be left out."""
+    M, C = x.shape
+    dev, here = _current()
+    xp, ldx, x_dtype = _matrix(x, M, C, dev, "layernorm_fwd x")
+    yp, ldy, y_dtype = _matrix(y, M, C, dev, "layernorm_fwd y")
+    gp, _, w_dtype = _matrix(gamma, 1, C, dev, "layernorm_fwd gamma")
+    bp, _, b_dtype = _matrix(beta, 1, C, dev, "layernorm_fwd beta")
+    if gamma is None:
+        w_dtype = b_dtype
+    elif beta is not None and b_dtype != w_dtype:
+        raise MXError(4, "layernorm_fwd: gamma and beta are of different types")
+    mp, _, _ = _matrix(mean, 1, M, dev, "layernorm_fwd mean", (F32,))
+    rp, _, _ = _matrix(rstd, 1, M, dev, "layernorm_fwd rstd", (F32,))
+    args = _pack_layernorm_fwd(M, C, xp, ldx, gp, bp, yp, ldy, mp, rp, *_operand(row, M, C, fmt, dev, "layernorm_fwd row"),
+                               *_operand(saved, M, C, E4M3, dev, "layernorm_fwd saved"), eps, x_dtype, y_dtype, w_dtype,
+                               fmt, scale_mode, int(hadamard), 0)
+    _check(lib().mx_layernorm_fwd(args, _handle(stream, here)), "mx_layernorm_fwd")
+
+
+def layernorm_partial_rows(M: int, C: int) -> int:
+    """Rows of layernorm_bwd's partials, float32 [rows][2][C]."""
+    return lib().mx_layernorm_partial_rows(M, C)
+
+
+def layernorm_bwd(dy, x, mean, rstd, dx=None, gamma=None, residual=None, dgamma=None, dbeta=None, partials=None,
+                  accumulate: bool = False, stream=None):
+    """mx_layernorm_bwd: dx [M][C] (+ residual, of one type with dx), dgamma and
+    dbeta float32 [C], each optional; partials float32 of at least
+    layernorm_partial_rows(M, C) * 2 * C elements for the latter two."""
+    M, C = x.shape
+    dev, here = _current()
+    yp, lddy, dy_dtype = _matrix(dy, M, C, dev, "layernorm_bwd dy")
+    xp, ldx, x_dtype = _matrix(x, M, C, dev, "layernorm_bwd x")
+    op, lddx, dx_dtype = _matrix(dx, M, C, dev, "layernorm_bwd dx")
+    rp, ldr, r_dtype = _matrix(residual, M, C, dev, "layernorm_bwd residual")
+    if residual is not None and dx is not None and r_dtype != dx_dtype:
+        raise MXError(4, "layernorm_bwd: residual and dx are of different types")
+    gp, _, w_dtype = _matrix(gamma, 1, C, dev, "layernorm_bwd gamma")
+    dgp, _, _ = _matrix(dgamma, 1, C, dev, "layernorm_bwd dgamma", (F32,))
+    dbp, _, _ = _matrix(dbeta, 1, C, dev, "layernorm_bwd dbeta", (F32,))
+    mp, _, _ = _matrix(mean, 1, M, dev, "layernorm_bwd mean", (F32,))
+    sp, _, _ = _matrix(rstd, 1, M, dev, "layernorm_bwd rstd", (F32,))
+    pp = _work(partials, 8 * C * lib().mx_layernorm_partial_rows(M, C), dev, "layernorm_bwd partials")
+    args = _pack_layernorm_bwd(M, C, yp, lddy, xp, ldx, mp, sp, gp, rp, ldr, op, lddx, dgp, dbp, pp, dy_dtype, x_dtype,
+                               dx_dtype, w_dtype, int(accumulate), 0)
+    _check(lib().mx_layernorm_bwd(args, _handle(stream, here)), "mx_layernorm_bwd")
+
+
+def _work(t, nbytes: int, dev: int, what: str):
+    """Address of a work buffer of at least nbytes, or 0."""
+    if t is None:
+        return 0
+    if not t.is_contiguous():
+        raise MXError(2, f"{what}: tensor argument is a strided view; pass a contiguous tensor")
+    _need(t, nbytes, what)
+    if t.get_device() != dev or dev < 0:
+        _refuse_device(t, dev, what)
+    return t.data_ptr()
+
+
+def _labels(t, M: int, dev: int, what: str):
+    if t.dtype != torch.int64 or t.numel() != M or not t.is_contiguous():
+        raise MXError(2, f"{what}: labels are a contiguous int64 tensor of {M}")
+    if t.get_device() != dev or dev < 0:
+        _refuse_device(t, dev, what)
+    return t.data_ptr()
+
+
+def head_loss_work_bytes(M: int, V: int) -> int:
+    """Bytes of head_loss's work buffer."""
+    return lib().mx_head_loss_work_bytes(M, V)
+
+
+def head_loss(a, b, M: int, V: int, K: int, fmt: int, labels, loss, lse, work, stream=None):
+    """mx_head_loss: loss and lse float32 [M] of the logits A . B^T [M][V] under
+    labels int64 [M] (outside [0, V): none); work: any tensor of at least
+    head_loss_work_bytes(M, V)."""
+    dev, here = _current()
+    lp, _, _ = _matrix(loss, 1, M, dev, "head_loss loss", (F32,))
+    sp, _, _ = _matrix(lse, 1, M, dev, "head_loss lse", (F32,))
+    args = _pack_head_loss(M, V, K, fmt, 0, *_operand(a, M, K, fmt, dev, "head_loss A"),
+                           *_operand(b, V, K, fmt, dev, "head_loss B"), _labels(labels, M, dev, "head_loss"), lp, sp,
+                           _work(work, lib().mx_head_loss_work_bytes(M, V), dev, "head_loss work"))
+    _check(lib().mx_head_loss(args, _handle(stream, here)), "mx_head_loss")
+
+
+def head_loss_bwd(a, b, Wc, Xc, M: int, V: int, K: int, fmt: int, scale_mode: int, labels, lse, dloss, dX=None, dW=None,
+                  Gr=None, Gc=None, piece: int = 16384, sums=None, hadamard: bool = False, accumulate: bool = False,
+                  stream=None):
+    """mx_head_loss_bwd: dX [M][K] (bf16) and dW [V][K] (bf16 or float32), each
+    optional.  dloss float32: [M], or one value for every token.  Wc [K] x K = V
+    rounded up to 32 and Xc [K] x K = M rounded up to 32, the columns of W and X.
+    Work: Gr of alloc_packed(M, min(piece, V) rounded up to 32, fmt) for dX, Gc of
+    alloc_packed(min(piece, V), M rounded up to 32, fmt) for dW, sums float32
+    [M][K] for dX where V > piece."""
+    dev, here = _current()
+    xp, lddx, _ = _matrix(dX, M, K, dev, "head_loss_bwd dX", (BF16,))
+    wp, lddw, dw_dtype = _matrix(dW, V, K, dev, "head_loss_bwd dW")
+    sp, _, _ = _matrix(lse, 1, M, dev, "head_loss_bwd lse", (F32,))
+    n = dloss.numel()
+    if n != M and n != 1:
+        raise MXError(2, f"head_loss_bwd dloss: {n} values for {M} tokens")
+    dp, _, _ = _matrix(dloss, 1, n, dev, "head_loss_bwd dloss", (F32,))
+    Mp, Vp, part = _rows32(M), _rows32(V), min(piece, V)
+    args = _pack_head_loss_bwd(M, V, K, fmt, scale_mode, int(hadamard), int(accumulate),
+                               *_operand(a, M, K, fmt, dev, "head_loss_bwd A"),
+                               *_operand(b, V, K, fmt, dev, "head_loss_bwd B"),
+                               *_operand(Wc, K, Vp, fmt, dev, "head_loss_bwd Wc"),
+                               *_operand(Xc, K, Mp, fmt, dev, "head_loss_bwd Xc"),
+                               _labels(labels, M, dev, "head_loss_bwd"), sp, dp, int(n == M and n != 1), xp, lddx, wp,
+                               lddw, dw_dtype, 0, *_operand(Gr, M, _rows32(part), fmt, dev, "head_loss_bwd Gr"),
+                               *_operand(Gc, part, Mp, fmt, dev, "head_loss_bwd Gc"), piece,
+                               _work(sums, 4 * M * K, dev, "head_loss_bwd sums"))
+    _check(lib().mx_head_loss_bwd(args, _handle(stream, here)), "mx_head_loss_bwd")
+
+
+class AdamwItems:
+    """The tensors of adamw, checked and laid out for mx_adamw once: make it
+    anew when a tensor is replaced (it keeps the tensors alive)."""
+
+    def __init__(self, items):
+        self.tensors = items = [dict(it) for it in items]
+        self.array = (AdamwItem * max(len(items), 1))()
+        self.n = len(items)
+        self.device = _current()[0]
+        for i, it in enumerate(items):
+            self.array[i] = self._item(it, f"adamw item {i}")
+
+    def _item(self, it, what):
+        n, dev = it["p"].numel(), self.device
+        state = []
+        for key in ("m", "v"):
+            t = it[key]
+            if isinstance(t, torch.Tensor):
+                state.append((32, Packed(_matrix(t, 1, n, dev, f"{what} {key}", (F32,))[0], None)))
+            else:
+                state.append((8, Packed(*_operand(t, 1, _rows32(n), E4M3, dev, f"{what} {key}"))))
+        if state[0][0] != state[1][0]:
+            raise MXError(4, f"{what}: m and v are kept in different ways")
+        g, _, g_dtype = _matrix(it["g"], 1, n, dev, what + " g")
+        return AdamwItem(_matrix(it["p"], 1, n, dev, what + " p", (F32,))[0], g, state[0][1], state[1][1],
+                         _matrix(it.get("copy"), 1, n, dev, what + " copy", (BF16,))[0], n, g_dtype, state[0][0])
+
+
+def adamw_items(items) -> AdamwItems:
+    """The tensors of an optimizer for adamw: each a dict of p (float32), g
+    (bf16 or float32), m and v (both float32, or both (codes, scales) of
+    alloc_packed(1, n rounded up to 32, E4M3), zeroed before the first step) and
+    optionally copy (bf16), all of one length and contiguous."""
+    return AdamwItems(items)
+
+
+def adamw(items, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.0,
+          step: int = 0, seed: int = 0, state=None, lr_device=None, grad_scale=None, stream=None):
+    """mx_adamw: one step over adamw_items(...) (or a list that it takes), in
+    place.  step counts from 1; or state, a zeroed device tensor of
+    ADAMW_STATE_BYTES, counts it on the device.  lr_device and grad_scale: float32
+    device tensors of one element."""
+    if not isinstance(items, AdamwItems):
+        items = AdamwItems(items)
+    dev, here = _current()
+    if items.n and items.device != dev:
+        raise MXError(7, f"adamw: the tensors are on cuda:{items.device}, the current device is cuda:{dev}")
+    args = _pack_adamw(lr, beta1, beta2, eps, weight_decay, step, seed & 0xFFFFFFFFFFFFFFFF,
+                       _work(state, ADAMW_STATE_BYTES, dev, "adamw state"),
+                       _matrix(lr_device, 1, 1, dev, "adamw lr_device", (F32,))[0],
+                       _matrix(grad_scale, 1, 1, dev, "adamw grad_scale", (F32,))[0])
+    _check(lib().mx_adamw(items.array, items.n, args, _handle(stream, here)), "mx_adamw")
 
 
 def status_str(st: int) -> str:

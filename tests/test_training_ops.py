@@ -1,0 +1,1123 @@
+"""The training operators (mx_layernorm_fwd / _bwd, mx_head_loss / _bwd,
+mx_adamw) against plain implementations in 64 bits, their refusals, and a step
+of them together.
+
+Tolerances.  u = 2^-24 is half a step of binary32, relative; a rounding to
+bf16 is off by at most 2^-8 of the value, one to E4M3 2^-4 (or 2^-10 of the
+block's scale), E2M3 1/16 of the block's scale below 2 of it and then 2^-4 of the
+value, E2M1 1/4 of the scale below 2 of it and then 2^-2 of the value.
+
+Layer norm: a row's sum has at most 64 roundings on any value's way (16 values
+a thread in order, six steps of a wavefront, at most 16 wavefronts), so mean is
+within 64 u max|x| and, the sum of squares likewise, rstd within 70 u of itself
+(beside the second order of the mean's error); h = (x - mean) rstd is within
+E_h = u (66 rstd max|x| + 72 |h|).
+
+Cross entropy: on operands of small integers under one scale every logit is
+exact.  An exponential is off by 2 u (exp2, 1 ulp) and by the rounding of its
+argument, |l - max| log2(e) u, times ln 2; log2(e) itself is off by under u / 2 of
+the argument; a sum over V classes has at most 32 + 8 + V / 128 + 16 roundings on
+any value's way.  Those relative errors of the sum are absolute ones of lse,
+which adds three roundings of its own."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from microscaling_block_scaled_mx_amd import mx
+from parity_checks import REL
+from test_linear_ops import (FMTS, code_values, codes_of, decode, dev_bf16, exact_operand, f64, operand, quantised64)
+from packed_layout import unblocked, untiled
+
+gpu = pytest.mark.gpu
+U = 2.0 ** -24
+BF16_STEP = 2.0 ** -8
+P = [ctypes.c_void_p(0x1000 * (i + 1)) for i in range(24)]
+ODD = ctypes.c_void_p(0x1004)
+NULL, SHAPE, ALIGN, FORMAT, OVERFLOW, DEVICE = 1, 2, 3, 4, 6, 7
+NONE = mx.Packed(None, None)
+OK_HERE = 0 if torch.cuda.is_available() else DEVICE
+
+
+def pk(i):
+    return mx.Packed(P[i], P[i + 1])
+
+
+def struct_of(cls, base, kw):
+    a = {f: 0 for f, _ in cls._fields_}
+    a.update(base)
+    a.update(kw)
+    return cls(*[a[f] for f, _ in cls._fields_])
+
+
+@pytest.fixture(scope="module", autouse=True)
+def need_device(request):
+    if torch.cuda.is_available():
+        assert mx.device_supported(0)
+
+
+# ---------------------------------------------------------------- refusals (no GPU call)
+def norm_fwd_args(**kw):
+    return struct_of(mx.LayernormFwdArgs, dict(M=5, C=64, x=P[0], ldx=64, gamma=P[1], beta=P[2], y=P[3], ldy=64, mean=P[4],
+                                               rstd=P[5], row=pk(6), saved=pk(8), eps=1e-5, fmt=mx.E2M3, hadamard=1), kw)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(x_dtype=2), FORMAT), (dict(y_dtype=-1), FORMAT), (dict(w_dtype=3), FORMAT), (dict(fmt=0), FORMAT),
+    (dict(fmt=mx.E2M1), FORMAT), (dict(scale_mode=1), FORMAT), (dict(hadamard=2), FORMAT),
+    (dict(M=-1), SHAPE), (dict(C=0), SHAPE), (dict(C=-8), SHAPE), (dict(C=60), SHAPE), (dict(C=72, ldx=72, ldy=72), SHAPE),
+    (dict(C=16416, ldx=16416, ldy=16416), SHAPE), (dict(eps=-1e-9), SHAPE), (dict(eps=float("nan")), SHAPE),
+    (dict(eps=float("inf")), SHAPE), (dict(ldx=56), SHAPE), (dict(ldx=68), SHAPE), (dict(ldy=32), SHAPE),
+    (dict(x=None), NULL), (dict(row=mx.Packed(P[0], None)), NULL), (dict(saved=mx.Packed(None, P[0])), NULL),
+    (dict(y=None, mean=None, rstd=None, row=NONE, saved=NONE), NULL),
+    (dict(x=ODD), ALIGN), (dict(gamma=ODD), ALIGN), (dict(mean=ODD), ALIGN), (dict(saved=mx.Packed(ODD, P[0])), ALIGN),
+    (dict(M=1 << 41), OVERFLOW), (dict(M=1 << 39, ldx=1 << 30), OVERFLOW), (dict(ldy=1 << 60), OVERFLOW),
+])
+def test_layernorm_fwd_refusals(kw, want):
+    assert mx.lib().mx_layernorm_fwd(ctypes.byref(norm_fwd_args(**kw)), None) == want
+
+
+def norm_bwd_args(**kw):
+    return struct_of(mx.LayernormBwdArgs, dict(M=5, C=64, dy=P[0], lddy=64, x=P[1], ldx=64, mean=P[2], rstd=P[3], gamma=P[4],
+                                               residual=P[5], ldr=64, dx=P[6], lddx=64, dgamma=P[7], dbeta=P[8],
+                                               partials=P[9]), kw)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(dy_dtype=2), FORMAT), (dict(x_dtype=2), FORMAT), (dict(dx_dtype=2), FORMAT), (dict(w_dtype=2), FORMAT),
+    (dict(accumulate=2), FORMAT), (dict(M=-1), SHAPE), (dict(C=12), SHAPE), (dict(C=16392), SHAPE), (dict(lddy=8), SHAPE),
+    (dict(ldr=66), SHAPE), (dict(lddx=63), SHAPE), (dict(residual=P[6], ldr=72), SHAPE),
+    (dict(dy=None), NULL), (dict(x=None), NULL), (dict(mean=None), NULL), (dict(rstd=None), NULL),
+    (dict(partials=None), NULL), (dict(dx=None), NULL), (dict(dx=None, residual=None, dgamma=None, dbeta=None), NULL),
+    (dict(partials=ODD), ALIGN), (dict(dgamma=ODD), ALIGN), (dict(residual=ODD), ALIGN),
+    (dict(M=1 << 41), OVERFLOW), (dict(lddx=1 << 60), OVERFLOW),
+])
+def test_layernorm_bwd_refusals(kw, want):
+    assert mx.lib().mx_layernorm_bwd(ctypes.byref(norm_bwd_args(**kw)), None) == want
+
+
+def head_args(**kw):
+    return struct_of(mx.HeadLossArgs, dict(M=5, V=100, K=96, fmt=mx.E4M3, A=pk(0), B=pk(2), labels=P[4], loss=P[5], lse=P[6],
+                                           work=P[7]), kw)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(fmt=0), FORMAT), (dict(fmt=4), FORMAT), (dict(M=-1), SHAPE), (dict(V=0), SHAPE), (dict(K=0), SHAPE),
+    (dict(K=100), SHAPE), (dict(K=-32), SHAPE), (dict(A=NONE), NULL), (dict(B=mx.Packed(P[0], None)), NULL),
+    (dict(labels=None), NULL), (dict(loss=None), NULL), (dict(lse=None), NULL), (dict(work=None), NULL),
+    (dict(labels=ODD), ALIGN), (dict(work=ODD), ALIGN), (dict(A=mx.Packed(ODD, P[0])), ALIGN),
+    (dict(V=1 << 31), OVERFLOW), (dict(V=1 << 20, K=2048), OVERFLOW), (dict(M=1 << 20, K=2048), OVERFLOW),
+    (dict(K=1 << 40), OVERFLOW), (dict(M=1 << 24, V=1 << 24, K=32), OVERFLOW),
+])
+def test_head_loss_refusals(kw, want):
+    assert mx.lib().mx_head_loss(ctypes.byref(head_args(**kw)), None) == want
+
+
+def head_bwd_args(**kw):
+    return struct_of(mx.HeadLossBwdArgs, dict(
+        M=5, V=300, K=96, fmt=mx.E4M3, scale_mode=mx.RCEIL, A=pk(0), B=pk(2), Wc=pk(4), Xc=pk(6), labels=P[8], lse=P[9],
+        dloss=P[10], dloss_step=1, dX=P[11], lddx=96, dW=P[12], lddw=96, Gr=pk(13), Gc=pk(15), piece=128, sums=P[17]), kw)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(fmt=0), FORMAT), (dict(scale_mode=mx.FLOOR), FORMAT), (dict(fmt=mx.E2M3), FORMAT), (dict(hadamard=1), FORMAT),
+    (dict(accumulate=2), FORMAT), (dict(dw_dtype=2), FORMAT), (dict(M=-1), SHAPE), (dict(V=0), SHAPE), (dict(K=40), SHAPE),
+    (dict(piece=0), SHAPE), (dict(piece=100), SHAPE), (dict(piece=-128), SHAPE), (dict(dloss_step=2), SHAPE),
+    (dict(lddx=88), SHAPE), (dict(lddw=100), SHAPE),
+    (dict(A=NONE), NULL), (dict(B=NONE), NULL), (dict(Wc=NONE), NULL), (dict(Xc=NONE), NULL), (dict(Gr=NONE), NULL),
+    (dict(Gc=NONE), NULL), (dict(sums=None), NULL), (dict(labels=None), NULL), (dict(lse=None), NULL),
+    (dict(dloss=None), NULL), (dict(dX=None, dW=None), NULL),
+    (dict(lse=ODD), ALIGN), (dict(dloss=ctypes.c_void_p(0x1002)), ALIGN), (dict(sums=ODD), ALIGN), (dict(dX=ODD), ALIGN),
+    (dict(Gr=mx.Packed(ODD, P[0])), ALIGN), (dict(Gc=mx.Packed(P[0], ODD)), ALIGN),
+    (dict(M=1 << 26, V=1 << 20, piece=1 << 20, K=32, lddx=32, lddw=32), OVERFLOW),
+    (dict(M=1 << 20, V=4096, piece=4096, K=32, lddx=32, lddw=32), OVERFLOW), (dict(V=1 << 25, K=96), OVERFLOW),
+])
+def test_head_loss_bwd_refusals(kw, want):
+    assert mx.lib().mx_head_loss_bwd(ctypes.byref(head_bwd_args(**kw)), None) == want
+
+
+def adamw_refusal(item=(), args=(), n=1):
+    it = struct_of(mx.AdamwItem, dict(p=P[0], g=P[1], m=pk(2), v=pk(4), copy=P[6], n=100, state_bits=8), dict(item))
+    a = struct_of(mx.AdamwArgs, dict(lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8, step=1), dict(args))
+    return mx.lib().mx_adamw(ctypes.byref(it), n, ctypes.byref(a), None)
+
+
+@pytest.mark.parametrize("item,args,want", [
+    (dict(g_dtype=2), {}, FORMAT), (dict(state_bits=16), {}, FORMAT), (dict(n=-1), {}, SHAPE), (dict(n=(1 << 34) + 1), {}, OVERFLOW),
+    (dict(p=None), {}, NULL), (dict(g=None), {}, NULL), (dict(m=NONE), {}, NULL), (dict(v=mx.Packed(P[0], None)), {}, NULL),
+    (dict(state_bits=32), {}, NULL), (dict(p=ODD), {}, ALIGN), (dict(g=ODD), {}, ALIGN), (dict(copy=ODD), {}, ALIGN),
+    (dict(m=mx.Packed(P[0], ODD)), {}, ALIGN),
+    ({}, dict(beta1=1.0), SHAPE), ({}, dict(beta2=-0.1), SHAPE), ({}, dict(beta1=float("nan")), SHAPE),
+    ({}, dict(lr=-1e-3), SHAPE), ({}, dict(lr=float("nan")), SHAPE), ({}, dict(eps=float("inf")), SHAPE),
+    ({}, dict(weight_decay=-0.1), SHAPE), ({}, dict(step=0), SHAPE), ({}, dict(step=-3), SHAPE),
+    ({}, dict(state=ODD), ALIGN), ({}, dict(grad_scale=ctypes.c_void_p(0x1002)), ALIGN),
+    ({}, dict(state=P[7], lr_device=ctypes.c_void_p(0x1001)), ALIGN), ({}, dict(lr_device=P[7]), NULL),
+])
+def test_adamw_refusals(item, args, want):
+    assert adamw_refusal(item, args) == want
+
+
+def test_adamw_item_counts():
+    assert adamw_refusal(n=-1) == SHAPE
+    assert adamw_refusal(n=1000001) == SHAPE
+    a = struct_of(mx.AdamwArgs, dict(lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8, step=1), {})
+    assert mx.lib().mx_adamw(None, 1, ctypes.byref(a), None) == NULL
+    assert mx.lib().mx_adamw(None, 0, None, None) == NULL
+    assert mx.lib().mx_adamw(None, 0, ctypes.byref(a), None) == OK_HERE
+    assert adamw_refusal(dict(n=0, p=None, g=None, m=NONE, v=NONE)) == OK_HERE
+
+
+def test_no_tokens_need_no_pointers():
+    L = mx.lib()
+    empty = norm_fwd_args(M=0, x=None, y=None, mean=None, rstd=None, row=NONE, saved=NONE)
+    assert L.mx_layernorm_fwd(ctypes.byref(empty), None) == OK_HERE
+    assert L.mx_head_loss(ctypes.byref(head_args(M=0, A=NONE, B=NONE, labels=None, loss=None, lse=None, work=None)), None) == OK_HERE
+    assert L.mx_layernorm_fwd(None, None) == L.mx_layernorm_bwd(None, None) == NULL
+    assert L.mx_head_loss(None, None) == L.mx_head_loss_bwd(None, None) == NULL
+
+
+def test_sizes_of_work_buffers():
+    L = mx.lib()
+    assert [L.mx_layernorm_partial_rows(m, c) for m, c in ((1, 64), (9, 64), (1 << 30, 16384), (3, 16384), (3, 12), (-1, 64))] == \
+        [1, 2, 256, 3, 0, 0]
+    assert L.mx_layernorm_partial_rows(0, 64) == 0
+    assert L.mx_head_loss_work_bytes(10, 128) == 4 * 30 and L.mx_head_loss_work_bytes(10, 129) == 4 * 50
+    assert L.mx_head_loss_work_bytes(-1, 5) == L.mx_head_loss_work_bytes(5, 0) == 0
+
+
+def test_binding_refuses_host_tensors():
+    x = torch.zeros(4, 64)
+    with pytest.raises(mx.MXError):
+        mx.layernorm_fwd(x, x.clone())
+    with pytest.raises(mx.MXError):
+        mx.adamw([{"p": x, "g": x, "m": x, "v": x}], lr=1e-3, step=1)
+    with pytest.raises(mx.MXError):
+        mx.head_loss(None, None, 4, 10, 32, mx.E4M3, torch.zeros(4, dtype=torch.int32), x, x, x)
+
+
+# ---------------------------------------------------------------- layer norm
+def tensor(rng, shape, dtype, std=1.0, offset=0.0):
+    x = torch.from_numpy((rng.standard_normal(shape) * std + offset).astype(np.float32))
+    return (x.bfloat16() if dtype == mx.BF16 else x).cuda()
+
+
+def torch_type(dtype):
+    return torch.bfloat16 if dtype == mx.BF16 else torch.float32
+
+
+def norm64(x, gamma, beta, eps):
+    mean = x.mean(1, keepdims=True)
+    rstd = 1 / np.sqrt(((x - mean) ** 2).mean(1, keepdims=True) + eps)
+    h = (x - mean) * rstd
+    return h * (1 if gamma is None else gamma) + (0 if beta is None else beta), mean, rstd, h
+
+
+def h_error(x, rstd, h):
+    return U * (66 * rstd * np.abs(x).max(1, keepdims=True) + 72 * np.abs(h))
+
+
+def check_norm(x, y, gamma, beta, mean, rstd, eps, y_dtype):
+    g, b = None if gamma is None else f64(gamma), None if beta is None else f64(beta)
+    want, m64, r64, h = norm64(f64(x), g, b, eps)
+    if mean is not None:
+        assert (np.abs(f64(mean) - m64[:, 0]) <= 64 * U * np.abs(f64(x)).max(1)).all()
+        assert (np.abs(f64(rstd) / r64[:, 0] - 1) <= 72 * U).all()
+    tol = h_error(f64(x), r64, h) * (1 if g is None else np.abs(g)) + 2 * U * np.abs(want)
+    tol = tol + (BF16_STEP * (np.abs(want) + tol) if y_dtype == mx.BF16 else 0)
+    assert (np.abs(f64(y) - want) <= tol).all()
+
+
+WIDTHS = [8, 64, 520, 776, 1024, 1032, 2048, 2080, 4096, 4104, 8192, 8200, 16384]
+
+
+@gpu
+@pytest.mark.parametrize("C", WIDTHS)
+@pytest.mark.parametrize("x_dtype,y_dtype,w_dtype", [(0, 0, 0), (1, 1, 1), (0, 1, 1), (1, 0, 0)])
+def test_layernorm_widths_and_types(C, x_dtype, y_dtype, w_dtype):
+    rng = np.random.default_rng(C + x_dtype)
+    for M in (1, 7):
+        x = tensor(rng, (M, C), x_dtype, 2.0, 0.5)
+        gamma, beta = tensor(rng, (C,), w_dtype, 0.2, 1.0), tensor(rng, (C,), w_dtype)
+        y = torch.empty(M, C, dtype=torch_type(y_dtype), device="cuda")
+        mean, rstd = torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+        mx.layernorm_fwd(x, y, gamma, beta, 1e-5, mean, rstd)
+        check_norm(x, y, gamma, beta, mean, rstd, 1e-5, y_dtype)
+
+
+@gpu
+@pytest.mark.parametrize("M,C", [(2500, 96), (4999, 1024), (3001, 2080), (1500, 4096), (1027, 8192), (600, 12000)])
+def test_layernorm_many_rows(M, C):
+    """Workgroups that walk over several rows, an uneven number each."""
+    rng = np.random.default_rng(M)
+    x, gamma = tensor(rng, (M, C), mx.BF16, 1.0, -0.3), tensor(rng, (C,), mx.BF16, 0.2, 1.0)
+    y = torch.empty(M, C, dtype=torch.bfloat16, device="cuda")
+    mx.layernorm_fwd(x, y, gamma)
+    check_norm(x, y, gamma, None, None, None, 1e-5, mx.BF16)
+
+
+@gpu
+@pytest.mark.parametrize("fmt,mode,had", FMTS + [(mx.E2M3, mx.FLOOR, False), (mx.E4M3, mx.FLOOR, False)])
+@pytest.mark.parametrize("M,C", [(1, 32), (5, 96), (33, 160), (70, 2080), (9, 4096), (3, 16384)])
+def test_layernorm_packs(M, C, fmt, mode, had):
+    """row and saved are the packs of y in bf16, byte for byte (pads included), with or without y."""
+    rng = np.random.default_rng(M * C)
+    x = tensor(rng, (M, C), mx.F32, 1.0) * torch.exp(2 * tensor(rng, (1, C), mx.F32))
+    gamma, beta = tensor(rng, (C,), mx.F32, 0.5, 1.0), tensor(rng, (C,), mx.F32, 0.1)
+    gamma[::7] = 0
+    beta[:32] = 0  # with gamma 0: zeros, a block of nothing else where C = 32
+    gamma[:32] = 0
+    y = torch.empty(M, C, dtype=torch.bfloat16, device="cuda")
+    row, saved = mx.alloc_packed(M, C, fmt), mx.alloc_packed(M, C, mx.E4M3)
+    mx.layernorm_fwd(x, y, gamma, beta, row=row, fmt=fmt, scale_mode=mode, hadamard=had, saved=saved)
+    row2, saved2 = mx.alloc_packed(M, C, fmt), mx.alloc_packed(M, C, mx.E4M3)
+    mx.quantize_saved(M, C, fmt, mode, had, x=y, row=row2)
+    mx.checkpoint_save(y, saved2)
+    only = mx.alloc_packed(M, C, fmt)
+    mx.layernorm_fwd(x, None, gamma, beta, row=only, fmt=fmt, scale_mode=mode, hadamard=had)
+    for a, b in ((row, row2), (saved, saved2), (only, row)):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@gpu
+def test_layernorm_packs_of_extreme_values():
+    """Every rounding of the formats, saturation, signed zeros and the smallest and largest scales: a norm whose
+    gamma and beta place y (one value a row is 1 / -1 in turn) where they want."""
+    C = 4096
+    rng = np.random.default_rng(5)
+    x = torch.ones(8, C, device="cuda")
+    x[:, 1::2] = -1.0  # mean 0, rstd 1 under eps = 0: y = +-gamma + beta
+    for case in range(6):
+        bits = rng.integers(0, 1 << 15, C).astype(np.uint16)
+        if case == 1:
+            bits &= 0x00FF  # bf16 subnormals and the least normal numbers
+        elif case == 2:
+            bits = (0x3F80 + rng.integers(0, 0x300, C)).astype(np.uint16)  # 1 .. 64: ties of every format
+        elif case == 3:
+            bits[:] = 0
+        elif case == 4:
+            bits = (0x7F00 + rng.integers(0, 0x80, C)).astype(np.uint16)  # up to the largest
+        elif case == 5:
+            bits[::96] = 0x7F80  # infinities in some blocks
+        gamma = torch.from_numpy(bits.view(np.int16)).cuda().view(torch.bfloat16)
+        y = torch.empty(8, C, dtype=torch.bfloat16, device="cuda")
+        for fmt, mode, had in FMTS + [(mx.E2M3, mx.FLOOR, False), (mx.E4M3, mx.FLOOR, False)]:
+            row, row2 = mx.alloc_packed(8, C, fmt), mx.alloc_packed(8, C, fmt)
+            mx.layernorm_fwd(x, y, gamma, eps=0.0, row=row, fmt=fmt, scale_mode=mode, hadamard=had)
+            mx.quantize_saved(8, C, fmt, mode, had, x=y, row=row2)
+            assert torch.equal(row[1], row2[1]), (case, fmt)
+            assert torch.equal(row[0], row2[0]), (case, fmt)
+
+
+@gpu
+def test_layernorm_pitches_in_place_and_nothing_else_written():
+    rng = np.random.default_rng(3)
+    M, C = 37, 200
+    wide = tensor(rng, (M, 264), mx.BF16)
+    before = wide.clone()
+    x = wide[:, 16:16 + C]
+    out = torch.full((M + 1, 216), 7.0, dtype=torch.float32, device="cuda")
+    mx.layernorm_fwd(x, out[:M, 8:8 + C])
+    check_norm(x, out[:M, 8:8 + C], None, None, None, None, 1e-5, mx.F32)
+    assert (out[M] == 7).all() and (out[:, :8] == 7).all() and (out[:, 208:] == 7).all() and torch.equal(wide, before)
+    mx.layernorm_fwd(x, x)  # in place
+    check_norm(before[:, 16:16 + C], x, None, None, None, None, 1e-5, mx.BF16)
+    assert torch.equal(wide[:, :16], before[:, :16]) and torch.equal(wide[:, 216:], before[:, 216:])
+
+
+@gpu
+def test_layernorm_rows_of_one_value_and_not_finite():
+    x = torch.full((4, 64), 3.0, device="cuda")
+    x[1, 5] = float("nan")
+    x[2, 5] = float("inf")
+    x[3] = torch.arange(64.0)
+    y, mean, rstd = torch.empty_like(x), torch.empty(4, device="cuda"), torch.empty(4, device="cuda")
+    saved = mx.alloc_packed(4, 64, mx.E4M3)
+    mx.layernorm_fwd(x, y, mean=mean, rstd=rstd, saved=saved, eps=1e-5)
+    assert (y[0] == 0).all() and y[1].isnan().all() and y[2].isnan().all()
+    check_norm(x[3:], y[3:], None, None, None, None, 1e-5, mx.F32)
+    assert (saved[1][0, 1] == torch.tensor([255, 255, 0, 0], device="cuda")).all()
+    assert torch.isfinite(decode_ok(saved, 4, 64)[[0, 3]]).all()
+
+
+def decode_ok(p, R, C):
+    y = torch.empty(R, C, device="cuda")
+    mx.checkpoint_load(p, y)
+    return y
+
+
+def norm_bwd64(dy, x, mean, rstd, gamma):
+    h = (x - mean) * rstd
+    g = dy if gamma is None else dy * gamma
+    return rstd * (g - g.mean(1, keepdims=True) - h * (g * h).mean(1, keepdims=True)), (dy * h).sum(0), dy.sum(0), h, g
+
+
+def check_norm_bwd(dy, x, mean, rstd, gamma, residual, dx, dgamma, dbeta, before=(0.0, 0.0)):
+    d, xx, m, r = f64(dy), f64(x), f64(mean)[:, None], f64(rstd)[:, None]
+    want, wg, wb, h, g = norm_bwd64(d, xx, m, r, None if gamma is None else f64(gamma))
+    eh = U * (np.abs(xx - m) * r + 2 * np.abs(h))  # mean and rstd are given: two roundings
+    if dx is not None:
+        gh = np.abs(g * h).mean(1, keepdims=True)
+        tol = r * (U * (4 * np.abs(g) + 70 * np.abs(g).mean(1, keepdims=True)) + eh * gh
+                   + np.abs(h) * ((np.abs(g) * eh).mean(1, keepdims=True) + 72 * U * gh))
+        if residual is not None:
+            want = want + f64(residual)
+        tol = tol + 4 * U * np.abs(want)
+        if dx.dtype == torch.bfloat16:
+            tol = tol + BF16_STEP * (np.abs(want) + tol)
+        assert (np.abs(f64(dx) - want) <= tol).all()
+    n = len(d) / 256 + 256 / 4 + 16
+    if dgamma is not None:
+        tol = U * (n + 2) * (np.abs(d * h).sum(0) + np.abs(before[0])) + (np.abs(d) * eh).sum(0)
+        assert (np.abs(f64(dgamma) - (wg + before[0])) <= tol).all()
+    if dbeta is not None:
+        assert (np.abs(f64(dbeta) - (wb + before[1])) <= U * n * (np.abs(d).sum(0) + np.abs(before[1]))).all()
+
+
+def norm_bwd_inputs(rng, M, C, dy_dtype, x_dtype, w_dtype):
+    x, dy = tensor(rng, (M, C), x_dtype, 2.0, 0.5), tensor(rng, (M, C), dy_dtype)
+    gamma = tensor(rng, (C,), w_dtype, 0.2, 1.0)
+    _, mean, rstd, _ = norm64(f64(x), None, None, 1e-5)
+    as32 = lambda v: torch.from_numpy(v[:, 0].astype(np.float32)).cuda()  # noqa: E731
+    return x, dy, gamma, as32(mean), as32(rstd)
+
+
+def partials_of(M, C):
+    return torch.full((mx.layernorm_partial_rows(M, C), 2, C), float("nan"), device="cuda")
+
+
+@gpu
+@pytest.mark.parametrize("C", WIDTHS)
+@pytest.mark.parametrize("dy_dtype,x_dtype,dx_dtype", [(0, 0, 0), (1, 1, 1), (0, 1, 1), (1, 0, 0)])
+def test_layernorm_bwd_widths_and_types(C, dy_dtype, x_dtype, dx_dtype):
+    rng = np.random.default_rng(C + 2 * x_dtype)
+    for M in (1, 19):
+        x, dy, gamma, mean, rstd = norm_bwd_inputs(rng, M, C, dy_dtype, x_dtype, dx_dtype)
+        residual = tensor(rng, (M, C), dx_dtype)
+        dx = torch.empty(M, C, dtype=torch_type(dx_dtype), device="cuda")
+        dgamma, dbeta = torch.empty(C, device="cuda"), torch.empty(C, device="cuda")
+        mx.layernorm_bwd(dy, x, mean, rstd, dx, gamma, residual, dgamma, dbeta, partials_of(M, C))
+        check_norm_bwd(dy, x, mean, rstd, gamma, residual, dx, dgamma, dbeta)
+
+
+@gpu
+@pytest.mark.parametrize("M,C", [(2500, 96), (4999, 1024), (3001, 2080), (1500, 4096), (1027, 8192), (600, 12000)])
+def test_layernorm_bwd_many_rows(M, C):
+    rng = np.random.default_rng(M + 1)
+    x, dy, gamma, mean, rstd = norm_bwd_inputs(rng, M, C, mx.BF16, mx.BF16, mx.BF16)
+    dx = torch.empty_like(x)
+    start = torch.ones(C, device="cuda"), torch.full((C,), -2.0, device="cuda")
+    dgamma, dbeta = start[0].clone(), start[1].clone()
+    mx.layernorm_bwd(dy, x, mean, rstd, dx, gamma, None, dgamma, dbeta, partials_of(M, C), accumulate=True)
+    check_norm_bwd(dy, x, mean, rstd, gamma, None, dx, dgamma, dbeta, (f64(start[0]), f64(start[1])))
+
+
+@gpu
+def test_layernorm_bwd_parts():
+    """Each output alone gives the bits it has beside the others; dx over dy, x and the residual; pitches."""
+    rng = np.random.default_rng(8)
+    M, C = 45, 136
+    x, dy, gamma, mean, rstd = norm_bwd_inputs(rng, M, C, mx.F32, mx.F32, mx.F32)
+    residual = tensor(rng, (M, C), mx.F32)
+    new = lambda: torch.empty(C, device="cuda")  # noqa: E731
+    dx, dgamma, dbeta = torch.empty_like(x), new(), new()
+    mx.layernorm_bwd(dy, x, mean, rstd, dx, gamma, residual, dgamma, dbeta, partials_of(M, C))
+    one, g1, b1 = torch.empty_like(x), new(), new()
+    mx.layernorm_bwd(dy, x, mean, rstd, one, gamma, residual)
+    mx.layernorm_bwd(dy, x, mean, rstd, gamma=gamma, dgamma=g1, partials=partials_of(M, C))
+    mx.layernorm_bwd(dy, x, mean, rstd, gamma=gamma, dbeta=b1, partials=partials_of(M, C))
+    assert torch.equal(one, dx) and torch.equal(g1, dgamma) and torch.equal(b1, dbeta)
+    for which in range(3):
+        t = [dy.clone(), x.clone(), residual.clone()]
+        mx.layernorm_bwd(t[0], t[1], mean, rstd, t[which], gamma, t[2], g1, b1, partials_of(M, C))
+        assert torch.equal(t[which], dx) and torch.equal(g1, dgamma) and torch.equal(b1, dbeta)
+    wide = torch.full((M, 160), 5.0, device="cuda")
+    view = wide[:, 8:8 + C]
+    view.copy_(dy)
+    out = torch.full((M, 144), 9.0, device="cuda")
+    mx.layernorm_bwd(view, x, mean, rstd, out[:, :C], gamma, residual)
+    assert torch.equal(out[:, :C], dx) and (out[:, C:] == 9).all() and (wide[:, :8] == 5).all()
+    check_norm_bwd(dy, x, mean, rstd, gamma, residual, dx, dgamma, dbeta)
+
+
+@gpu
+def test_layernorm_bwd_without_tokens():
+    g, b = torch.full((64,), 3.0, device="cuda"), torch.full((64,), 4.0, device="cuda")
+    e = torch.empty(0, 64, device="cuda")
+    m = torch.empty(0, device="cuda")
+    mx.layernorm_bwd(e, e, m, m, e, None, None, g, b, torch.empty(0, device="cuda"), accumulate=True)
+    assert (g == 3).all() and (b == 4).all()
+    mx.layernorm_bwd(e, e, m, m, e, None, None, g, b, torch.empty(0, device="cuda"))
+    assert (g == 0).all() and (b == 0).all()
+
+
+@gpu
+def test_layernorm_gradients_against_differences():
+    """sum(w y) over a small norm: central differences of the 64-bit forward pass."""
+    rng = np.random.default_rng(11)
+    M, C, eps = 3, 24, 1e-5
+    x, w = rng.standard_normal((M, C)), rng.standard_normal((M, C))
+    gamma, beta = 1 + 0.3 * rng.standard_normal(C), rng.standard_normal(C)
+    x, w, gamma, beta = (v.astype(np.float32).astype(np.float64) for v in (x, w, gamma, beta))
+    total = lambda x, g, b: (w * norm64(x, g, b, eps)[0]).sum()  # noqa: E731
+    d = lambda v: torch.from_numpy(v.astype(np.float32)).cuda()  # noqa: E731
+    y, mean, rstd = torch.empty(M, C, device="cuda"), torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+    mx.layernorm_fwd(d(x), y, d(gamma), d(beta), eps, mean, rstd)
+    dx, dg, db = torch.empty_like(y), torch.empty(C, device="cuda"), torch.empty(C, device="cuda")
+    mx.layernorm_bwd(d(w), d(x), mean, rstd, dx, d(gamma), None, dg, db, partials_of(M, C))
+    s = 1e-5
+    for _ in range(8):
+        a, bx, c = rng.standard_normal((M, C)), rng.standard_normal(C), rng.standard_normal(C)
+        diff = (total(x + s * a, gamma + s * bx, beta + s * c) - total(x - s * a, gamma - s * bx, beta - s * c)) / (2 * s)
+        got = (f64(dx) * a).sum() + (f64(dg) * bx).sum() + (f64(db) * c).sum()
+        # binary32 gradients (of order 1, 100 u each) against a difference with an error of s^2
+        assert abs(got - diff) <= 2e-5 * (np.abs(f64(dx) * a).sum() + np.abs(f64(dg) * bx).sum() + np.abs(f64(db) * c).sum())
+
+
+@gpu
+def test_layernorm_offsets_past_32_bits():
+    M, C = 70001, 16384
+    x = torch.zeros(M, C, dtype=torch.bfloat16, device="cuda")
+    x[-3:] = torch.randn(3, C, device="cuda")
+    y, row = torch.empty_like(x), mx.alloc_packed(M, C, mx.E2M1)
+    mean, rstd = torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+    mx.layernorm_fwd(x, y, mean=mean, rstd=rstd, row=row, fmt=mx.E2M1, scale_mode=mx.FLOOR)
+    check_norm(x[-3:], y[-3:], None, None, mean[-3:], rstd[-3:], 1e-5, mx.BF16)
+    assert (y[:-3] == 0).all()
+    tail = mx.alloc_packed(3, C, mx.E2M1)
+    mx.quantize_saved(3, C, mx.E2M1, mx.FLOOR, x=y[-3:].contiguous(), row=tail)
+    assert torch.equal(row[0][:, -3:], tail[0]) and torch.equal(row[1][:, -3:], tail[1])
+    dx = torch.empty_like(x)
+    mx.layernorm_bwd(y, x, mean, rstd, dx)
+    check_norm_bwd(y[-3:], x[-3:], mean[-3:], rstd[-3:], None, None, dx[-3:], None, None)
+
+
+# ---------------------------------------------------------------- cross entropy
+def integer_operands(rng, M, V, K, fmt):
+    """Operands of small integers, B's scaled by 2^-5: every logit is exact (and of a few units)."""
+    a, av = exact_operand(rng, M, K, fmt)
+    b, bv = exact_operand(rng, V, K, fmt)
+    b = (b[0], torch.where(b[1] == 127, torch.full_like(b[1], 122), b[1]))
+    return a, b, av, bv / 32
+
+
+def labels_of(rng, M, V):
+    y = rng.integers(0, V, M)
+    y[rng.random(M) < 0.2] = -100
+    if M > 3:
+        y[0], y[1], y[2] = 0, V - 1, V  # the ends, and one past them
+    return torch.from_numpy(y).cuda()
+
+
+def loss64(l, labels):
+    y = labels.cpu().numpy()
+    V = l.shape[1]
+    top = l.max(1, keepdims=True)
+    lse = np.log(np.exp(l - top).sum(1)) + top[:, 0]
+    ok = (y >= 0) & (y < V)
+    return np.where(ok, lse - l[np.arange(len(y)), np.where(ok, y, 0)], 0.0), lse, ok
+
+
+def head_loss(a, b, M, V, K, fmt, labels):
+    loss, lse = torch.full((M,), float("nan"), device="cuda"), torch.full((M,), float("nan"), device="cuda")
+    work = torch.full((mx.head_loss_work_bytes(M, V) // 4,), float("nan"), device="cuda")
+    mx.head_loss(a, b, M, V, K, fmt, labels, loss, lse, work)
+    return loss, lse
+
+
+def lse_tolerance(l, lse):
+    spread = np.abs(l).max(1)
+    V = l.shape[1]
+    return U * (2 + 3 * spread + 56 + V / 128) + 4 * U * (np.abs(lse) + spread)
+
+
+HEAD_SIZES = [(1, 1, 32), (1, 130, 64), (3, 31, 96), (33, 257, 160), (130, 1000, 32), (257, 300, 288), (5, 4099, 64),
+              (700, 24000, 32)]
+
+
+@gpu
+@pytest.mark.parametrize("fmt", [mx.E2M1, mx.E2M3, mx.E4M3])
+@pytest.mark.parametrize("M,V,K", HEAD_SIZES)
+def test_head_loss(M, V, K, fmt):
+    rng = np.random.default_rng(M + V)
+    a, b, av, bv = integer_operands(rng, M, V, K, fmt)
+    labels = labels_of(rng, M, V)
+    loss, lse = head_loss(a, b, M, V, K, fmt, labels)
+    l = av @ bv.T
+    want, want_lse, ok = loss64(l, labels)
+    tol = lse_tolerance(l, want_lse)
+    assert (np.abs(f64(lse) - want_lse) <= tol).all()
+    assert (np.abs(f64(loss) - want) <= tol + U * np.abs(want)).all()
+    assert (f64(loss)[~ok] == 0).all()
+
+
+@gpu
+@pytest.mark.parametrize("fmt,mode,had", FMTS)
+def test_head_loss_of_real_values(fmt, mode, had):
+    """Random operands: the logits' error is the product's (REL of the largest, the library's bar; a sum of
+    exponentials is off by no more than its largest logit is)."""
+    rng = np.random.default_rng(4)
+    M, V, K = 300, 5003, 1056
+    a, av = operand(rng, M, K, fmt, mode, had)
+    b, bv = operand(rng, V, K, fmt, mode, had, std=0.05)
+    labels = labels_of(rng, M, V)
+    loss, lse = head_loss(a, b, M, V, K, fmt, labels)
+    l = av @ bv.T
+    want, want_lse, _ = loss64(l, labels)
+    assert np.abs(f64(lse) - want_lse).max() <= REL * np.abs(l).max() + lse_tolerance(l, want_lse).max()
+    assert np.abs(f64(loss) - want).max() <= 2 * REL * np.abs(l).max() + lse_tolerance(l, want_lse).max()
+
+
+@gpu
+def test_head_loss_far_logits():
+    """Logits of +-several thousand: no overflow, a loss of exactly 0 where the label has all the weight."""
+    K, V = 128, 300
+    a = torch.zeros(2, K, device="cuda")
+    a[0, 0], a[1, 0] = 6.0, -6.0
+    w = torch.zeros(V, K, device="cuda")
+    w[7, 0] = 1024.0
+    A, B = mx.alloc_packed(2, K, mx.E4M3), mx.alloc_packed(V, K, mx.E4M3)
+    mx.checkpoint_save(a, A)
+    mx.checkpoint_save(w, B)
+    loss, lse = head_loss(A, B, 2, V, K, mx.E4M3, torch.tensor([7, 7], device="cuda"))
+    assert float(loss[0]) == 0.0 and float(lse[0]) == 6144.0
+    assert abs(float(loss[1]) - (6144 + np.log(V - 1))) <= 4 * U * 6150
+    assert abs(float(lse[1]) - np.log(V - 1)) <= 1e-5
+
+
+@gpu
+def test_head_loss_nan_operand():
+    rng = np.random.default_rng(2)
+    a, b, _, _ = integer_operands(rng, 4, 200, 64, mx.E2M3)
+    a[1][0, 2, 1] = 255  # one NaN block in token 2
+    loss, lse = head_loss(a, b, 4, 200, 64, mx.E2M3, torch.tensor([1, 2, 3, -1], device="cuda"))
+    assert torch.isnan(loss).tolist() == [False, False, True, False] and torch.isnan(lse).tolist() == [False, False, True, False]
+    assert float(loss[3]) == 0
+
+
+def half_step(v, X, fmt):
+    """The most a value v under block exponents X is off after packing (saturated blocks under FLOOR aside)."""
+    s = 2.0 ** X
+    a = np.abs(v) / s
+    if fmt == mx.E4M3:
+        return s * np.maximum(a * 2.0 ** -4, 2.0 ** -10)
+    low, high = (0.25, 0.25) if fmt == mx.E2M1 else (1 / 16, 1 / 16)
+    step = np.where(a < 2, low, a * high)
+    top = 6.0 if fmt == mx.E2M1 else 7.5
+    return s * np.maximum(step, np.where(a > top, a - top, 0))
+
+
+def grads(a, b, wc, xc, M, V, K, fmt, mode, had, labels, lse, dloss, piece, dw=None, accumulate=False, only=""):
+    part = min(piece, V)
+    e = lambda *s: torch.full(s, float("nan"), device="cuda")  # noqa: E731
+    dX = e(M, K).bfloat16() if only != "dW" else None
+    dW = (e(V, K) if dw is None else dw) if only != "dX" else None
+    Gr = mx.alloc_packed(M, (part + 31) // 32 * 32, fmt) if only != "dW" else None
+    Gc = mx.alloc_packed(part, (M + 31) // 32 * 32, fmt) if only != "dX" else None
+    mx.head_loss_bwd(a, b, wc, xc, M, V, K, fmt, mode, labels, lse, dloss, dX=dX, dW=dW, Gr=Gr, Gc=Gc, piece=piece,
+                     sums=e(M, K) if V > piece and only != "dW" else None, hadamard=had, accumulate=accumulate)
+    return dX, dW, Gr, Gc
+
+
+def columns(rng, rows, K, fmt, mode, had, std):
+    """[K] x K = rows rounded up to 32: a columnwise operand and what it stands for."""
+    x = dev_bf16(rng.standard_normal((rows, K)) * std)
+    p = mx.alloc_packed(K, (rows + 31) // 32 * 32, fmt)
+    mx.quantize_saved(rows, K, fmt, mode, had, x=x, col=p)
+    return p, decode(p, K, (rows + 31) // 32 * 32, fmt)
+
+
+@gpu
+@pytest.mark.parametrize("fmt,mode,had", FMTS + [(mx.E2M3, mx.FLOOR, False)])
+@pytest.mark.parametrize("M,V,K", [(1, 1, 32), (1, 130, 64), (3, 31, 96), (33, 257, 160), (130, 1000, 32), (257, 300, 288),
+                                   (700, 24000, 32)])
+def test_head_loss_bwd(M, V, K, fmt, mode, had):
+    """One piece: the packs of G against G in 64 bits, the products against the packs."""
+    rng = np.random.default_rng(M * V)
+    a, b, av, bv = integer_operands(rng, M, V, K, fmt)
+    labels = labels_of(rng, M, V)
+    l = av @ bv.T
+    _, lse64, ok = loss64(l, labels)
+    lse = torch.from_numpy(lse64.astype(np.float32)).cuda()
+    dloss = torch.from_numpy((rng.random(M) + 0.5).astype(np.float32) / M).cuda()
+    wc, wv = columns(rng, V, K, fmt, mode, had, 0.05)
+    xc, xv = columns(rng, M, K, fmt, mode, had, 1.0)
+    piece = (V + 127) // 128 * 128
+    dX, dW, Gr, Gc = grads(a, b, wc, xc, M, V, K, fmt, mode, had, labels, lse, dloss, piece)
+    p = np.exp(l - f64(lse)[:, None])
+    G = p.copy()
+    y = labels.cpu().numpy()
+    G[np.arange(M)[ok], y[ok]] -= 1
+    scale = np.where(ok, f64(dloss), 0.0)[:, None]
+    G *= scale
+    # G in binary32: the exponential as in the forward pass, one rounding each of the difference and the product
+    eG = scale * (p * U * (6 + 6 * np.abs(l) + 3 * np.abs(f64(lse))[:, None]) + 2 * U * np.abs(p - 1) * (G < 0)) + U * np.abs(G)
+    for packed, want, err, rows, k in ((Gr, G, eG, M, V), (Gc, G.T, eG.T, V, M)):
+        kp = (k + 31) // 32 * 32
+        want, err = (np.pad(t, ((0, 0), (0, kp - k))) for t in (want, err))
+        got = decode(packed, rows, kp, fmt)
+        X = np.repeat(unblocked(packed[1].cpu().numpy(), kp // 32).astype(np.float64) - 127, 32, axis=1)
+        if had:  # the rotation (binary32, 6 roundings) spreads a block's error over it
+            i = np.arange(32)
+            H = (1 - 2.0 * np.array([[bin(q & c).count("1") & 1 for c in i] for q in i])) / np.sqrt(32)
+            want = (want.reshape(rows, -1, 32) @ H).reshape(rows, kp)
+            err = ((err + 8 * U * np.abs(want)).reshape(rows, -1, 32).sum(-1, keepdims=True) / np.sqrt(32)
+                   + 8 * U * np.abs(want).reshape(rows, -1, 32).max(-1, keepdims=True)).repeat(32, -1).reshape(rows, kp)
+        assert (np.abs(got - want) <= half_step(want, X, fmt) * (1 + 2.0 ** -16) + 1.2 * err).all()
+        # the scales are those that the format's rule gives G (its error aside: a block at the border may fall to either side)
+        blocks = np.abs(want).reshape(rows, -1, 32).max(-1)
+        Xb = X[:, ::32]
+        if fmt == mx.E4M3:
+            assert (blocks <= 448 * 2.0 ** Xb * (1 + 1e-4)).all()
+            assert ((blocks >= 224 * 2.0 ** Xb * (1 - 1e-4)) | (Xb == -127)).all()
+        else:
+            assert (blocks < 8 * 2.0 ** Xb * (1 + 1e-4)).all() and ((blocks >= 4 * 2.0 ** Xb * (1 - 1e-4)) | (Xb == -127)).all()
+        codes = untiled(packed[0].cpu().numpy(), kp, mx.BITS[fmt])
+        assert codes.shape[0] == rows
+    Vp, Mp = (V + 31) // 32 * 32, (M + 31) // 32 * 32
+    want = decode(Gr, M, Vp, fmt) @ wv.T
+    assert np.abs(f64(dX) - want).max() <= REL * np.abs(want).max() + BF16_STEP * np.abs(want).max()
+    want = decode(Gc, V, Mp, fmt) @ xv.T
+    assert np.abs(f64(dW) - want).max() <= REL * np.abs(want).max()
+    assert (f64(dX)[~ok] == 0).all()
+
+
+@gpu
+@pytest.mark.parametrize("fmt,mode,had", FMTS)
+def test_head_loss_bwd_pieces(fmt, mode, had):
+    """Pieces of any size give the products of the same packs; dX and dW alone, accumulated, in bf16 and binary32."""
+    rng = np.random.default_rng(9)
+    M, V, K = 150, 1111, 224
+    a, b, av, bv = integer_operands(rng, M, V, K, fmt)
+    labels = labels_of(rng, M, V)
+    _, lse64, _ = loss64(av @ bv.T, labels)
+    lse = torch.from_numpy(lse64.astype(np.float32)).cuda()
+    dloss = torch.full((1,), 1.0 / M, device="cuda")
+    wc, _ = columns(rng, V, K, fmt, mode, had, 0.05)
+    xc, _ = columns(rng, M, K, fmt, mode, had, 1.0)
+    args = (a, b, wc, xc, M, V, K, fmt, mode, had, labels, lse)
+    whole, dW, _, _ = grads(*args, dloss, 1152)
+    per_token, dW2, _, _ = grads(*args, dloss.expand(M).contiguous(), 1152)
+    assert torch.equal(whole, per_token) and torch.equal(dW, dW2)
+    for piece in (128, 384, 1024, 4096):
+        dX, dW2, _, _ = grads(*args, dloss, piece)
+        # (binary32 sums in another order, one bf16 rounding each)
+        assert (f64(dX) - f64(whole)).__abs__().max() <= (REL + 2 * BF16_STEP) * np.abs(f64(whole)).max()
+        assert (f64(dW2) - f64(dW)).__abs__().max() <= REL * np.abs(f64(dW)).max()
+    one, _, _, _ = grads(*args, dloss, 384, only="dX")
+    _, two, _, _ = grads(*args, dloss, 384, only="dW")
+    assert (f64(one) - f64(whole)).__abs__().max() <= (REL + 2 * BF16_STEP) * np.abs(f64(whole)).max()
+    assert (f64(two) - f64(dW)).__abs__().max() <= REL * np.abs(f64(dW)).max()
+    start = torch.randn(V, K, device="cuda")
+    _, sum32, _, _ = grads(*args, dloss, 384, dw=start.clone(), accumulate=True)
+    tol = REL * np.abs(f64(dW)).max()
+    assert (f64(sum32) - (f64(start) + f64(dW))).__abs__().max() <= tol + U * np.abs(f64(start)).max()
+    _, sum16, _, _ = grads(*args, dloss, 384, dw=start.bfloat16(), accumulate=True)
+    want = f64(start.bfloat16()) + f64(dW)
+    assert (np.abs(f64(sum16) - want) <= tol + BF16_STEP * np.abs(want)).all()
+
+
+@gpu
+def test_head_loss_bwd_without_tokens_or_labels():
+    rng = np.random.default_rng(6)
+    fmt, mode, had = FMTS[0]
+    V, K = 200, 64
+    b, _ = exact_operand(rng, V, K, fmt)
+    wc, _ = columns(rng, V, K, fmt, mode, had, 0.05)
+    none = mx.alloc_packed(0, K, fmt)
+    xc0 = mx.alloc_packed(K, 0, fmt)
+    e = torch.empty(0, device="cuda")
+    dW = torch.full((V, K), 3.0, device="cuda")
+    args = dict(dW=dW, Gc=mx.alloc_packed(128, 32, fmt), piece=128)
+    call = lambda **kw: mx.head_loss_bwd(none, b, wc, xc0, 0, V, K, fmt, mode, e.long(), e, torch.ones(1, device="cuda"), **args, **kw)  # noqa: E731,E501
+    call(accumulate=True)
+    assert (dW == 3).all()
+    call()
+    assert (dW == 0).all()
+    M = 40
+    a, _ = exact_operand(rng, M, K, fmt)
+    xc, _ = columns(rng, M, K, fmt, mode, had, 1.0)
+    labels = torch.full((M,), -100, device="cuda")
+    loss, lse = head_loss(a, b, M, V, K, fmt, labels)
+    dX, dW, _, _ = grads(a, b, wc, xc, M, V, K, fmt, mode, had, labels, lse, torch.ones(M, device="cuda"), 128)
+    assert (loss == 0).all() and (dX == 0).all() and (dW == 0).all()
+
+
+@gpu
+def test_head_gradient_against_differences():
+    """d sum(w loss) / dX along random directions, by central differences of the 64-bit loss; what packing G and
+    rounding dX may add is computed from the packs."""
+    rng = np.random.default_rng(12)
+    M, V, K, (fmt, mode, had) = 20, 333, 96, FMTS[2]
+    x, w = dev_bf16(rng.standard_normal((M, K))), dev_bf16(rng.standard_normal((V, K)) * 0.2)
+    a, b, wc = mx.alloc_packed(M, K, fmt), mx.alloc_packed(V, K, fmt), mx.alloc_packed(K, 352, fmt)
+    mx.quantize_saved(M, K, fmt, mode, x=x, row=a)
+    mx.quantize_saved(V, K, fmt, mode, x=w, row=b, col=wc)
+    av, bv, wv = decode(a, M, K, fmt), decode(b, V, K, fmt), decode(wc, K, 352, fmt)[:, :V].T
+    labels = labels_of(rng, M, V)
+    loss, lse = head_loss(a, b, M, V, K, fmt, labels)
+    dloss = torch.from_numpy((rng.random(M) + 0.5).astype(np.float32)).cuda()
+    dX, _, Gr, _ = grads(a, b, wc, None, M, V, K, fmt, mode, had, labels, lse, dloss, 384, only="dX")
+    l = av @ bv.T
+    _, lse64, ok = loss64(l, labels)
+    G = np.exp(l - lse64[:, None])
+    G[np.arange(M)[ok], labels.cpu().numpy()[ok]] -= 1
+    G *= np.where(ok, f64(dloss), 0.0)[:, None]
+    off = np.abs(decode(Gr, M, 352, fmt)[:, :V] - G)
+    total = lambda z: (f64(dloss) * loss64(z @ bv.T, labels)[0]).sum()  # noqa: E731
+    for _ in range(8):
+        D = rng.standard_normal((M, K))
+        diff = (total(av + 1e-4 * D) - total(av - 1e-4 * D)) / 2e-4
+        got = (f64(dX) * D).sum()
+        # the two packs of W differ: (W's columns - W's rows) with G; G's packing; dX's rounding; the difference's s^2
+        tol = (np.abs(G) * np.abs(D @ (wv - bv).T)).sum() + (off * np.abs(D @ wv.T)).sum()
+        tol += (BF16_STEP + REL) * np.abs(f64(dX) * D).sum() + 1e-5
+        assert abs(got - diff) <= tol
+        # and without what the packing adds, the sum with G itself is the difference
+        assert abs((G @ bv * D).sum() - diff) <= 1e-5 * (np.abs(G @ bv * D).sum() + 1)
+
+
+# ---------------------------------------------------------------- AdamW
+HYPER = dict(lr=1e-2, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.1)
+
+
+def philox64(i, c2, c3, seed):
+    """Words of Philox4x32-10 at counter (i low, i high, c2, c3): [len(i)][4], by Python integers' rules."""
+    low = np.uint64(0xFFFFFFFF)
+    i = np.asarray(i, np.uint64)
+    c = [i & low, i >> np.uint64(32), np.full_like(i, c2), np.full_like(i, c3)]
+    k0, k1 = seed & 0xFFFFFFFF, seed >> 32
+    for _ in range(10):
+        p0, p1 = c[0] * np.uint64(0xD2511F53), c[2] * np.uint64(0xCD9E8D57)
+        c = [(p1 >> np.uint64(32)) ^ c[1] ^ np.uint64(k0), p1 & low, (p0 >> np.uint64(32)) ^ c[3] ^ np.uint64(k1), p0 & low]
+        k0, k1 = (k0 + 0x9E3779B9) & 0xFFFFFFFF, (k1 + 0xBB67AE85) & 0xFFFFFFFF
+    return np.stack(c, -1)
+
+
+def test_philox_of_the_tests_is_the_published_one():
+    import json
+    import os
+    kat = json.load(open(os.path.join(os.path.dirname(__file__), "golden", "philox4x32_10_kat.json")))
+    text = json.dumps(kat)
+    # the all-zero vector: counter 0, key 0
+    got = philox64(np.array([0]), 0, 0, 0)[0]
+    assert [f"{int(w):08x}" for w in got] == ["6627e8d5", "e169c58d", "bc57ac4c", "9b00dbd8"]
+    assert "6627e8d5" in text.lower()
+
+
+def adam64(p, g, m, v, step, h=HYPER, scale=1.0):
+    g = g * scale
+    m = h["beta1"] * m + (1 - h["beta1"]) * g
+    v = h["beta2"] * v + (1 - h["beta2"]) * g * g
+    den = np.sqrt(v / (1 - h["beta2"] ** step)) + h["eps"]
+    move = h["lr"] / (1 - h["beta1"] ** step) * m / den
+    return p * (1 - h["lr"] * h["weight_decay"]) - move, m, v, move
+
+
+def state8(n):
+    p = mx.alloc_packed(1, (n + 31) // 32 * 32, mx.E4M3)
+    p[0].zero_()
+    p[1].zero_()
+    return p
+
+
+def state8_of(values, n):
+    """An 8-bit state of given values (nearest) as a test's start."""
+    p = state8(n)
+    x = torch.zeros(1, (n + 31) // 32 * 32, device="cuda")
+    x[0, :n] = values
+    mx.checkpoint_save(x, p)
+    return p
+
+
+def values8(p, n):
+    return decode(p, 1, (n + 31) // 32 * 32, mx.E4M3)[0, :n]
+
+
+LENGTHS = [1, 7, 8, 31, 32, 33, 100, 128, 129, 2047, 2048, 4096, 4099, 12345]
+
+
+def check_adam32(before, after, g, step, scale):
+    p, m, v = (f64(before[k]) for k in "pmv")
+    wp, wm, wv, move = adam64(p, f64(g), m, v, step, scale=scale)
+    # m, v: at most four roundings of each term; p: eight in the move (v's four count half), two of its own
+    gs = np.abs(f64(g) * scale)
+    em = 4 * U * (0.9 * np.abs(m) + 0.1 * gs)
+    assert (np.abs(f64(after["m"]) - wm) <= em).all()
+    assert (np.abs(f64(after["v"]) - wv) <= 6 * U * wv).all()
+    den = np.sqrt(wv / (1 - 0.999 ** step)) + HYPER["eps"]
+    tol = 12 * U * np.abs(move) + HYPER["lr"] / (1 - 0.9 ** step) * em / den + 3 * U * np.abs(p)
+    assert (np.abs(f64(after["p"]) - wp) <= tol).all()
+
+
+@gpu
+@pytest.mark.parametrize("g_dtype", [mx.BF16, mx.F32])
+def test_adamw_32_bits(g_dtype):
+    """Tensors of every kind of length in one call, of more than one launch."""
+    rng = np.random.default_rng(1)
+    sizes = LENGTHS * 4
+    t = [{"p": tensor(rng, (n,), 1), "g": tensor(rng, (n,), g_dtype, 0.1), "m": tensor(rng, (n,), 1, 0.1),
+          "v": tensor(rng, (n,), 1, 0.1).square(), "copy": torch.empty(n, dtype=torch.bfloat16, device="cuda") if i % 2 else None}
+         for i, n in enumerate(sizes)]
+    before = [{k: x[k].clone() for k in "pmv"} for x in t]
+    scale = torch.full((1,), 0.5, device="cuda")
+    mx.adamw(mx.adamw_items(t), **HYPER, step=5, grad_scale=scale)
+    for b, x in zip(before, t):
+        check_adam32(b, x, x["g"], 5, 0.5)
+        if x["copy"] is not None:
+            assert torch.equal(x["copy"], x["p"].bfloat16())
+
+
+@gpu
+def test_adamw_first_step_and_zero_gradient():
+    n = 100
+    p, z = torch.ones(n, device="cuda"), lambda: torch.zeros(n, device="cuda")  # noqa: E731
+    t = {"p": p.clone(), "g": z(), "m": z(), "v": z()}
+    mx.adamw([t], **HYPER, step=1)
+    assert (t["m"] == 0).all() and (t["v"] == 0).all() and (np.abs(f64(t["p"]) - 0.999) <= 2 * U).all()
+    t8 = {"p": p.clone(), "g": z(), "m": state8(n), "v": state8(n)}
+    mx.adamw([t8], **HYPER, step=1)
+    assert torch.equal(t8["p"], t["p"]) and (values8(t8["m"], n) == 0).all() and (values8(t8["v"], n) == 0).all()
+    # beta = 0: the gradient alone; the first move is lr g / (|g| + eps)
+    t = {"p": z(), "g": torch.linspace(-1, 1, n, device="cuda"), "m": z(), "v": z()}
+    mx.adamw([t], lr=1e-2, beta1=0.0, beta2=0.0, eps=1e-8, step=1)
+    g = f64(t["g"])
+    assert (np.abs(f64(t["p"]) + 1e-2 * g / (np.abs(g) + 1e-8)) <= 1e-2 * 8 * U).all()
+
+
+def check_state8(packed, want, err, r16, n):
+    """The codes are those that the random bits give `want`, or, where its error `err` may decide, the neighbours."""
+    kp = (n + 31) // 32 * 32
+    scales = unblocked(packed[1].cpu().numpy(), kp // 32).astype(np.float64)[0] - 127
+    w = np.pad(want, (0, kp - n)).reshape(-1, 32)
+    amax = np.abs(w).max(-1)
+    mant, e = np.frexp(amax)
+    X = np.where(amax == 0, -127, np.clip(e - 9 + (mant > 0.875), -127, 127))
+    border = np.abs(mant / 0.875 - 1) < 1e-6  # the scale may fall to either side
+    assert ((scales == X) | border).all()
+    s = np.repeat(2.0 ** scales, 32)[:n]
+    a = np.abs(want) / s
+    _, ea = np.frexp(a)
+    ulp = 2.0 ** (np.maximum(ea - 1, -6) - 3)
+    lo = np.floor(a / ulp)
+    share = (a / ulp - lo) * 65536
+    code = (lo + (r16 < np.floor(share))) * ulp * s
+    got = np.abs(values8(packed, n))
+    unsure = np.abs(share - r16) <= 1 + 65536 * err / (ulp * s)
+    wrap = (share < 65536 * err / (ulp * s)) | (share > 65536 * (1 - err / (ulp * s)))
+    assert ((got == code) | unsure | wrap).all()
+    assert (np.abs(got - np.abs(want)) <= ulp * s * (1 + 1e-5)).all()
+    assert (np.mean(got != code) < 1e-3) or n < 4000
+    assert ((np.sign(values8(packed, n)) == np.sign(want)) | (got == 0)).all()
+    codes = untiled(packed[0].cpu().numpy(), (n + 127) // 128 * 128, 8)[0]
+    assert (codes[n:] & 0x7F == 0).all()
+
+
+@gpu
+@pytest.mark.parametrize("g_dtype,step,seed", [(mx.BF16, 3, 0x123456789ABCDEF0), (mx.F32, 1000, 7)])
+def test_adamw_8_bits(g_dtype, step, seed):
+    rng = np.random.default_rng(step)
+    t, before = [], []
+    for n in LENGTHS + [0, 70000]:
+        scale = torch.exp(tensor(rng, (n,), 1)) if n else torch.empty(0, device="cuda")
+        m0 = tensor(rng, (n,), 1, 0.1) * scale
+        u0 = tensor(rng, (n,), 1, 0.1).abs() * scale
+        x = {"p": tensor(rng, (n,), 1), "g": (tensor(rng, (n,), 1, 0.1) * scale).to(torch_type(g_dtype)), "m": state8_of(m0, n) if n else state8(0),
+             "v": state8_of(u0, n) if n else state8(0)}
+        before.append((f64(x["p"]), values8(x["m"], n) if n else None, values8(x["v"], n) if n else None))
+        t.append(x)
+    mx.adamw(t, **HYPER, step=step, seed=seed)
+    for i, (x, (p, m, u)) in enumerate(zip(t, before)):
+        n = len(p)
+        if n == 0:
+            continue
+        wp, wm, wv, move = adam64(p, f64(x["g"]), m, u * u, step)
+        g = np.abs(f64(x["g"]))
+        em = 4 * U * (0.9 * np.abs(m) + 0.1 * g)
+        den = np.sqrt(wv / (1 - 0.999 ** step)) + HYPER["eps"]
+        tol = 12 * U * np.abs(move) + HYPER["lr"] / (1 - 0.9 ** step) * em / den + 3 * U * np.abs(p)
+        assert (np.abs(f64(x["p"]) - wp) <= tol).all()
+        words = philox64(np.arange((n + 3) // 4), i, step & 0xFFFFFFFF, seed).reshape(-1)[:n].astype(np.int64)
+        check_state8(x["m"], wm, em, words & 0xFFFF, n)
+        check_state8(x["v"], np.sqrt(wv), 4 * U * np.sqrt(wv), words >> 16, n)
+
+
+@gpu
+def test_adamw_8_bits_move_and_decay():
+    """Half a step of E4M3 is more than a step changes: the mean over many elements of one value still follows."""
+    n = 1 << 18
+    p, g = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    m, v = state8_of(torch.full((n,), 1.05, device="cuda"), n), state8_of(torch.full((n,), 1.05, device="cuda"), n)
+    m0, u0 = values8(m, n).mean(), values8(v, n).mean()
+    for s in range(1, 11):
+        mx.adamw([{"p": p, "g": g, "m": m, "v": v}], lr=0.0, beta1=0.99, beta2=0.999, step=s, seed=3)
+    # each step adds rounding noise of at most half a step's deviation, 2^-4 of the value, to the mean of n: six deviations
+    noise = 6 * 10 ** 0.5 * 2.0 ** -4 / n ** 0.5
+    assert abs(values8(m, n).mean() / (m0 * 0.99 ** 10) - 1) <= noise
+    # sqrt(v) decays by sqrt(beta2); its square is averaged, and rounding adds its variance (2^-8 / 4 at most a step) to v
+    assert abs(values8(v, n).mean() / (u0 * 0.999 ** 5) - 1) <= noise + 10 * 2.0 ** -10
+
+
+@gpu
+def test_adamw_not_finite():
+    n = 200
+    t = {"p": torch.ones(n, device="cuda"), "g": torch.ones(n, device="cuda"), "m": state8(n), "v": state8(n)}
+    t["g"][40] = float("nan")
+    mx.adamw([t], **HYPER, step=1)
+    bad = torch.isnan(t["p"])
+    assert bad.nonzero().flatten().tolist() == [40]
+    y = decode(t["m"], 1, 224, mx.E4M3)[0, :n]
+    assert np.isnan(y).nonzero()[0].tolist() == list(range(32, 64))
+
+
+@gpu
+@pytest.mark.parametrize("bits", [8, 32])
+def test_adamw_step_count_on_the_device(bits):
+    rng = np.random.default_rng(bits)
+    n = 5000
+    g = [tensor(rng, (n,), 1, 0.1) for _ in range(4)]
+    p0 = tensor(rng, (n,), 1)
+    new = lambda: {"p": p0.clone(), "g": torch.empty(n, device="cuda"),  # noqa: E731
+                   "m": state8(n) if bits == 8 else torch.zeros(n, device="cuda"),
+                   "v": state8(n) if bits == 8 else torch.zeros(n, device="cuda")}
+    a, b = new(), new()
+    state = torch.zeros(mx.ADAMW_STATE_BYTES, dtype=torch.uint8, device="cuda")
+    lr = torch.full((1,), HYPER["lr"], device="cuda")
+    h = {**HYPER, "lr": float(lr)}
+    ia, ib = mx.adamw_items([a]), mx.adamw_items([b])
+    for s in range(4):
+        a["g"].copy_(g[s])
+        b["g"].copy_(g[s])
+        mx.adamw(ia, **h, step=s + 1, seed=11)
+        mx.adamw(ib, **{**HYPER, "lr": 123.0}, state=state, lr_device=lr, seed=11)
+        # the factors are formed in binary64 on both sides and rounded once
+        assert (np.abs(f64(a["p"]) - f64(b["p"])) <= (s + 1) * 4 * U * (np.abs(f64(a["p"])) + 0.05)).all()
+    assert int(state[:8].view(torch.int64)) == 4
+
+
+@gpu
+def test_adamw_offsets_past_32_bits():
+    n = (1 << 31) // 4 + 12345  # binary32: past 2^31 bytes
+    t = {"p": torch.zeros(n, device="cuda"), "g": torch.zeros(n, dtype=torch.bfloat16, device="cuda"), "m": state8(n), "v": state8(n)}
+    t["g"][-100:] = 1.0
+    t["g"][:100] = -1.0
+    mx.adamw([t], lr=1e-2, step=1, seed=5)
+    p = t["p"]
+    assert (np.abs(f64(p[-100:]) + 1e-2) <= 1e-2 * 1e-6).all() and (np.abs(f64(p[:100]) - 1e-2) <= 1e-2 * 1e-6).all()
+    assert not p[100:-100].any()
+
+
+# ---------------------------------------------------------------- graphs, streams, a step together
+class Step:
+    """A norm, the projection onto V classes and its loss, all gradients, and the step over gamma, beta and W."""
+
+    def __init__(self, seed, M=100, C=256, V=700, fmt=FMTS[2], bits=8):
+        rng = np.random.default_rng(seed)
+        self.M, self.C, self.V, (self.fmt, self.mode, self.had) = M, C, V, fmt
+        e = lambda *s, t=torch.float32: torch.zeros(*s, dtype=t, device="cuda")  # noqa: E731
+        self.x = tensor(rng, (M, C), mx.BF16, 2.0, 0.3)
+        self.labels = labels_of(rng, M, V)
+        self.valid = (self.labels >= 0) & (self.labels < V)
+        self.dloss = torch.where(self.valid, 1.0 / self.valid.sum(), torch.zeros((), device="cuda"))
+        self.gamma, self.beta, self.W = 1 + 0.1 * tensor(rng, (C,), 1), 0.1 * tensor(rng, (C,), 1), 0.05 * tensor(rng, (V, C), 1)
+        self.gamma16, self.beta16 = self.gamma.bfloat16(), self.beta.bfloat16()
+        self.W16 = self.W.bfloat16()
+        self.y, self.mean, self.rstd = e(M, C, t=torch.bfloat16), e(M), e(M)
+        up = lambda n: (n + 31) // 32 * 32  # noqa: E731
+        P = lambda r, k: mx.alloc_packed(r, k, self.fmt)  # noqa: E731
+        self.yr, self.yc, self.Wr, self.Wc = P(M, C), P(C, up(M)), P(V, C), P(C, up(V))
+        self.Gr, self.Gc, self.piece = P(M, 256), P(256, up(M)), 256
+        self.loss, self.lse, self.work, self.sums = e(M), e(M), e(mx.head_loss_work_bytes(M, V) // 4), e(M, C)
+        self.dy, self.dW, self.dx = e(M, C, t=torch.bfloat16), e(V, C, t=torch.bfloat16), e(M, C, t=torch.bfloat16)
+        self.dgamma, self.dbeta, self.partials = e(C), e(C), e(mx.layernorm_partial_rows(M, C), 2, C)
+        self.state = torch.zeros(mx.ADAMW_STATE_BYTES, dtype=torch.uint8, device="cuda")
+        new = lambda n: state8(n) if bits == 8 else torch.zeros(n, device="cuda")  # noqa: E731
+        self.tensors = [{"p": p, "g": g, "m": new(p.numel()), "v": new(p.numel()), "copy": c}
+                        for p, g, c in ((self.gamma, self.dgamma, self.gamma16), (self.beta, self.dbeta, self.beta16),
+                                        (self.W, self.dW, self.W16))]
+        self.items = mx.adamw_items(self.tensors)
+
+    def run(self):
+        M, C, V, fmt, mode, had = self.M, self.C, self.V, self.fmt, self.mode, self.had
+        mx.layernorm_fwd(self.x, self.y, self.gamma16, self.beta16, 1e-5, self.mean, self.rstd, self.yr, fmt, mode, had)
+        mx.quantize_saved(M, C, fmt, mode, had, x=self.y, col=self.yc)
+        mx.quantize_saved(V, C, fmt, mode, had, x=self.W16, row=self.Wr, col=self.Wc)
+        mx.head_loss(self.yr, self.Wr, M, V, C, fmt, self.labels, self.loss, self.lse, self.work)
+        mx.head_loss_bwd(self.yr, self.Wr, self.Wc, self.yc, M, V, C, fmt, mode, self.labels, self.lse, self.dloss,
+                         dX=self.dy, dW=self.dW, Gr=self.Gr, Gc=self.Gc, piece=self.piece, sums=self.sums, hadamard=had)
+        mx.layernorm_bwd(self.dy, self.x, self.mean, self.rstd, self.dx, self.gamma16, None, self.dgamma, self.dbeta,
+                         self.partials)
+        mx.adamw(self.items, lr=1e-3, weight_decay=0.01, state=self.state, seed=9)
+
+    def outputs(self):
+        out = [self.loss, self.lse, self.dx, self.dW, self.dgamma, self.dbeta, self.gamma, self.beta, self.W, self.W16]
+        for t in self.tensors:
+            for k in "mv":
+                out += list(t[k]) if isinstance(t[k], tuple) else [t[k]]
+        return [t.clone() for t in out]
+
+
+def same_bits(a, b):
+    return all(torch.equal(x.contiguous().view(torch.uint8), y.contiguous().view(torch.uint8)) for x, y in zip(a, b))
+
+
+@gpu
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("bits", [8, 32])
+def test_a_step_together(fmt, bits):
+    """The step's gradients against autograd in 64 bits on the CPU."""
+    s = Step(21, fmt=fmt, bits=bits)
+    gamma, beta, W = (t.double().cpu().requires_grad_() for t in (s.gamma16, s.beta16, s.W16))
+    x = s.x.double().cpu().requires_grad_()
+    s.run()
+    y = torch.nn.functional.layer_norm(x, (s.C,), gamma, beta, 1e-5)
+    valid = s.valid.cpu()
+    loss = torch.nn.functional.cross_entropy((y @ W.t())[valid], s.labels.cpu()[valid])
+    loss.backward()
+    # the operands are packed: 8, 6 or 4 bits of a value and its scale.  The mean loss moves by no more than the logits do
+    # (|y| of about 16 times |W| of 0.8, each off by its format's share); the gradients' direction by the shares of three packs
+    share = {mx.E4M3: 2.0 ** -4, mx.E2M3: 2.0 ** -4, mx.E2M1: 0.25}[s.fmt]
+    assert abs(float(s.loss.double().cpu()[valid].mean()) - float(loss.detach())) <= 2 * share
+    for got, want in ((s.dx, x.grad), (s.dW, W.grad), (s.dgamma, gamma.grad), (s.dbeta, beta.grad)):
+        got, want = f64(got).reshape(-1), want.numpy().reshape(-1)
+        assert np.linalg.norm(got - want) <= 3 * share * np.linalg.norm(want)
+    assert not torch.equal(s.W, 0 * s.W) and torch.equal(s.W16, s.W.bfloat16()) and torch.equal(s.gamma16, s.gamma.bfloat16())
+
+
+@gpu
+def test_a_captured_step_is_the_eager_one():
+    """A graph of the whole step, replayed between other work, makes the eager steps' bits, one step further each time."""
+    eager, captured = Step(33), Step(33)
+    other = Step(34)
+    start = captured.outputs()
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            captured.run()
+    torch.cuda.synchronize()
+    assert same_bits(captured.outputs()[6:], start[6:])  # capturing runs nothing
+    for _ in range(5):
+        eager.run()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same_bits(eager.outputs(), captured.outputs())
+        other.run()
+    torch.cuda.synchronize()
+
+
+@gpu
+def test_two_streams_at_once():
+    a, b, alone = Step(41), Step(42), [Step(41), Step(42)]
+    for s in alone:
+        for _ in range(3):
+            s.run()
+    torch.cuda.synchronize()
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(3):
+        with torch.cuda.stream(sa):
+            a.run()
+        with torch.cuda.stream(sb):
+            b.run()
+    torch.cuda.synchronize()
+    assert same_bits(a.outputs(), alone[0].outputs()) and same_bits(b.outputs(), alone[1].outputs())
