@@ -815,7 +815,8 @@ int64_t mx_layernorm_partial_rows(int64_t M, int64_t C);
  *  work         mx_head_loss_work_bytes(M, V) bytes; calls that share it must be
  *               ordered.
  * exp is the hardware's exp2 (1 ulp).  E4M3 logits carry the error of their
- * products (mx_gemm_act: 1.5e-5 of their norm), which is then the loss's.
+ * products (mx_gemm_act: 1.5e-5 of their norm); it averages out in lse, and in
+ * the loss the label's logit is the product in binary32.
  * Errors: MX_ERR_NULL, MX_ERR_SHAPE, MX_ERR_ALIGN, MX_ERR_FORMAT,
  * MX_ERR_INDEX_OVERFLOW, MX_ERR_DEVICE, MX_ERR_LAUNCH.
  *
@@ -889,7 +890,14 @@ int64_t mx_head_loss_work_bytes(int64_t M, int64_t V);
  *       - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
  * in binary32, the factors formed in binary64.
  *
- *  items        host array; read before the call returns.  Each:
+ * The tensors are named once, in a table on the device: mx_adamw_table_size
+ * gives its bytes and the number of chunks (of 4096 elements) in it,
+ * mx_adamw_table writes it (by launches that carry the items, so it can be
+ * captured too; `items` is read before the call returns), and mx_adamw makes a
+ * step over it in one launch.  A table holds addresses: it is written anew when a
+ * tensor moves.
+ *
+ *  items        host array of n.  Each:
  *    p          binary32 [n], the master weights.
  *    g          [n] of g_dtype.
  *    m, v       state_bits 32: `codes` is binary32 [n], `scales` NULL.
@@ -898,7 +906,7 @@ int64_t mx_head_loss_work_bytes(int64_t M, int64_t V);
  *               values of sqrt(v).  All zero bytes is the state before the first
  *               step.  The update takes m and v before they are rounded.
  *    copy       bf16 [n], p after the step, rounded; or NULL.
- *    n          any number >= 0, at most 2^34.
+ *    n          any number >= 0.
  *  States in 8 bits are rounded stochastically (the nearest code would never
  *  move: a step changes a mean by less than half a code).  With neighbours
  *  lo <= |x| / 2^X < hi in E4M3 and t = (|x| / 2^X - lo) / (hi - lo), the
@@ -919,10 +927,13 @@ int64_t mx_head_loss_work_bytes(int64_t M, int64_t V);
  *               NULL.
  *  grad_scale   binary32 on the device (gradient clipping, loss scaling), or
  *               NULL for 1.
- * One launch for every 40 tensors that are not empty.  No two tensors may
- * overlap.  Errors: MX_ERR_NULL, MX_ERR_SHAPE (a size, rate or step out of range,
- * more than MX_ADAMW_MAX_ITEMS tensors), MX_ERR_ALIGN (grad_scale and lr_device:
- * 4 bytes), MX_ERR_FORMAT, MX_ERR_INDEX_OVERFLOW, MX_ERR_DEVICE, MX_ERR_LAUNCH.
+ *  table, n, chunks   the table, and its items and chunks as they were at
+ *               mx_adamw_table_size.  n = 0 steps over nothing (table may be NULL).
+ * No two tensors may overlap.  Errors: MX_ERR_NULL, MX_ERR_SHAPE (a size, rate or
+ * step out of range, more than MX_ADAMW_MAX_ITEMS tensors), MX_ERR_ALIGN (4 bytes
+ * suffice for grad_scale, lr_device and the scales of states),
+ * MX_ERR_FORMAT, MX_ERR_INDEX_OVERFLOW (2^24 or more chunks), MX_ERR_DEVICE,
+ * MX_ERR_LAUNCH.
  */
 #define MX_ADAMW_STATE_BYTES 64
 #define MX_ADAMW_MAX_ITEMS 1000000
@@ -944,7 +955,9 @@ typedef struct {
   const float* grad_scale;
 } mx_adamw_args;
 
-int mx_adamw(const mx_adamw_item* items, int64_t n, const mx_adamw_args* args, void* stream);
+int mx_adamw_table_size(const mx_adamw_item* items, int64_t n, int64_t* chunks, int64_t* bytes);
+int mx_adamw_table(const mx_adamw_item* items, int64_t n, void* table, void* stream);
+int mx_adamw(const void* table, int64_t n, int64_t chunks, const mx_adamw_args* args, void* stream);
 
 /* ---------------------------------------------------------------- misc */
 /* Human-readable name of a status code (static string). */

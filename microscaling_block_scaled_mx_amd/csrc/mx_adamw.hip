@@ -13,12 +13,10 @@
 //
 // Bound by HBM: 16 bytes an element with bf16 gradients and 8-bit states (28
 // with binary32 states), each read and written once.  A thread takes eight
-// consecutive elements a step, four lanes a block.  The tensors' addresses
-// travel in the launch's arguments, so no table has to be copied and a launch
-// can be captured into a graph.
-#include <limits.h>
+// consecutive elements a step, four lanes a block; a workgroup finds its tensor
+// by two loads from a table on the device, which is written once (by launches
+// whose arguments carry the items, so that nothing is copied from the host).
 #include <math.h>
-#include <string.h>
 
 #include "mx_lanes.h"
 #include "mx_train.h"
@@ -127,19 +125,23 @@ __device__ __forceinline__ void write_state8(void* codes, uint8_t* scales, int64
   }
 }
 
+__global__ __launch_bounds__(256) void adam_fill_kernel(AdamFill f) {
+  const AdamItem& it = f.item[blockIdx.x];
+  const int32_t place = (int32_t)(f.at + blockIdx.x);
+  if (threadIdx.x == 0) f.items[place] = it;
+  const int chunks = (int)((it.n + kAdamChunk - 1) / kAdamChunk);
+  for (int c = threadIdx.x; c < chunks; c += 256) f.chunk_item[it.first + c] = place;
+}
+
 __global__ __launch_bounds__(256) void adamw_kernel(AdamParams all) {
-  // this workgroup's tensor: the last that starts at or before it
-  const int block = blockIdx.x;
-  int k = -1;
-#pragma unroll
-  for (int i = 0; i < kAdamItems; ++i) k += block >= all.first[i] ? 1 : 0;
-  const AdamItem& it = all.item[k];
+  const int block = blockIdx.x, place = all.chunk_item[block];
+  const AdamItem it = all.items[place];
   const AdamFactors f = all.state != nullptr ? all.state->f : all.f;
   const uint32_t step = all.state != nullptr ? (uint32_t)all.state->step : all.step;
   const float gs = all.grad_scale != nullptr ? *all.grad_scale : 1.0f;
   const bool eight = it.m_scales != nullptr;
   const int64_t n = it.n, padded = (n + 127) & ~(int64_t)127;
-  const int64_t c0 = (int64_t)(block - all.first[k]) * kAdamChunk;
+  const int64_t c0 = (int64_t)(block - it.first) * kAdamChunk;
 #pragma unroll 1
   for (int64_t c = c0 + 8 * (int64_t)threadIdx.x; c - 8 * (int64_t)threadIdx.x < c0 + kAdamChunk; c += 8 * 256) {
     float p[8], g[8], m[8], v[8];
@@ -171,7 +173,7 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamParams all) {
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const uint64_t i = ((uint64_t)c >> 2) + q;
-        uint32_t x[4] = {(uint32_t)i, (uint32_t)(i >> 32), it.index, step};
+        uint32_t x[4] = {(uint32_t)i, (uint32_t)(i >> 32), (uint32_t)place, step};
         philox4x32_10(x, (uint32_t)all.seed, (uint32_t)(all.seed >> 32));
 #pragma unroll
         for (int e = 0; e < 4; ++e) w[4 * q + e] = x[e];
@@ -199,21 +201,13 @@ hipError_t launch_adam_advance(AdamState* state, const AdamHyper& h, const float
   return hipGetLastError();
 }
 
-hipError_t launch_adam(AdamParams& p, int count, hipStream_t stream) {
-  int64_t blocks = 0;
-  for (int i = 0; i < kAdamItems; ++i) {
-    if (i < count) {
-      if (blocks >= INT_MAX) return hipErrorInvalidValue;
-      p.first[i] = (int)blocks;
-      blocks += (p.item[i].n + kAdamChunk - 1) / kAdamChunk;
-    } else {
-      p.first[i] = INT_MAX;
-      memset(&p.item[i], 0, sizeof p.item[i]);
-    }
-  }
-  if (blocks >= (1ll << 32) / 256) return hipErrorInvalidValue;
-  if (blocks == 0) return hipSuccess;
-  hipLaunchKernelGGL(adamw_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, p);
+hipError_t launch_adam_fill(const AdamFill& f, int count, hipStream_t stream) {
+  hipLaunchKernelGGL(adam_fill_kernel, dim3((unsigned)count), dim3(256), 0, stream, f);
+  return hipGetLastError();
+}
+
+hipError_t launch_adam(const AdamParams& p, int64_t chunks, hipStream_t stream) {
+  hipLaunchKernelGGL(adamw_kernel, dim3((unsigned)chunks), dim3(256), 0, stream, p);
   return hipGetLastError();
 }
 

@@ -419,6 +419,29 @@ mx::HeadParams head_params(const mx_packed& A, const mx_packed& B, int64_t M, in
   return mx::HeadParams{bytes(A.codes), bytes(A.scales), bytes(B.codes), bytes(B.scales), M, V, K, labels};
 }
 
+// one launch has fewer than 2^32 threads
+constexpr int64_t kMaxAdamChunks = (1ll << 32) / 256 - 1;
+
+int validate_adamw_items(const mx_adamw_item* items, int64_t n, int64_t* chunks) {
+  if (n < 0 || n > MX_ADAMW_MAX_ITEMS) return MX_ERR_SHAPE;
+  if (n > 0 && !items) return MX_ERR_NULL;
+  int64_t sum = 0;
+  for (int64_t i = 0; i < n; ++i) {
+    const mx_adamw_item& q = items[i];
+    if (!dtype_ok(q.g_dtype) || (q.state_bits != 8 && q.state_bits != 32)) return MX_ERR_FORMAT;
+    if (q.n < 0) return MX_ERR_SHAPE;
+    if (q.n > kMaxExtent || (sum += mx::adam_chunks(q.n)) > kMaxAdamChunks) return MX_ERR_INDEX_OVERFLOW;
+    if (!all_aligned({q.p, q.g, q.m.codes, q.v.codes, q.copy})) return MX_ERR_ALIGN;
+    if (((uintptr_t)q.m.scales | (uintptr_t)q.v.scales) & 3u) return MX_ERR_ALIGN;
+    if (q.n == 0) continue;
+    if (!q.p || !q.g || !q.m.codes || !q.v.codes) return MX_ERR_NULL;
+    // states in binary32 have no scales
+    if (q.state_bits == 8 ? !q.m.scales || !q.v.scales : q.m.scales || q.v.scales) return MX_ERR_NULL;
+  }
+  *chunks = sum;
+  return MX_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1199,33 +1222,56 @@ int mx_head_loss_bwd(const mx_head_loss_bwd_args* args, void* stream) {
   return launched(mx::launch_to_bf16(a.sums, a.M, a.K, static_cast<uint16_t*>(a.dX), a.lddx, s));
 }
 
-int mx_adamw(const mx_adamw_item* items, int64_t n, const mx_adamw_args* args, void* stream) {
-  if (!args || (n > 0 && !items)) return MX_ERR_NULL;
-  if (n < 0 || n > MX_ADAMW_MAX_ITEMS) return MX_ERR_SHAPE;
+int mx_adamw_table_size(const mx_adamw_item* items, int64_t n, int64_t* chunks, int64_t* bytes) {
+  if (!chunks || !bytes) return MX_ERR_NULL;
+  const int st = validate_adamw_items(items, n, chunks);
+  if (st == MX_OK) *bytes = mx::adam_table_bytes(n, *chunks);
+  return st;
+}
+
+int mx_adamw_table(const mx_adamw_item* items, int64_t n, void* table, void* stream) {
+  int64_t chunks = 0;
+  int st = validate_adamw_items(items, n, &chunks);
+  if (st != MX_OK) return st;
+  if (n > 0 && !table) return MX_ERR_NULL;
+  if (!aligned16(table)) return MX_ERR_ALIGN;
+  if ((st = check_device()) != MX_OK) return st;
+  mx::AdamFill f;
+  memset(&f, 0, sizeof f);
+  f.items = static_cast<mx::AdamItem*>(table);
+  f.chunk_item = reinterpret_cast<int32_t*>(f.items + n);
+  int64_t first = 0;
+  for (f.at = 0; f.at < n; f.at += mx::kAdamFill) {
+    const int count = (int)(n - f.at < mx::kAdamFill ? n - f.at : mx::kAdamFill);
+    for (int i = 0; i < count; ++i) {
+      const mx_adamw_item& q = items[f.at + i];
+      f.item[i] = mx::AdamItem{q.p, q.g, q.m.codes, q.v.codes, bytes(q.m.scales), bytes(q.v.scales),
+                               static_cast<uint16_t*>(q.copy), q.n, (int32_t)first, q.g_dtype == MX_F32};
+      first += mx::adam_chunks(q.n);
+    }
+    if ((st = launched(mx::launch_adam_fill(f, count, static_cast<hipStream_t>(stream)))) != MX_OK) return st;
+  }
+  return MX_OK;
+}
+
+int mx_adamw(const void* table, int64_t n, int64_t chunks, const mx_adamw_args* args, void* stream) {
+  if (!args) return MX_ERR_NULL;
   const mx_adamw_args& a = *args;
   const auto unit = [](double b) { return b >= 0.0 && b < 1.0; };
   const auto plain = [](double x) { return x >= 0.0 && !isinf(x); };
+  if (n < 0 || n > MX_ADAMW_MAX_ITEMS || chunks < 0 || chunks > kMaxAdamChunks || (n == 0 && chunks > 0)) return MX_ERR_SHAPE;
   if (!unit(a.beta1) || !unit(a.beta2) || !plain(a.eps) || !plain(a.weight_decay) || !plain(a.lr)) return MX_ERR_SHAPE;
   if (!a.state && a.step < 1) return MX_ERR_SHAPE;
-  if (!all_aligned({a.state}) || ((uintptr_t)a.grad_scale & 3u) || ((uintptr_t)a.lr_device & 3u)) return MX_ERR_ALIGN;
-  if (a.lr_device && !a.state) return MX_ERR_NULL;
-  for (int64_t i = 0; i < n; ++i) {
-    const mx_adamw_item& q = items[i];
-    if (!dtype_ok(q.g_dtype) || (q.state_bits != 8 && q.state_bits != 32)) return MX_ERR_FORMAT;
-    if (q.n < 0) return MX_ERR_SHAPE;
-    if (q.n > (1ll << 34)) return MX_ERR_INDEX_OVERFLOW;
-    if (!all_aligned({q.p, q.g, q.m.codes, q.m.scales, q.v.codes, q.v.scales, q.copy})) return MX_ERR_ALIGN;
-    if (q.n == 0) continue;
-    if (!q.p || !q.g || !q.m.codes || !q.v.codes) return MX_ERR_NULL;
-    // states in binary32 have no scales
-    if (q.state_bits == 8 ? !q.m.scales || !q.v.scales : q.m.scales || q.v.scales) return MX_ERR_NULL;
-  }
+  if (!all_aligned({table, a.state}) || ((uintptr_t)a.grad_scale & 3u) || ((uintptr_t)a.lr_device & 3u)) return MX_ERR_ALIGN;
+  if ((n > 0 && !table) || (a.lr_device && !a.state)) return MX_ERR_NULL;
   int st = check_device();
   if (st != MX_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const mx::AdamHyper h = {a.lr, a.beta1, a.beta2, a.eps, a.weight_decay};
   mx::AdamParams p;
   memset(&p, 0, sizeof p);
+  p.items = static_cast<const mx::AdamItem*>(table);
+  p.chunk_item = reinterpret_cast<const int32_t*>(p.items + n);
   p.grad_scale = a.grad_scale;
   p.seed = a.seed;
   if (a.state) {
@@ -1235,19 +1281,7 @@ int mx_adamw(const mx_adamw_item* items, int64_t n, const mx_adamw_args* args, v
     p.f = mx::adam_factors(h, a.step);
     p.step = (uint32_t)a.step;
   }
-  int count = 0;
-  for (int64_t i = 0; i < n; ++i) {
-    const mx_adamw_item& q = items[i];
-    if (q.n > 0) {
-      p.item[count++] = mx::AdamItem{q.p, q.g, q.m.codes, q.v.codes, bytes(q.m.scales), bytes(q.v.scales),
-                                     static_cast<uint16_t*>(q.copy), q.n, q.g_dtype == MX_F32, (uint32_t)i};
-    }
-    if (count == mx::kAdamItems || (i == n - 1 && count > 0)) {
-      if ((st = launched(mx::launch_adam(p, count, s))) != MX_OK) return st;
-      count = 0;
-    }
-  }
-  return MX_OK;
+  return chunks > 0 ? launched(mx::launch_adam(p, chunks, s)) : MX_OK;
 }
 
 const char* mx_status_str(int status) {

@@ -143,35 +143,85 @@ struct HeadLossParams : GemmParams {
   }
 };
 
+// Sixteen elements of K of token m's and class y's rows (E4M3), multiplied in
+// binary32: unit u of the row's 8 a K group.  NaN under a NaN scale.
+__device__ __forceinline__ float e4m3_unit(const GemmParams& p, int64_t m, int64_t y, int u) {
+  const int64_t ga = (int64_t)(u >> 3) * p.M + m, gb = (int64_t)(u >> 3) * p.b_group_rows + y;
+  const uint4 a = *reinterpret_cast<const uint4*>(p.a_codes + ga * 128 + 16 * (u & 7));
+  const uint4 b = *reinterpret_cast<const uint4*>(p.b_codes + gb * 128 + 16 * (u & 7));
+  const int sa = p.a_scales[ga * 4 + ((u & 7) >> 1)], sb = p.b_scales[gb * 4 + ((u & 7) >> 1)];
+  const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+  float sum = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    float x[4], z[4];
+    e4m3_decode4(aw[w], 1.0f, x);
+    e4m3_decode4(bw[w], 1.0f, z);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum = __builtin_fmaf(x[e], z[e], sum);
+  }
+  return sa == 255 || sb == 255 ? __builtin_nanf("") : __builtin_ldexpf(sum, sa + sb - 254);
+}
+
 // Joins the parts of ROWS tokens a workgroup: 256 / ROWS threads a token take
 // every so manieth tile, then meet in LDS in a fixed order.
-template <int ROWS>
-__global__ __launch_bounds__(256) void head_join_kernel(const Part* __restrict__ parts, int64_t tiles, int64_t M,
-                                                        int64_t V, const int64_t* __restrict__ labels,
+//
+// REDO (E4M3): the matrix cores leave about 1.5e-5 of its norm in a logit, and of
+// the loss that is the label's logit's error alone, as those of the others
+// average out in lse.  The label's logit l is therefore formed again, to
+// binary32 accuracy, and put in its place in both terms: with d the difference
+// and q = exp(l - lse), lse grows by q d (d^2 is under 1e-9), so the loss falls by
+// (1 - q) d.  lse is stored as it is: the gradient's probabilities, formed from
+// the same products, then add up to 1.
+template <int ROWS, bool REDO>
+__global__ __launch_bounds__(256) void head_join_kernel(GemmParams p, const Part* __restrict__ parts, int64_t tiles,
+                                                        const int64_t* __restrict__ labels,
                                                         const float* __restrict__ label_logit,
                                                         float* __restrict__ loss, float* __restrict__ lse) {
   constexpr int kSides = 256 / ROWS;
   __shared__ Part red[256];
+  __shared__ float dots[REDO ? 256 : 1];
   const int t = threadIdx.x, row = t % ROWS, side = t / ROWS;
-  const int64_t m = (int64_t)blockIdx.x * ROWS + row;
+  const int64_t M = p.M, m = (int64_t)blockIdx.x * ROWS + row;
   Part all = {-__builtin_inff(), 0.0f};
+  const int64_t y = m < M ? labels[m] : -1;
+  const bool counts = y >= 0 && y < p.N;
+  float dot = 0.0f;
   if (m < M) {
+    if constexpr (REDO) {
+      const int units = (int)((p.K + 127) / 128) * 8;
+      if (counts) {
+        for (int u = side; u < units; u += kSides) dot = dot + e4m3_unit(p, m, y, u);
+      }
+    }
 #pragma unroll 4
     for (int64_t q = side; q < tiles; q += kSides) all = joined(all, parts[q * M + m]);
   }
   red[t] = all;
+  if constexpr (REDO) dots[t] = dot;
   __syncthreads();
 #pragma unroll
   for (int half = kSides / 2; half > 0; half /= 2) {
-    if (side < half) red[t] = joined(red[t], red[t + half * ROWS]);
+    if (side < half) {
+      red[t] = joined(red[t], red[t + half * ROWS]);
+      if constexpr (REDO) dots[t] = dots[t] + dots[t + half * ROWS];
+    }
     __syncthreads();
   }
   if (side != 0 || m >= M) return;
   all = red[t];
   const float total = (all.top + log2_hw(all.sum)) * kLn2;
   lse[m] = total;
-  const int64_t y = labels[m];
-  loss[m] = y >= 0 && y < V ? total - label_logit[m] : 0.0f;
+  float l = 0.0f;
+  if (counts) {
+    const float logit = label_logit[m];
+    l = total - logit;
+    if constexpr (REDO) {
+      const float d = dots[t] - logit, q = exp2_hw(-l * kLog2e);
+      if (__builtin_fabsf(d) < __builtin_inff()) l = l - (1.0f - q) * d;
+    }
+  }
+  loss[m] = l;
 }
 
 // ------------------------------------------------------------------ gradient
@@ -354,6 +404,19 @@ P head_params(const HeadParams& h) {
   return p;
 }
 
+template <int ROWS>
+hipError_t launch_join(const HeadLossParams& p, int fmt, int64_t tiles, float* loss, float* lse, hipStream_t stream) {
+  const dim3 grid((unsigned)((p.M + ROWS - 1) / ROWS));
+  const GemmParams& g = p;
+  if (fmt == kE4M3)
+    hipLaunchKernelGGL((head_join_kernel<ROWS, true>), grid, dim3(256), 0, stream, g, p.parts, tiles, p.labels,
+                       p.label_logit, loss, lse);
+  else
+    hipLaunchKernelGGL((head_join_kernel<ROWS, false>), grid, dim3(256), 0, stream, g, p.parts, tiles, p.labels,
+                       p.label_logit, loss, lse);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 int64_t head_work_floats(int64_t M, int64_t V) { return (V + 127) / 128 * 2 * M + M; }
@@ -368,13 +431,7 @@ hipError_t launch_head_loss(const HeadParams& h, int fmt, float* loss, float* ls
   const int64_t tiles = (h.V + width - 1) / width;
   // 16 tokens a workgroup read whole 128-byte lines of a tile's parts, where
   // that leaves enough workgroups
-  if (h.M >= 2048)
-    hipLaunchKernelGGL(head_join_kernel<16>, dim3((unsigned)((h.M + 15) / 16)), dim3(256), 0, stream, p.parts, tiles,
-                       h.M, h.V, h.labels, p.label_logit, loss, lse);
-  else
-    hipLaunchKernelGGL(head_join_kernel<1>, dim3((unsigned)h.M), dim3(256), 0, stream, p.parts, tiles, h.M, h.V,
-                       h.labels, p.label_logit, loss, lse);
-  return hipGetLastError();
+  return h.M >= 2048 ? launch_join<16>(p, fmt, tiles, loss, lse, stream) : launch_join<1>(p, fmt, tiles, loss, lse, stream);
 }
 
 hipError_t launch_head_grad(const HeadParams& h, const HeadGradOut& o, int fmt, hipStream_t stream) {

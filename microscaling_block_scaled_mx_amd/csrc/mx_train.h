@@ -119,26 +119,36 @@ struct AdamItem {
   uint8_t* v_scales;
   uint16_t* copy;   // bf16 [n] or nullptr
   int64_t n;
+  int32_t first;    // its first chunk
   int32_t g_f32;
-  uint32_t index;   // of the tensor, for its random words
 };
-// As many as the launch's arguments hold.
-constexpr int kAdamItems = 40;
+constexpr int64_t kAdamChunk = 4096;  // elements a workgroup
+inline int64_t adam_chunks(int64_t n) { return (n + kAdamChunk - 1) / kAdamChunk; }
+// The table on the device: the items, then of every chunk its item's place.
+inline int64_t adam_table_bytes(int64_t items, int64_t chunks) { return items * (int64_t)sizeof(AdamItem) + 4 * chunks; }
+// Writes items [at, at + count) (count <= kAdamFill, as many as a launch's
+// arguments hold) and their chunks into the table of n.
+constexpr int kAdamFill = 48;
+struct AdamFill {
+  AdamItem item[kAdamFill];
+  int64_t at;
+  AdamItem* items;
+  int32_t* chunk_item;
+};
+static_assert(sizeof(AdamFill) <= 4096, "kernel arguments");
+hipError_t launch_adam_fill(const AdamFill& f, int count, hipStream_t stream);
 struct AdamParams {
-  AdamItem item[kAdamItems];
-  int first[kAdamItems];        // first workgroup of each; past the last item: INT_MAX
+  const AdamItem* items;
+  const int32_t* chunk_item;
   AdamFactors f;
   const AdamState* state;       // on the device, or nullptr: f and step
   const float* grad_scale;      // on the device, or nullptr
   uint64_t seed;
   uint32_t step;
 };
-static_assert(sizeof(AdamParams) <= 4096, "kernel arguments");
-constexpr int64_t kAdamChunk = 4096;  // elements a workgroup
 // Advances the device's step count and forms its factors; lr from the device
 // where given.
 hipError_t launch_adam_advance(AdamState* state, const AdamHyper& h, const float* lr, hipStream_t stream);
-// items: `count` <= kAdamItems filled in; `first` is filled in here.
-hipError_t launch_adam(AdamParams& p, int count, hipStream_t stream);
+hipError_t launch_adam(const AdamParams& p, int64_t chunks, hipStream_t stream);
 
 }  // namespace mx

@@ -224,7 +224,11 @@ def lib():
         L.mx_head_loss_work_bytes.restype = i64
         L.mx_head_loss_work_bytes.argtypes = [i64, i64]
         L.mx_adamw.restype = ci
-        L.mx_adamw.argtypes = [vp, i64, vp, vp]
+        L.mx_adamw.argtypes = [vp, i64, i64, vp, vp]
+        L.mx_adamw_table.restype = ci
+        L.mx_adamw_table.argtypes = [vp, i64, vp, vp]
+        L.mx_adamw_table_size.restype = ci
+        L.mx_adamw_table_size.argtypes = [vp, i64, ctypes.POINTER(i64), ctypes.POINTER(i64)]
         L.mx_status_str.restype = ctypes.c_char_p
         L.mx_status_str.argtypes = [ci]
         L.mx_device_supported.restype = ci
@@ -843,16 +847,22 @@ def head_loss_bwd(a, b, Wc, Xc, M: int, V: int, K: int, fmt: int, scale_mode: in
 
 
 class AdamwItems:
-    """The tensors of adamw, checked and laid out for mx_adamw once: make it
+    """The tensors of adamw and their table on the device, written once: make it
     anew when a tensor is replaced (it keeps the tensors alive)."""
 
-    def __init__(self, items):
+    def __init__(self, items, stream=None):
         self.tensors = items = [dict(it) for it in items]
-        self.array = (AdamwItem * max(len(items), 1))()
+        array = (AdamwItem * max(len(items), 1))()
         self.n = len(items)
-        self.device = _current()[0]
+        self.device, here = _current()
         for i, it in enumerate(items):
-            self.array[i] = self._item(it, f"adamw item {i}")
+            array[i] = self._item(it, f"adamw item {i}")
+        chunks, size = ctypes.c_int64(0), ctypes.c_int64(0)
+        _check(lib().mx_adamw_table_size(array, self.n, ctypes.byref(chunks), ctypes.byref(size)), "mx_adamw_table_size")
+        self.chunks = chunks.value
+        self.table = torch.empty(max(size.value, 16), dtype=torch.uint8, device="cuda")
+        self.address = self.table.data_ptr()
+        _check(lib().mx_adamw_table(array, self.n, self.address, _handle(stream, here)), "mx_adamw_table")
 
     def _item(self, it, what):
         n, dev = it["p"].numel(), self.device
@@ -870,12 +880,12 @@ class AdamwItems:
                          _matrix(it.get("copy"), 1, n, dev, what + " copy", (BF16,))[0], n, g_dtype, state[0][0])
 
 
-def adamw_items(items) -> AdamwItems:
-    """The tensors of an optimizer for adamw: each a dict of p (float32), g
+def adamw_items(items, stream=None) -> AdamwItems:
+    """mx_adamw_table: the tensors of an optimizer for adamw, each a dict of p (float32), g
     (bf16 or float32), m and v (both float32, or both (codes, scales) of
     alloc_packed(1, n rounded up to 32, E4M3), zeroed before the first step) and
     optionally copy (bf16), all of one length and contiguous."""
-    return AdamwItems(items)
+    return AdamwItems(items, stream)
 
 
 def adamw(items, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.0,
@@ -885,7 +895,7 @@ def adamw(items, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float
     ADAMW_STATE_BYTES, counts it on the device.  lr_device and grad_scale: float32
     device tensors of one element."""
     if not isinstance(items, AdamwItems):
-        items = AdamwItems(items)
+        items = AdamwItems(items, stream)
     dev, here = _current()
     if items.n and items.device != dev:
         raise MXError(7, f"adamw: the tensors are on cuda:{items.device}, the current device is cuda:{dev}")
@@ -893,7 +903,7 @@ def adamw(items, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float
                        _work(state, ADAMW_STATE_BYTES, dev, "adamw state"),
                        _matrix(lr_device, 1, 1, dev, "adamw lr_device", (F32,))[0],
                        _matrix(grad_scale, 1, 1, dev, "adamw grad_scale", (F32,))[0])
-    _check(lib().mx_adamw(items.array, items.n, args, _handle(stream, here)), "mx_adamw")
+    _check(lib().mx_adamw(items.address, items.n, items.chunks, args, _handle(stream, here)), "mx_adamw")
 
 
 def status_str(st: int) -> str:

@@ -137,35 +137,63 @@ def test_head_loss_bwd_refusals(kw, want):
     assert mx.lib().mx_head_loss_bwd(ctypes.byref(head_bwd_args(**kw)), None) == want
 
 
-def adamw_refusal(item=(), args=(), n=1):
-    it = struct_of(mx.AdamwItem, dict(p=P[0], g=P[1], m=pk(2), v=pk(4), copy=P[6], n=100, state_bits=8), dict(item))
-    a = struct_of(mx.AdamwArgs, dict(lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8, step=1), dict(args))
-    return mx.lib().mx_adamw(ctypes.byref(it), n, ctypes.byref(a), None)
+def adamw_item(**kw):
+    return struct_of(mx.AdamwItem, dict(p=P[0], g=P[1], m=pk(2), v=pk(4), copy=P[6], n=100, state_bits=8), kw)
 
 
-@pytest.mark.parametrize("item,args,want", [
-    (dict(g_dtype=2), {}, FORMAT), (dict(state_bits=16), {}, FORMAT), (dict(n=-1), {}, SHAPE), (dict(n=(1 << 34) + 1), {}, OVERFLOW),
-    (dict(p=None), {}, NULL), (dict(g=None), {}, NULL), (dict(m=NONE), {}, NULL), (dict(v=mx.Packed(P[0], None)), {}, NULL),
-    (dict(state_bits=32), {}, NULL), (dict(p=ODD), {}, ALIGN), (dict(g=ODD), {}, ALIGN), (dict(copy=ODD), {}, ALIGN),
-    (dict(m=mx.Packed(P[0], ODD)), {}, ALIGN),
-    ({}, dict(beta1=1.0), SHAPE), ({}, dict(beta2=-0.1), SHAPE), ({}, dict(beta1=float("nan")), SHAPE),
-    ({}, dict(lr=-1e-3), SHAPE), ({}, dict(lr=float("nan")), SHAPE), ({}, dict(eps=float("inf")), SHAPE),
-    ({}, dict(weight_decay=-0.1), SHAPE), ({}, dict(step=0), SHAPE), ({}, dict(step=-3), SHAPE),
-    ({}, dict(state=ODD), ALIGN), ({}, dict(grad_scale=ctypes.c_void_p(0x1002)), ALIGN),
-    ({}, dict(state=P[7], lr_device=ctypes.c_void_p(0x1001)), ALIGN), ({}, dict(lr_device=P[7]), NULL),
+def table_status(item, n=1):
+    chunks, size = ctypes.c_int64(-1), ctypes.c_int64(-1)
+    st = mx.lib().mx_adamw_table_size(ctypes.byref(item), n, ctypes.byref(chunks), ctypes.byref(size))
+    return st, chunks.value, size.value
+
+
+@pytest.mark.parametrize("item,want", [
+    (dict(g_dtype=2), FORMAT), (dict(state_bits=16), FORMAT), (dict(n=-1), SHAPE), (dict(n=(1 << 40) + 1), OVERFLOW),
+    (dict(n=1 << 37), OVERFLOW),
+    (dict(p=None), NULL), (dict(g=None), NULL), (dict(m=NONE), NULL), (dict(v=mx.Packed(P[0], None)), NULL),
+    (dict(state_bits=32), NULL), (dict(p=ODD), ALIGN), (dict(g=ODD), ALIGN), (dict(copy=ODD), ALIGN),
+    (dict(m=mx.Packed(ODD, P[0])), ALIGN), (dict(v=mx.Packed(P[0], ctypes.c_void_p(0x1002))), ALIGN),
 ])
-def test_adamw_refusals(item, args, want):
-    assert adamw_refusal(item, args) == want
+def test_adamw_table_refusals(item, want):
+    assert table_status(adamw_item(**item))[0] == want
+    assert mx.lib().mx_adamw_table(ctypes.byref(adamw_item(**item)), 1, P[7], None) == want
 
 
-def test_adamw_item_counts():
-    assert adamw_refusal(n=-1) == SHAPE
-    assert adamw_refusal(n=1000001) == SHAPE
+def test_adamw_table_sizes():
+    assert table_status(adamw_item()) == (0, 1, 72 + 4)
+    assert table_status(adamw_item(n=4097, v=mx.Packed(P[0], ODD))) == (0, 2, 72 + 8)
+    assert table_status(adamw_item(n=0, p=None, g=None, m=NONE, v=NONE)) == (0, 0, 72)
+    assert table_status(adamw_item(), -1)[0] == table_status(adamw_item(), 1000001)[0] == SHAPE
+    L = mx.lib()
+    c = ctypes.c_int64(0)
+    assert L.mx_adamw_table_size(None, 1, ctypes.byref(c), ctypes.byref(c)) == NULL
+    assert L.mx_adamw_table_size(None, 0, None, ctypes.byref(c)) == NULL
+    assert L.mx_adamw_table(ctypes.byref(adamw_item()), 1, None, None) == NULL
+    assert L.mx_adamw_table(ctypes.byref(adamw_item()), 1, ODD, None) == ALIGN
+    assert L.mx_adamw_table(None, 0, None, None) == OK_HERE
+
+
+@pytest.mark.parametrize("args,want", [
+    (dict(beta1=1.0), SHAPE), (dict(beta2=-0.1), SHAPE), (dict(beta1=float("nan")), SHAPE), (dict(lr=-1e-3), SHAPE),
+    (dict(lr=float("nan")), SHAPE), (dict(eps=float("inf")), SHAPE), (dict(weight_decay=-0.1), SHAPE),
+    (dict(step=0), SHAPE), (dict(step=-3), SHAPE), (dict(state=ODD), ALIGN),
+    (dict(grad_scale=ctypes.c_void_p(0x1002)), ALIGN), (dict(state=P[7], lr_device=ctypes.c_void_p(0x1001)), ALIGN),
+    (dict(lr_device=P[7]), NULL),
+])
+def test_adamw_refusals(args, want):
+    a = struct_of(mx.AdamwArgs, dict(lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8, step=1), args)
+    assert mx.lib().mx_adamw(P[0], 1, 1, ctypes.byref(a), None) == want
+
+
+def test_adamw_table_arguments():
     a = struct_of(mx.AdamwArgs, dict(lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8, step=1), {})
-    assert mx.lib().mx_adamw(None, 1, ctypes.byref(a), None) == NULL
-    assert mx.lib().mx_adamw(None, 0, None, None) == NULL
-    assert mx.lib().mx_adamw(None, 0, ctypes.byref(a), None) == OK_HERE
-    assert adamw_refusal(dict(n=0, p=None, g=None, m=NONE, v=NONE)) == OK_HERE
+    L = mx.lib()
+    assert L.mx_adamw(P[0], 1, 1, None, None) == NULL
+    assert L.mx_adamw(None, 1, 1, ctypes.byref(a), None) == NULL
+    assert L.mx_adamw(ODD, 1, 1, ctypes.byref(a), None) == ALIGN
+    assert L.mx_adamw(P[0], -1, 1, ctypes.byref(a), None) == L.mx_adamw(P[0], 1, -1, ctypes.byref(a), None) == SHAPE
+    assert L.mx_adamw(P[0], 1, 1 << 24, ctypes.byref(a), None) == L.mx_adamw(P[0], 0, 1, ctypes.byref(a), None) == SHAPE
+    assert L.mx_adamw(None, 0, 0, ctypes.byref(a), None) == OK_HERE
 
 
 def test_no_tokens_need_no_pointers():
@@ -853,7 +881,7 @@ def check_adam32(before, after, g, step, scale):
 @gpu
 @pytest.mark.parametrize("g_dtype", [mx.BF16, mx.F32])
 def test_adamw_32_bits(g_dtype):
-    """Tensors of every kind of length in one call, of more than one launch."""
+    """Tensors of every kind of length in one step, their table written by more than one launch."""
     rng = np.random.default_rng(1)
     sizes = LENGTHS * 4
     t = [{"p": tensor(rng, (n,), 1), "g": tensor(rng, (n,), g_dtype, 0.1), "m": tensor(rng, (n,), 1, 0.1),
