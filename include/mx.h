@@ -891,7 +891,7 @@ int64_t mx_head_loss_work_bytes(int64_t M, int64_t V);
  * in binary32, the factors formed in binary64.
  *
  * The tensors are named once, in a table on the device: mx_adamw_table_size
- * gives its bytes and the number of chunks (of 4096 elements) in it,
+ * gives its bytes and the number of chunks (of 2048 elements) in it,
  * mx_adamw_table writes it (by launches that carry the items, so it can be
  * captured too; `items` is read before the call returns), and mx_adamw makes a
  * step over it in one launch.  A table holds addresses: it is written anew when a

@@ -11,9 +11,9 @@
 // Everything else is binary32, and the update takes m and v before they are
 // rounded.
 //
-// Bound by HBM: 16 bytes an element with bf16 gradients and 8-bit states (28
-// with binary32 states), each read and written once.  A thread takes eight
-// consecutive elements a step, four lanes a block; a workgroup finds its tensor
+// Bound by HBM: 16 bytes an element with bf16 gradients, 8-bit states and a bf16
+// copy (28 with binary32 states), each read and written once.  A thread takes
+// eight consecutive elements, four lanes a block of 32; a workgroup finds its tensor
 // by two loads from a table on the device, which is written once (by launches
 // whose arguments carry the items, so that nothing is copied from the host).
 #include <math.h>
@@ -141,54 +141,51 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamParams all) {
   const float gs = all.grad_scale != nullptr ? *all.grad_scale : 1.0f;
   const bool eight = it.m_scales != nullptr;
   const int64_t n = it.n, padded = (n + 127) & ~(int64_t)127;
-  const int64_t c0 = (int64_t)(block - it.first) * kAdamChunk;
-#pragma unroll 1
-  for (int64_t c = c0 + 8 * (int64_t)threadIdx.x; c - 8 * (int64_t)threadIdx.x < c0 + kAdamChunk; c += 8 * 256) {
-    float p[8], g[8], m[8], v[8];
-    read8(it.p, c, n, 1, p);
-    read8(it.g, c, n, it.g_f32, g);
-    if (eight) {
-      read_state8(it.m, it.m_scales, c, c < padded, m);
-      read_state8(it.v, it.v_scales, c, c < padded, v);
+  const int64_t c = (int64_t)(block - it.first) * kAdamChunk + 8 * (int64_t)threadIdx.x;
+  float p[8], g[8], m[8], v[8];
+  read8(it.p, c, n, 1, p);
+  read8(it.g, c, n, it.g_f32, g);
+  if (eight) {
+    read_state8(it.m, it.m_scales, c, c < padded, m);
+    read_state8(it.v, it.v_scales, c, c < padded, v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = v[e] * v[e];
-    } else {
-      read8(it.m, c, n, 1, m);
-      read8(it.v, c, n, 1, v);
+    for (int e = 0; e < 8; ++e) v[e] = v[e] * v[e];
+  } else {
+    read8(it.m, c, n, 1, m);
+    read8(it.v, c, n, 1, v);
+  }
+  float root[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const bool in = c + e < n;
+    const float x = g[e] * gs;
+    m[e] = in ? __builtin_fmaf(f.b1, m[e], f.g1 * x) : 0.0f;
+    v[e] = in ? __builtin_fmaf(f.b2, v[e], f.g2 * x * x) : 0.0f;
+    root[e] = __builtin_sqrtf(v[e]);
+    p[e] = __builtin_fmaf(-f.rate, m[e] / __builtin_fmaf(root[e], f.inv_root, f.eps), p[e] * f.decay);
+  }
+  write8(it.p, c, n, 1, p);
+  if (it.copy != nullptr) write8(it.copy, c, n, 0, p);
+  if (eight) {
+    uint32_t w[8], rm[8], rv[8];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const uint64_t i = ((uint64_t)c >> 2) + q;
+      uint32_t x[4] = {(uint32_t)i, (uint32_t)(i >> 32), (uint32_t)place, step};
+      philox4x32_10(x, (uint32_t)all.seed, (uint32_t)(all.seed >> 32));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[4 * q + e] = x[e];
     }
-    float root[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const bool in = c + e < n;
-      const float x = g[e] * gs;
-      m[e] = in ? __builtin_fmaf(f.b1, m[e], f.g1 * x) : 0.0f;
-      v[e] = in ? __builtin_fmaf(f.b2, v[e], f.g2 * x * x) : 0.0f;
-      root[e] = __builtin_sqrtf(v[e]);
-      p[e] = __builtin_fmaf(-f.rate, m[e] / __builtin_fmaf(root[e], f.inv_root, f.eps), p[e] * f.decay);
+      rm[e] = w[e] & 0xffffu;
+      rv[e] = w[e] >> 16;
     }
-    write8(it.p, c, n, 1, p);
-    if (it.copy != nullptr) write8(it.copy, c, n, 0, p);
-    if (eight) {
-      uint32_t w[8], rm[8], rv[8];
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const uint64_t i = ((uint64_t)c >> 2) + q;
-        uint32_t x[4] = {(uint32_t)i, (uint32_t)(i >> 32), (uint32_t)place, step};
-        philox4x32_10(x, (uint32_t)all.seed, (uint32_t)(all.seed >> 32));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[4 * q + e] = x[e];
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        rm[e] = w[e] & 0xffffu;
-        rv[e] = w[e] >> 16;
-      }
-      write_state8(it.m, it.m_scales, c, c < padded, m, rm);
-      write_state8(it.v, it.v_scales, c, c < padded, root, rv);
-    } else {
-      write8(it.m, c, n, 1, m);
-      write8(it.v, c, n, 1, v);
-    }
+    write_state8(it.m, it.m_scales, c, c < padded, m, rm);
+    write_state8(it.v, it.v_scales, c, c < padded, root, rv);
+  } else {
+    write8(it.m, c, n, 1, m);
+    write8(it.v, c, n, 1, v);
   }
 }
 

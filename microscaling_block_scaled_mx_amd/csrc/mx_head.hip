@@ -84,38 +84,43 @@ struct HeadLossParams : GemmParams {
     const int lrow = lane & 31, g = lane >> 5;
     const int64_t mw = m0 + wm * CF::kWM, nw = n0 + wn * CF::kWN;
     Part* const red = reinterpret_cast<Part*>(smem);  // [kWavesN][2 kWM]
-    if (nw + CF::kWN > N) {  // (uniform) classes past the end count nothing
+    // `masked`: the wavefront's classes end inside its columns; those past the
+    // end count nothing
+    const auto rows = [&](auto masked) __attribute__((always_inline)) {
+      const int limit = N - nw < CF::kWN ? (int)(N - nw) : CF::kWN;  // (may be <= 0)
 #pragma unroll
-      for (int i = 0; i < CF::kMI; ++i)
+      for (int i = 0; i < CF::kMI; ++i) {
+        const auto logit = [&](int j, int e) __attribute__((always_inline)) {
+          if constexpr (!decltype(masked)::value) return acc[i][j][e];
+          else return 32 * j + 8 * (e / 4) + 4 * g + e % 4 < limit ? acc[i][j][e] : -__builtin_inff();
+        };
+        float top = -__builtin_inff();
 #pragma unroll
         for (int j = 0; j < CF::kNJ; ++j)
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            acc[i][j][e] = nw + 32 * j + 8 * (e / 4) + 4 * g + e % 4 < N ? acc[i][j][e] : -__builtin_inff();
-    }
+          for (int e = 0; e < 16; ++e) top = __builtin_fmaxf(top, logit(j, e));
+        // a token's logits lie in lanes l and l ^ 32: one maximum for both
+        const uint32_t tb = __float_as_uint(top);
+        const auto tt = __builtin_amdgcn_permlane32_swap(tb, tb, false, false);
+        top = __builtin_fmaxf(__uint_as_float(tt[0]), __uint_as_float(tt[1])) * kLog2e;
+        const float base = top == -__builtin_inff() ? 0.0f : top;
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < CF::kNJ; ++j)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) sum = sum + exp2_hw(__builtin_fmaf(logit(j, e), kLog2e, -base));
+        const uint32_t sb = __float_as_uint(sum);
+        const auto ss = __builtin_amdgcn_permlane32_swap(sb, sb, false, false);
+        sum = __uint_as_float(ss[0]) + __uint_as_float(ss[1]);
+        if (g == 0) red[wn * 2 * CF::kWM + wm * CF::kWM + 32 * i + lrow] = Part{top, sum};
+      }
+    };
+    if (nw + CF::kWN > N) rows(std::true_type{});  // (uniform)
+    else rows(std::false_type{});
+    // the labels' logits, from the lanes that hold them
 #pragma unroll
     for (int i = 0; i < CF::kMI; ++i) {
       const int64_t m = mw + 32 * i + lrow;
-      float top = -__builtin_inff();
-#pragma unroll
-      for (int j = 0; j < CF::kNJ; ++j)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) top = __builtin_fmaxf(top, acc[i][j][e]);
-      // a token's logits lie in lanes l and l ^ 32: one maximum for both
-      const uint32_t tb = __float_as_uint(top);
-      const auto tt = __builtin_amdgcn_permlane32_swap(tb, tb, false, false);
-      top = __builtin_fmaxf(__uint_as_float(tt[0]), __uint_as_float(tt[1])) * kLog2e;
-      const float base = top == -__builtin_inff() ? 0.0f : top;
-      float sum = 0.0f;
-#pragma unroll
-      for (int j = 0; j < CF::kNJ; ++j)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) sum = sum + exp2_hw(__builtin_fmaf(acc[i][j][e], kLog2e, -base));
-      const uint32_t sb = __float_as_uint(sum);
-      const auto ss = __builtin_amdgcn_permlane32_swap(sb, sb, false, false);
-      sum = __uint_as_float(ss[0]) + __uint_as_float(ss[1]);
-      if (g == 0) red[wn * 2 * CF::kWM + wm * CF::kWM + 32 * i + lrow] = Part{top, sum};
-      // the label's logit, from the lane that holds it
       const int64_t y = m < M ? labels[m] : -1;
       const int at = y >= nw && y < nw + CF::kWN && y < N ? (int)(y - nw) : -1;
       if (__builtin_amdgcn_ballot_w64(at >= 0) != 0) {
@@ -354,25 +359,42 @@ hipError_t launch_tiles(const P& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Classes a tile: 256 x 256 where such tiles fill the chip, else 128 x 128, two
-// a compute unit.
-int tile_classes(int64_t M, int64_t N) {
-  const int64_t t256 = ((M + 255) / 256) * ((N + 255) / 256);
-  return M > 128 && t256 >= cu_count() ? 256 : 128;
+// The output tile.  128 x 128, two a compute unit, where 256 x 256 would leave
+// units idle (rounds of the chip by area, as mx_gemm_act picks them; 333 tokens,
+// 50257 classes, K = 800 in E2M1 / E2M3 / E4M3: 21 / 25 / 32 us, 256 x 256 26 /
+// 27 / 39; gradient 30 / 41 / 44 against 38 / 47 / 48; 8192 x 16384 x 4096: 282 /
+// 368 / 471, 256 x 256 246 / 298 / 486; gradient 319 / 432 / 606 against 291 /
+// 381 / 520).  E2M1, whose products are over soonest, over several rounds: 256 x
+// 128, two a unit, so that one tile's exponentials and packs run beside
+// another's products (8192 x 16384 x 2048: 137 us, gradient 173; 256 x 256 142
+// and 186; E2M3 178 and 259 against 166 and 249).
+enum Tile { kTile128, kTile256x128, kTile256 };
+Tile pick_tile(int fmt, int64_t M, int64_t N) {
+  const int64_t cus = cu_count();
+  const int64_t t256 = ((M + 255) / 256) * ((N + 255) / 256), t128 = ((M + 127) / 128) * ((N + 127) / 128);
+  const int64_t rest = t128 % (2 * cus);  // a last round of at most one tile per unit takes 2/3 of a full one
+  const int64_t cost256 = (t256 + cus - 1) / cus * 65536;
+  const int64_t cost128 = (t128 / (2 * cus) * 32768 + (rest == 0 ? 0 : rest <= cus ? 22000 : 32768)) * 115 / 100;
+  if (cost256 > cost128) return kTile128;
+  return fmt == kE2M1 && t256 > cus ? kTile256x128 : kTile256;
 }
+int tile_classes(Tile t) { return t == kTile256 ? 256 : 128; }
 
 template <int FMT, class P>
-hipError_t launch_of(const P& p, hipStream_t stream) {
-  return tile_classes(p.M, p.N) == 256 ? launch_tiles<FMT, 256, 256, 1>(p, stream)
-                                       : launch_tiles<FMT, 128, 128, 2>(p, stream);
+hipError_t launch_of(const P& p, Tile tile, hipStream_t stream) {
+  if (tile == kTile256) return launch_tiles<FMT, 256, 256, 1>(p, stream);
+  if constexpr (FMT == kE2M1) {
+    if (tile == kTile256x128) return launch_tiles<FMT, 256, 128, 2>(p, stream);
+  }
+  return launch_tiles<FMT, 128, 128, 2>(p, stream);
 }
 
 template <class P>
-hipError_t launch_fmt(const P& p, int fmt, hipStream_t stream) {
+hipError_t launch_fmt(const P& p, int fmt, Tile tile, hipStream_t stream) {
   switch (fmt) {
-    case kE2M1: return launch_of<kE2M1>(p, stream);
-    case kE2M3: return launch_of<kE2M3>(p, stream);
-    case kE4M3: return launch_of<kE4M3>(p, stream);
+    case kE2M1: return launch_of<kE2M1>(p, tile, stream);
+    case kE2M3: return launch_of<kE2M3>(p, tile, stream);
+    case kE4M3: return launch_of<kE4M3>(p, tile, stream);
     default: return hipErrorInvalidValue;
   }
 }
@@ -425,9 +447,10 @@ hipError_t launch_head_loss(const HeadParams& h, int fmt, float* loss, float* ls
   HeadLossParams p = head_params<HeadLossParams>(h);
   p.parts = reinterpret_cast<Part*>(work);
   p.label_logit = work + (h.V + 127) / 128 * 2 * h.M;
-  const hipError_t e = launch_fmt(p, fmt, stream);
+  const Tile tile = pick_tile(fmt, h.M, h.V);
+  const hipError_t e = launch_fmt(p, fmt, tile, stream);
   if (e != hipSuccess) return e;
-  const int width = tile_classes(h.M, h.V);
+  const int width = tile_classes(tile);
   const int64_t tiles = (h.V + width - 1) / width;
   // 16 tokens a workgroup read whole 128-byte lines of a tile's parts, where
   // that leaves enough workgroups
@@ -450,7 +473,7 @@ hipError_t launch_head_grad(const HeadParams& h, const HeadGradOut& o, int fmt, 
   p.q_row_scales = o.row_scales;
   p.q_col_codes = o.col_codes;
   p.q_col_scales = o.col_scales;
-  return launch_fmt(p, fmt, stream);
+  return launch_fmt(p, fmt, pick_tile(fmt, p.M, p.N), stream);
 }
 
 hipError_t launch_to_bf16(const float* x, int64_t R, int64_t C, uint16_t* y, int64_t ldy, hipStream_t stream) {

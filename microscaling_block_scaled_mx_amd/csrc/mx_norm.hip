@@ -1,13 +1,14 @@
 // Layer norm: y = (x - mean) rstd gamma + beta with y packed as it is formed,
 // and its backward pass with the reduction of the weights' gradients.
 //
-// A row is held in registers, eight values a lane and step, by a wavefront
-// (C up to 2048) or a workgroup, so x is read once and the variance is taken
-// from the differences to the mean (two sums; one pass over the data).  Both
-// kernels are bound by HBM.  Workgroups walk over rows with a fixed stride:
-// the weights stay in registers, the next row's loads are in flight while the
-// current one is reduced, and the backward pass keeps its share of dgamma and
-// dbeta in registers until its rows are done.  Sums are binary32.
+// A row is held in registers by one to sixteen wavefronts, eight values a lane
+// and step, so x is read once and the variance is taken from the differences to
+// the mean (two sums; one pass over the data).  Both kernels are bound by HBM.
+// Workgroups hold as many rows side by side as fit and walk over the rest with a
+// fixed stride: the weights stay in registers, the next rows' loads are in
+// flight while the current ones are reduced, and the backward pass keeps its
+// share of dgamma and dbeta in registers until its rows are done.  Sums are
+// binary32.
 #include "mx_lanes.h"
 #include "mx_train.h"
 
@@ -15,45 +16,59 @@ namespace mx {
 
 namespace {
 
-// Rows of the thread groups: T threads a row, NV steps of 8 values each, WG
-// threads a workgroup (WG / T rows side by side).
-template <int T, int NV, int WG>
-struct RowCfg {
-  static constexpr int kRows = WG / T, kWaves = WG / 64, kPer = T / 64;  // wavefronts a row
-  static_assert(T % 64 == 0 && WG % T == 0, "whole wavefronts");
-  static constexpr int kMaxC = T * NV * 8;
+// How a workgroup holds rows: `waves` wavefronts a row, `rows` side by side.
+struct Split {
+  int waves, rows;
 };
 
-// Sums of N values over the T threads of a row, in all of them; `red` is one
-// of two LDS arrays used in turn, so that one barrier is enough.
-template <class CF, int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[N]) {
+// Sums of N values over a row's wavefronts, in all their lanes.  `red` is one of
+// two LDS arrays used in turn, so that one barrier is enough; its 16 slots are
+// added by a tree over 16 lanes (slots past the row's wavefronts count 0).
+template <int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[N], int waves, int first) {
 #pragma unroll
   for (int n = 0; n < N; ++n) v[n] = wave_sum(v[n]);
-  if constexpr (CF::kPer > 1) {
-    const int wave = threadIdx.x >> 6, first = wave / CF::kPer * CF::kPer;
-    if ((threadIdx.x & 63) == 0) {
+  if (waves == 1) return;  // (uniform)
+  const int lane = threadIdx.x & 63, slot = lane & 15;
+  if (lane == 0) {
 #pragma unroll
-      for (int n = 0; n < N; ++n) red[wave][n] = v[n];
-    }
-    __syncthreads();
+    for (int n = 0; n < N; ++n) red[threadIdx.x >> 6][n] = v[n];
+  }
+  __syncthreads();
 #pragma unroll
-    for (int n = 0; n < N; ++n) v[n] = red[first][n];
-#pragma unroll
-    for (int w = 1; w < CF::kPer; ++w) {
-#pragma unroll
-      for (int n = 0; n < N; ++n) v[n] = v[n] + red[first + w][n];
-    }
+  for (int n = 0; n < N; ++n) {
+    float s = slot < waves ? red[first + slot][n] : 0.0f;
+    s = s + dpp_float<kDppXor1>(s);
+    s = s + dpp_float<kDppXor2>(s);
+    s = s + dpp_float<kDppHalfMirror>(s);
+    v[n] = s + dpp_float<kDppMirror>(s);
   }
 }
 
+__device__ __forceinline__ int uniform(int v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  return __builtin_amdgcn_readfirstlane(v);
+#else
+  return v;
+#endif
+}
+
+// Keeps a value as it lies in memory: without this the compiler converts the
+// weights once, outside the loop over rows, into twice the registers.
+template <int F32>
+__device__ __forceinline__ void keep_packed(Lane8<F32>& q) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  if constexpr (!F32) asm volatile("" : "+v"(q.w[0].x), "+v"(q.w[0].y), "+v"(q.w[0].z), "+v"(q.w[0].w));
+#endif
+}
+
 // ------------------------------------------------------------------ forward
-template <int X32, int T, int NV, int WG>
-__global__ __launch_bounds__(WG) void norm_fwd_kernel(NormFwdParams p) {
-  using CF = RowCfg<T, NV, WG>;
-  __shared__ float red[2][CF::kWaves][1];
-  const int t = threadIdx.x, tr = t % T;
-  const int64_t step = (int64_t)gridDim.x * CF::kRows;
+template <int X32, int W32, int NV, int MOST>
+__global__ __launch_bounds__(MOST) void norm_fwd_kernel(NormFwdParams p, Split split) {
+  __shared__ float red[2][16][1];
+  const int wave = uniform(threadIdx.x >> 6), side = wave / split.waves, first = side * split.waves;
+  const int tr = threadIdx.x - 64 * first, T = 64 * split.waves;
+  const int64_t step = (int64_t)gridDim.x * split.rows;
   const int64_t packed_c = (p.C + 127) & ~(int64_t)127;
   Lane8<X32> next[NV];
   const auto load = [&](int64_t r) {
@@ -63,26 +78,24 @@ __global__ __launch_bounds__(WG) void norm_fwd_kernel(NormFwdParams p) {
       next[i] = r < p.M && c < p.C ? lane8_load<X32>(p.x, r * p.ldx + c) : lane8_zero<X32>();
     }
   };
-  int64_t r = (int64_t)blockIdx.x * CF::kRows + t / T;
+  int64_t r = (int64_t)blockIdx.x * split.rows + side;
   load(r);
-  // (the weights as they lie in memory would take half the registers in bf16,
-  // but a branch on their type for every row)
-  float gamma[NV][8], beta[NV][8];
+  // the weights as they lie in memory: in bf16 half the registers of floats
+  Lane8<W32> gamma[NV], beta[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int64_t c = 8 * (int64_t)(tr + T * i);
+    const uint32_t one = W32 ? 0x3f800000u : 0x3f803f80u;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      gamma[i][e] = 1.0f;
-      beta[i][e] = 0.0f;
-    }
+    for (int k = 0; k < (W32 ? 2 : 1); ++k) gamma[i].w[k] = make_uint4(one, one, one, one);
+    beta[i] = lane8_zero<W32>();
     if (c < p.C) {
-      if (p.gamma != nullptr) lane8_read(p.gamma, c, p.w_f32, gamma[i]);
-      if (p.beta != nullptr) lane8_read(p.beta, c, p.w_f32, beta[i]);
+      if (p.gamma != nullptr) gamma[i] = lane8_load<W32>(p.gamma, c);
+      if (p.beta != nullptr) beta[i] = lane8_load<W32>(p.beta, c);
     }
   }
-  // every thread group of the workgroup makes the same number of turns
-  for (int64_t r0 = (int64_t)blockIdx.x * CF::kRows; r0 < p.M; r0 += step, r += step) {
+  // every row of the workgroup makes the same number of turns
+  for (int64_t r0 = (int64_t)blockIdx.x * split.rows; r0 < p.M; r0 += step, r += step) {
     float v[NV][8], sum[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -91,7 +104,7 @@ __global__ __launch_bounds__(WG) void norm_fwd_kernel(NormFwdParams p) {
       for (int e = 0; e < 8; ++e) sum[0] = sum[0] + v[i][e];
     }
     load(r + step);
-    row_sums<CF>(sum, red[0]);
+    row_sums(sum, red[0], split.waves, first);
     const float mean = sum[0] * p.inv_c;
     float sq[1] = {0.0f};
 #pragma unroll
@@ -104,7 +117,7 @@ __global__ __launch_bounds__(WG) void norm_fwd_kernel(NormFwdParams p) {
         }
       }
     }
-    row_sums<CF>(sq, red[1]);
+    row_sums(sq, red[1], split.waves, first);
     const float rstd = 1.0f / __builtin_sqrtf(__builtin_fmaf(sq[0], p.inv_c, p.eps));
     const bool in_m = r < p.M;
     if (in_m && tr == 0) {
@@ -114,8 +127,13 @@ __global__ __launch_bounds__(WG) void norm_fwd_kernel(NormFwdParams p) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int64_t c = 8 * (int64_t)(tr + T * i);
+      float g[8], b[8];
+      keep_packed(gamma[i]);
+      keep_packed(beta[i]);
+      lane8_values<W32>(gamma[i], g);
+      lane8_values<W32>(beta[i], b);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = __builtin_fmaf(v[i][e] * rstd, gamma[i][e], beta[i][e]);
+      for (int e = 0; e < 8; ++e) v[i][e] = __builtin_fmaf(v[i][e] * rstd, g[e], b[e]);
       if (in_m && c < p.C && p.y != nullptr) lane8_store(p.y, r * p.ldy + c, p.y_f32, v[i]);
       if (p.row_codes != nullptr || p.saved_codes != nullptr) {
         // the packs take y rounded to bf16; columns past C are pad blocks: zeros
@@ -146,15 +164,20 @@ __global__ __launch_bounds__(WG) void norm_fwd_kernel(NormFwdParams p) {
 
 // ------------------------------------------------------------------ backward
 // With h = (x - mean) rstd and g = dy gamma: dx = rstd (g - mean(g) - h mean(g h)).
-template <int X32, int D32, int T, int NV, int WG>
-__global__ __launch_bounds__(WG) void norm_bwd_kernel(NormBwdParams p) {
-  using CF = RowCfg<T, NV, WG>;
-  // 1024 threads have 128 registers each: no room for the next row and gamma
-  constexpr bool kAhead = WG < 1024;
-  __shared__ float red[2][CF::kWaves][2];
-  __shared__ float part[CF::kRows > 1 ? 2 * CF::kMaxC : 1];
-  const int t = threadIdx.x, tr = t % T;
-  const int64_t step = (int64_t)gridDim.x * CF::kRows;
+// One row a turn and 1024 threads a workgroup (128 registers a thread): 16
+// wavefronts of one compute unit make one partial sum of dgamma and dbeta, so
+// that 256 of them, 2 C values each, are all that is written and read again.
+constexpr int kBwdMost = 1024, kBwdSideC = 4096;  // rows stand side by side up to this width
+
+template <int X32, int D32, int NV>
+__global__ __launch_bounds__(kBwdMost) void norm_bwd_kernel(NormBwdParams p, Split split) {
+  // two steps a thread leave no registers for the next row and gamma
+  constexpr bool kAhead = NV == 1;
+  __shared__ float red[2][16][2];
+  __shared__ __attribute__((aligned(16))) float part[NV == 1 ? 2 * kBwdSideC : 4];
+  const int wave = uniform(threadIdx.x >> 6), side = wave / split.waves, first = side * split.waves;
+  const int tr = threadIdx.x - 64 * first, T = 64 * split.waves;
+  const int64_t step = (int64_t)gridDim.x * split.rows;
   Lane8<X32> next_x[NV];
   Lane8<D32> next_d[NV];
   float next_mean = 0.0f, next_rstd = 0.0f;
@@ -170,7 +193,7 @@ __global__ __launch_bounds__(WG) void norm_bwd_kernel(NormBwdParams p) {
       next_d[i] = in ? lane8_load<D32>(p.dy, r * p.lddy + c) : lane8_zero<D32>();
     }
   };
-  int64_t r = (int64_t)blockIdx.x * CF::kRows + t / T;
+  int64_t r = (int64_t)blockIdx.x * split.rows + side;
   if constexpr (kAhead) load(r);
   float gamma[kAhead ? NV : 1][8], dgamma[NV][8], dbeta[NV][8];
   const auto load_gamma = [&](int i, float (&w)[8]) {
@@ -186,7 +209,7 @@ __global__ __launch_bounds__(WG) void norm_bwd_kernel(NormBwdParams p) {
     for (int e = 0; e < 8; ++e) dgamma[i][e] = dbeta[i][e] = 0.0f;
   }
   int turn = 0;
-  for (int64_t r0 = (int64_t)blockIdx.x * CF::kRows; r0 < p.M; r0 += step, r += step, turn ^= 1) {
+  for (int64_t r0 = (int64_t)blockIdx.x * split.rows; r0 < p.M; r0 += step, r += step, turn ^= 1) {
     if constexpr (!kAhead) load(r);
     float h[NV][8], g[NV][8], sum[2] = {0.0f, 0.0f};
     const float mean = next_mean, rstd = next_rstd;
@@ -209,47 +232,34 @@ __global__ __launch_bounds__(WG) void norm_bwd_kernel(NormBwdParams p) {
     }
     if constexpr (kAhead) load(r + step);
     if (p.dx == nullptr) continue;  // (uniform)
-    row_sums<CF>(sum, red[turn]);
+    float o[kAhead ? NV : 1][8];
+    const bool in_m = r < p.M;
+    const auto load_residual = [&](int i, float (&w)[8]) {
+      const int64_t c = 8 * (int64_t)(tr + T * i);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = 0.0f;
+      if (p.residual != nullptr && in_m && c < p.C) lane8_read(p.residual, r * p.ldr + c, p.dx_f32, w);
+    };
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) load_residual(i, o[i]);
+    }
+    row_sums(sum, red[turn], split.waves, first);
     const float m1 = sum[0] * p.inv_c, m2 = sum[1] * p.inv_c;
-    if (r < p.M) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int64_t c = 8 * (int64_t)(tr + T * i);
-        if (c < p.C) {
-          float o[8];
+    for (int i = 0; i < NV; ++i) {
+      const int64_t c = 8 * (int64_t)(tr + T * i);
+      float (&w)[8] = o[kAhead ? i : 0];
+      if constexpr (!kAhead) load_residual(i, w);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = 0.0f;
-          if (p.residual != nullptr) lane8_read(p.residual, r * p.ldr + c, p.dx_f32, o);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = __builtin_fmaf(rstd, __builtin_fmaf(-h[i][e], m2, g[i][e] - m1), o[e]);
-          lane8_store(p.dx, r * p.lddx + c, p.dx_f32, o);
-        }
-      }
+      for (int e = 0; e < 8; ++e) w[e] = __builtin_fmaf(rstd, __builtin_fmaf(-h[i][e], m2, g[i][e] - m1), w[e]);
+      if (in_m && c < p.C) lane8_store(p.dx, r * p.lddx + c, p.dx_f32, w);
     }
   }
   if (p.partials == nullptr) return;  // (uniform)
-  // the workgroup's partial sums: its thread groups' in order
+  // the workgroup's partial sums: its rows side by side in order
   float* const out = p.partials + (int64_t)blockIdx.x * 2 * p.C;
-  if constexpr (CF::kRows > 1) {
-    for (int k = 0; k < CF::kRows; ++k) {
-      if (t / T == k) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int c = 8 * (tr + T * i);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            part[c + e] = k == 0 ? dgamma[i][e] : part[c + e] + dgamma[i][e];
-            part[CF::kMaxC + c + e] = k == 0 ? dbeta[i][e] : part[CF::kMaxC + c + e] + dbeta[i][e];
-          }
-        }
-      }
-      __syncthreads();
-    }
-    for (int c = 4 * t; c < p.C; c += 4 * WG) {
-      *reinterpret_cast<float4*>(out + c) = *reinterpret_cast<const float4*>(part + c);
-      *reinterpret_cast<float4*>(out + p.C + c) = *reinterpret_cast<const float4*>(part + CF::kMaxC + c);
-    }
-  } else {
+  if (split.rows == 1) {  // (uniform)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int64_t c = 8 * (int64_t)(tr + T * i);
@@ -258,91 +268,127 @@ __global__ __launch_bounds__(WG) void norm_bwd_kernel(NormBwdParams p) {
         lane8_store(out, p.C + c, 1, dbeta[i]);
       }
     }
+    return;
+  }
+  if constexpr (NV == 1) {
+    const int c0 = 8 * tr;
+    for (int k = 0; k < split.rows; ++k) {
+      if (side == k && c0 < p.C) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          part[c0 + e] = k == 0 ? dgamma[0][e] : part[c0 + e] + dgamma[0][e];
+          part[kBwdSideC + c0 + e] = k == 0 ? dbeta[0][e] : part[kBwdSideC + c0 + e] + dbeta[0][e];
+        }
+      }
+      __syncthreads();
+    }
+    for (int c = 4 * threadIdx.x; c < p.C; c += 4 * blockDim.x) {
+      *reinterpret_cast<float4*>(out + c) = *reinterpret_cast<const float4*>(part + c);
+      *reinterpret_cast<float4*>(out + p.C + c) = *reinterpret_cast<const float4*>(part + kBwdSideC + c);
+    }
   }
 }
 
-// dgamma and dbeta from the partials [rows][2][C]: 64 columns a workgroup, its
-// four wavefronts taking every fourth row, their sums in wavefront order.
+// dgamma and dbeta from the partials [rows][2][C]: 32 columns a workgroup (whole
+// 128-byte lines), eight threads of four columns times 32 that take every 32nd
+// row and are added by a tree.
 __global__ __launch_bounds__(256) void norm_weights_kernel(const float* __restrict__ partials, int64_t rows, int64_t C,
                                                            float* __restrict__ dgamma, float* __restrict__ dbeta,
                                                            int accumulate) {
-  __shared__ float red[4][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t c = (int64_t)blockIdx.x * 64 + lane;  // of 2 C
-  float sum = 0.0f;
+  __shared__ float4 red[32][8];
+  const int quad = threadIdx.x & 7, slice = threadIdx.x >> 3;
+  const int64_t c = (int64_t)blockIdx.x * 32 + 4 * quad;  // of 2 C
+  float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const auto add = [](const float4& a, const float4& b) {
+    return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+  };
   if (c < 2 * C) {
 #pragma unroll 8
-    for (int64_t r = wave; r < rows; r += 4) sum = sum + partials[r * 2 * C + c];
+    for (int64_t r = slice; r < rows; r += 32) sum = add(sum, *reinterpret_cast<const float4*>(partials + r * 2 * C + c));
   }
-  red[wave][lane] = sum;
+  red[slice][quad] = sum;
   __syncthreads();
-  if (wave != 0 || c >= 2 * C) return;
-  const float total = ((red[0][lane] + red[1][lane]) + red[2][lane]) + red[3][lane];
-  float* const out = c < C ? dgamma : dbeta;
-  const int64_t at = c < C ? c : c - C;
-  if (out != nullptr) out[at] = accumulate ? out[at] + total : total;
+#pragma unroll
+  for (int half = 16; half > 0; half /= 2) {
+    if (slice < half) red[slice][quad] = add(red[slice][quad], red[slice + half][quad]);
+    __syncthreads();
+  }
+  if (slice != 0 || c >= 2 * C) return;
+  const float4 total = red[0][quad];
+  float* const out = c < C ? dgamma : dbeta;  // (C is a multiple of 4)
+  if (out == nullptr) return;
+  float4* const at = reinterpret_cast<float4*>(out + (c < C ? c : c - C));
+  *at = accumulate ? add(*at, total) : total;
 }
 
 // ------------------------------------------------------------------ launch
-template <int X32, int T, int NV, int WG>
+// NV steps of 512 values a wavefront, at most MOST threads a workgroup; no more
+// workgroups than PER a compute unit, so that the weights are loaded a few times
+// only (one turn each, 16 a compute unit, takes 4% to 15% longer).  Two steps are
+// the measured best from 1024 to 16384 columns: 8191 x 8192 bf16 with its MXFP8
+// pack 70 us, in one step (1024 threads) 78, in four 74; 4096 x 16384 70, in four
+// 77.
+template <int X32, int W32, int NV, int MOST, int PER>
 hipError_t fwd(const NormFwdParams& p, hipStream_t stream) {
-  const int64_t rows = WG / T, wanted = (p.M + rows - 1) / rows, most = (int64_t)cu_count() * (2048 / WG);
-  hipLaunchKernelGGL((norm_fwd_kernel<X32, T, NV, WG>), dim3((unsigned)(wanted < most ? wanted : most)), dim3(WG), 0,
-                     stream, p);
+  Split s;
+  s.waves = (int)((p.C + 512 * NV - 1) / (512 * NV));
+  s.rows = MOST / 64 / s.waves;
+  const int64_t wanted = (p.M + s.rows - 1) / s.rows, most = (int64_t)cu_count() * PER;
+  hipLaunchKernelGGL((norm_fwd_kernel<X32, W32, NV, MOST>), dim3((unsigned)(wanted < most ? wanted : most)),
+                     dim3(64 * s.waves * s.rows), 0, stream, p, s);
   return hipGetLastError();
 }
 
-template <int X32>
+template <int X32, int W32>
 hipError_t fwd_of(const NormFwdParams& p, hipStream_t stream) {
-  if (p.C <= 512) return fwd<X32, 64, 1, 256>(p, stream);
-  if (p.C <= 1024) return fwd<X32, 64, 2, 256>(p, stream);
-  if (p.C <= 2048) return fwd<X32, 128, 2, 256>(p, stream);
-  if (p.C <= 4096) return fwd<X32, 256, 2, 256>(p, stream);
-  if (p.C <= 8192) return fwd<X32, 512, 2, 512>(p, stream);
-  return fwd<X32, 1024, 2, 1024>(p, stream);
+  if (p.C <= 512) return fwd<X32, W32, 1, 256, 4>(p, stream);
+  if (p.C <= 4096) return fwd<X32, W32, 2, 256, 4>(p, stream);
+  if (p.C <= 8192) return fwd<X32, W32, 2, 512, 4>(p, stream);
+  return fwd<X32, W32, 2, 1024, 2>(p, stream);
 }
 
 constexpr int64_t kMostPartials = 256;
 
-int64_t bwd_rows_side_by_side(int64_t C) { return C <= 1024 ? 8 : C <= 2048 ? 4 : C <= 4096 ? 2 : 1; }
-
-template <int X32, int D32, int T, int NV, int WG>
-hipError_t bwd(const NormBwdParams& p, hipStream_t stream) {
-  hipLaunchKernelGGL((norm_bwd_kernel<X32, D32, T, NV, WG>), dim3((unsigned)norm_partial_rows(p.M, p.C)), dim3(WG), 0,
-                     stream, p);
-  return hipGetLastError();
+Split bwd_split(int64_t M, int64_t C) {
+  const int64_t width = C <= 512 * 16 ? 512 : 1024;
+  Split s;
+  s.waves = (int)((C + width - 1) / width);
+  // rows side by side: no more than leave every partial sum a workgroup
+  const int64_t fit = C <= kBwdSideC ? 16 / s.waves : 1, useful = (M + kMostPartials - 1) / kMostPartials;
+  s.rows = (int)(useful < 1 ? 1 : useful < fit ? useful : fit);
+  return s;
 }
 
 template <int X32, int D32>
-hipError_t bwd_of(const NormBwdParams& p, hipStream_t stream) {
-  if (p.C <= 512) return bwd<X32, D32, 64, 1, 512>(p, stream);
-  if (p.C <= 1024) return bwd<X32, D32, 64, 2, 512>(p, stream);
-  if (p.C <= 2048) return bwd<X32, D32, 128, 2, 512>(p, stream);
-  if (p.C <= 4096) return bwd<X32, D32, 256, 2, 512>(p, stream);
-  if (p.C <= 8192) return bwd<X32, D32, 512, 2, 512>(p, stream);
-  return bwd<X32, D32, 1024, 2, 1024>(p, stream);
+hipError_t bwd(const NormBwdParams& p, hipStream_t stream) {
+  const Split s = bwd_split(p.M, p.C);
+  const dim3 grid((unsigned)norm_partial_rows(p.M, p.C)), threads(64 * s.waves * s.rows);
+  if (p.C <= 512 * 16) hipLaunchKernelGGL((norm_bwd_kernel<X32, D32, 1>), grid, threads, 0, stream, p, s);
+  else hipLaunchKernelGGL((norm_bwd_kernel<X32, D32, 2>), grid, threads, 0, stream, p, s);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_norm_fwd(const NormFwdParams& p, int x_f32, hipStream_t stream) {
-  return x_f32 ? fwd_of<1>(p, stream) : fwd_of<0>(p, stream);
+  if (x_f32) return p.w_f32 ? fwd_of<1, 1>(p, stream) : fwd_of<1, 0>(p, stream);
+  return p.w_f32 ? fwd_of<0, 1>(p, stream) : fwd_of<0, 0>(p, stream);
 }
 
 int64_t norm_partial_rows(int64_t M, int64_t C) {
-  const int64_t side = bwd_rows_side_by_side(C), wanted = (M + side - 1) / side;
+  const int64_t rows = bwd_split(M, C).rows, wanted = (M + rows - 1) / rows;
   return wanted < kMostPartials ? wanted : kMostPartials;
 }
 
 hipError_t launch_norm_bwd(const NormBwdParams& p, int x_f32, int dy_f32, hipStream_t stream) {
-  if (x_f32) return dy_f32 ? bwd_of<1, 1>(p, stream) : bwd_of<1, 0>(p, stream);
-  return dy_f32 ? bwd_of<0, 1>(p, stream) : bwd_of<0, 0>(p, stream);
+  if (x_f32) return dy_f32 ? bwd<1, 1>(p, stream) : bwd<1, 0>(p, stream);
+  return dy_f32 ? bwd<0, 1>(p, stream) : bwd<0, 0>(p, stream);
 }
 
 hipError_t launch_norm_weights(const float* partials, int64_t rows, int64_t C, float* dgamma, float* dbeta,
                                int accumulate, hipStream_t stream) {
-  hipLaunchKernelGGL(norm_weights_kernel, dim3((unsigned)((2 * C + 63) / 64)), dim3(256), 0, stream, partials, rows, C,
-                     dgamma, dbeta, accumulate);
+  hipLaunchKernelGGL(norm_weights_kernel, dim3((unsigned)((2 * C + 31) / 32)), dim3(256), 0, stream,
+                     partials, rows, C, dgamma, dbeta, accumulate);
   return hipGetLastError();
 }
 

@@ -122,7 +122,7 @@ struct AdamItem {
   int32_t first;    // its first chunk
   int32_t g_f32;
 };
-constexpr int64_t kAdamChunk = 4096;  // elements a workgroup
+constexpr int64_t kAdamChunk = 2048;  // elements a workgroup
 inline int64_t adam_chunks(int64_t n) { return (n + kAdamChunk - 1) / kAdamChunk; }
 // The table on the device: the items, then of every chunk its item's place.
 inline int64_t adam_table_bytes(int64_t items, int64_t chunks) { return items * (int64_t)sizeof(AdamItem) + 4 * chunks; }
