@@ -1153,7 +1153,7 @@ int mx_head_loss_bwd(const mx_head_loss_bwd_args* args, void* stream) {
   d.C = a.dX;
   d.ldc = a.lddx;
   mx_gemm_act_args w = d;
-  w.M = a.V;  // (validated whole; launched piece by piece)
+  w.M = piece;
   w.N = a.K;
   w.K = Mp;
   w.A = a.Gc;
@@ -1165,16 +1165,19 @@ int mx_head_loss_bwd(const mx_head_loss_bwd_args* args, void* stream) {
   w.ldr = a.lddw;
   if (want_dx) {
     mx_gemm_act_args whole = d;
+    whole.M = 1;
     whole.K = up32(a.V);  // W's columns are one operand
     if ((st = validate_gemm_act(whole)) != MX_OK || (st = validate_gemm_act(d)) != MX_OK) return st;
   }
   if (want_dw && (st = validate_gemm_act(w)) != MX_OK) return st;
+  if (want_dw && !rows_fit(a.V, a.lddw)) return MX_ERR_INDEX_OVERFLOW;
   if (many && !aligned16(a.sums)) return MX_ERR_ALIGN;
   if (many && !threads_fit((a.M * (a.K / 8) + 255) / 256, 1, 256)) return MX_ERR_INDEX_OVERFLOW;
   if ((st = check_device()) != MX_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (a.M == 0) {  // the empty sum: K = 0
     if (!want_dw || a.accumulate) return MX_OK;
+    w.M = a.V;
     w.K = 0;
     return gemm_act_launch(w, s);
   }

@@ -191,6 +191,7 @@ __global__ __launch_bounds__(256) void head_join_kernel(GemmParams p, const Part
   Part all = {-__builtin_inff(), 0.0f};
   const int64_t y = m < M ? labels[m] : -1;
   const bool counts = y >= 0 && y < p.N;
+  const float logit = m < M ? label_logit[m] : 0.0f;  // (anything where there is no label)
   float dot = 0.0f;
   if (m < M) {
     if constexpr (REDO) {
@@ -199,7 +200,7 @@ __global__ __launch_bounds__(256) void head_join_kernel(GemmParams p, const Part
         for (int u = side; u < units; u += kSides) dot = dot + e4m3_unit(p, m, y, u);
       }
     }
-#pragma unroll 4
+#pragma unroll 8
     for (int64_t q = side; q < tiles; q += kSides) all = joined(all, parts[q * M + m]);
   }
   red[t] = all;
@@ -219,7 +220,6 @@ __global__ __launch_bounds__(256) void head_join_kernel(GemmParams p, const Part
   lse[m] = total;
   float l = 0.0f;
   if (counts) {
-    const float logit = label_logit[m];
     l = total - logit;
     if constexpr (REDO) {
       const float d = dots[t] - logit, q = exp2_hw(-l * kLog2e);
@@ -285,15 +285,17 @@ struct HeadGradParams : GemmParams {
     float* const tile = reinterpret_cast<float*>(smem) + wave * 32 * kPitch;
     const int limit = N - nw < CF::kWN ? (int)(N - nw) : CF::kWN;  // columns of this wavefront (may be <= 0)
     float top[CF::kMI], d[CF::kMI];
-    int at[CF::kMI];
+    int at[CF::kMI], end[CF::kMI];  // the label's column; columns from `end` on are zeros
 #pragma unroll
     for (int i = 0; i < CF::kMI; ++i) {
       const int64_t m = mw + 32 * i + lrow;
       const int64_t mc = m < M ? m : M - 1;
       const int64_t y = labels[mc];
       const bool counts = m < M && y >= 0 && y < classes;
-      top[i] = counts ? -lse[mc] * kLog2e : -__builtin_inff();  // no label: every exponential is 0
-      d[i] = counts ? dloss[mc * dloss_step] : 0.0f;
+      // (without a label everything is zeros, whatever the logits are)
+      end[i] = counts ? limit : 0;
+      top[i] = -lse[mc] * kLog2e;
+      d[i] = dloss[mc * dloss_step];
       const int64_t c = y - first - nw;
       at[i] = counts && c >= 0 && c < CF::kWN ? (int)c : -1;
     }
@@ -309,7 +311,7 @@ struct HeadGradParams : GemmParams {
           for (int q = 0; q < 4; ++q) {
             const float p = exp2_hw(__builtin_fmaf(acc[i][j][4 * e4 + q], kLog2e, top[i]));
             const float x = d[i] * (p - (at[i] == c + q ? 1.0f : 0.0f));
-            v[q] = c + q < limit ? x : 0.0f;
+            v[q] = c + q < end[i] ? x : 0.0f;
           }
           *reinterpret_cast<float4*>(tile + lrow * kPitch + c) = make_float4(v[0], v[1], v[2], v[3]);
         }
@@ -353,8 +355,8 @@ __global__ __launch_bounds__(tile_threads(BM, BN, kEpiOwn), OCC) void head_kerne
 template <int FMT, int BM, int BN, int OCC, class P>
 hipError_t launch_tiles(const P& p, hipStream_t stream) {
   const int64_t tiles = ((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
-  if (tiles >= (1ll << 31) / 512) return hipErrorInvalidValue;
   constexpr int kThreads = Cfg<FMT, BM, BN, kDense, kEpiOwn, OCC>::kThreads;
+  if (tiles >= (1ll << 32) / kThreads) return hipErrorInvalidValue;
   hipLaunchKernelGGL((head_kernel<FMT, BM, BN, OCC, P>), dim3((unsigned)tiles), dim3(kThreads), 0, stream, p);
   return hipGetLastError();
 }
@@ -452,9 +454,11 @@ hipError_t launch_head_loss(const HeadParams& h, int fmt, float* loss, float* ls
   if (e != hipSuccess) return e;
   const int width = tile_classes(tile);
   const int64_t tiles = (h.V + width - 1) / width;
-  // 16 tokens a workgroup read whole 128-byte lines of a tile's parts, where
-  // that leaves enough workgroups
-  return h.M >= 2048 ? launch_join<16>(p, fmt, tiles, loss, lse, stream) : launch_join<1>(p, fmt, tiles, loss, lse, stream);
+  // 16 tokens a workgroup read whole 128-byte lines of a tile's parts, where that
+  // leaves enough workgroups (333 tokens, 393 tiles: 4.8 us one by one, 5.2 four
+  // at a time)
+  if (h.M >= 2048) return launch_join<16>(p, fmt, tiles, loss, lse, stream);
+  return launch_join<1>(p, fmt, tiles, loss, lse, stream);
 }
 
 hipError_t launch_head_grad(const HeadParams& h, const HeadGradOut& o, int fmt, hipStream_t stream) {

@@ -847,8 +847,9 @@ def head_loss_bwd(a, b, Wc, Xc, M: int, V: int, K: int, fmt: int, scale_mode: in
 
 
 class AdamwItems:
-    """The tensors of adamw and their table on the device, written once: make it
-    anew when a tensor is replaced (it keeps the tensors alive)."""
+    """The tensors of adamw and their table on the device, written once, on
+    `stream`: make it anew when a tensor is replaced (it keeps the tensors
+    alive), and keep it until the steps that read it are done."""
 
     def __init__(self, items, stream=None):
         self.tensors = items = [dict(it) for it in items]
@@ -860,7 +861,11 @@ class AdamwItems:
         chunks, size = ctypes.c_int64(0), ctypes.c_int64(0)
         _check(lib().mx_adamw_table_size(array, self.n, ctypes.byref(chunks), ctypes.byref(size)), "mx_adamw_table_size")
         self.chunks = chunks.value
-        self.table = torch.empty(max(size.value, 16), dtype=torch.uint8, device="cuda")
+        # (of the stream that fills and first reads it, so that freeing it is in that stream's order)
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream)
+        with torch.cuda.stream(stream):
+            self.table = torch.empty(max(size.value, 16), dtype=torch.uint8, device="cuda")
         self.address = self.table.data_ptr()
         _check(lib().mx_adamw_table(array, self.n, self.address, _handle(stream, here)), "mx_adamw_table")
 

@@ -137,6 +137,16 @@ def test_head_loss_bwd_refusals(kw, want):
     assert mx.lib().mx_head_loss_bwd(ctypes.byref(head_bwd_args(**kw)), None) == want
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses: for the host's checks alone")
+def test_head_loss_bwd_sizes_that_fit():
+    """Only what is in memory at a time has to fit 2^31 bytes: Q(G) a piece, W whole, dW as far as its pitch reaches."""
+    L = mx.lib()
+    ok = dict(M=1 << 15, V=1 << 17, piece=1 << 10)  # M V bytes: 2^32
+    assert L.mx_head_loss_bwd(ctypes.byref(head_bwd_args(**ok)), None) == DEVICE
+    assert L.mx_head_loss_bwd(ctypes.byref(head_bwd_args(**{**ok, "piece": 1 << 16})), None) == OVERFLOW
+    assert L.mx_head_loss_bwd(ctypes.byref(head_bwd_args(**ok, lddw=1 << 44)), None) == OVERFLOW
+
+
 def adamw_item(**kw):
     return struct_of(mx.AdamwItem, dict(p=P[0], g=P[1], m=pk(2), v=pk(4), copy=P[6], n=100, state_bits=8), kw)
 
@@ -305,6 +315,30 @@ def test_layernorm_packs(M, C, fmt, mode, had):
     mx.layernorm_fwd(x, None, gamma, beta, row=only, fmt=fmt, scale_mode=mode, hadamard=had)
     for a, b in ((row, row2), (saved, saved2), (only, row)):
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@gpu
+def test_layernorm_packs_of_many_rows_and_other_outputs():
+    """Workgroups that take several rows; y in binary32 (the packs take it in bf16); a pitch; each output alone."""
+    rng = np.random.default_rng(17)
+    for M, C, fmt, mode, had in ((9000, 96, mx.E2M3, mx.FLOOR, True), (5001, 1056, mx.E2M1, mx.FLOOR, False),
+                                 (2500, 4128, mx.E4M3, mx.RCEIL, False)):
+        wide = tensor(rng, (M, C + 24), mx.F32, 1.0, 0.2)
+        x = wide[:, 8:8 + C]
+        beta = tensor(rng, (C,), mx.BF16)
+        y, row, saved = torch.empty(M, C, device="cuda"), mx.alloc_packed(M, C, fmt), mx.alloc_packed(M, C, mx.E4M3)
+        mx.layernorm_fwd(x, y, beta=beta, row=row, fmt=fmt, scale_mode=mode, hadamard=had, saved=saved)
+        check_norm(x, y, None, beta, None, None, 1e-5, mx.F32)
+        row2, saved2, alone = mx.alloc_packed(M, C, fmt), mx.alloc_packed(M, C, mx.E4M3), mx.alloc_packed(M, C, mx.E4M3)
+        mx.quantize_saved(M, C, fmt, mode, had, x=y.bfloat16(), row=row2)
+        mx.checkpoint_save(y.bfloat16(), saved2)
+        mx.layernorm_fwd(x, beta=beta, saved=alone)
+        for a, b in ((row, row2), (saved, saved2), (alone, saved2)):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        mean, rstd = torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+        mx.layernorm_fwd(x, mean=mean)
+        mx.layernorm_fwd(x, rstd=rstd)
+        check_norm(x, y, None, beta, mean, rstd, 1e-5, mx.F32)
 
 
 @gpu
@@ -746,6 +780,37 @@ def test_head_loss_bwd_pieces(fmt, mode, had):
 
 
 @gpu
+def test_head_loss_bwd_pitches_and_masked_nan():
+    """Gaps between the rows of dX and dW stay as they are; a token without label whose hidden state is not a number
+    changes no gradient of the others."""
+    rng = np.random.default_rng(19)
+    fmt, mode, had = FMTS[1]
+    M, V, K = 70, 300, 96
+    a, b, av, bv = integer_operands(rng, M, V, K, fmt)
+    labels = labels_of(rng, M, V)
+    labels[10] = -100
+    _, lse64, _ = loss64(av @ bv.T, labels)
+    lse = torch.from_numpy(lse64.astype(np.float32)).cuda()
+    dloss = torch.full((1,), 0.1, device="cuda")
+    wc, _ = columns(rng, V, K, fmt, mode, had, 0.05)
+    xc, _ = columns(rng, M, K, fmt, mode, had, 1.0)
+    dX, dW, Gr, Gc = grads(a, b, wc, xc, M, V, K, fmt, mode, had, labels, lse, dloss, 128)
+    bad = (a[0].clone(), a[1].clone())
+    bad[1][0, 10] = 255
+    loss2, lse2 = head_loss(bad, b, M, V, K, fmt, labels)
+    assert float(loss2[10]) == 0 and torch.isnan(lse2[10])
+    lse_bad = lse.clone()
+    lse_bad[10] = float("nan")
+    dl = dloss.expand(M).clone()
+    dl[10] = float("inf")
+    wide_x, wide_w = torch.full((M, K + 8), 3.0, dtype=torch.bfloat16, device="cuda"), torch.full((V + 1, K + 16), 4.0, device="cuda")
+    mx.head_loss_bwd(bad, b, wc, xc, M, V, K, fmt, mode, labels, lse_bad, dl, dX=wide_x[:, :K], dW=wide_w[:V, 8:8 + K],
+                     Gr=Gr, Gc=Gc, piece=128, sums=torch.empty(M, K, device="cuda"), hadamard=had)
+    assert torch.equal(wide_x[:, :K], dX) and torch.equal(wide_w[:V, 8:8 + K], dW)
+    assert (wide_x[:, K:] == 3).all() and (wide_w[V] == 4).all() and (wide_w[:, :8] == 4).all() and (wide_w[:, 8 + K:] == 4).all()
+
+
+@gpu
 def test_head_loss_bwd_without_tokens_or_labels():
     rng = np.random.default_rng(6)
     fmt, mode, had = FMTS[0]
@@ -1132,6 +1197,27 @@ def test_a_captured_step_is_the_eager_one():
         assert same_bits(eager.outputs(), captured.outputs())
         other.run()
     torch.cuda.synchronize()
+
+
+@gpu
+def test_a_stream_by_argument():
+    """The `stream` argument, and a table that lives no longer than its call."""
+    rng = np.random.default_rng(23)
+    s = torch.cuda.Stream()
+    x, p, g = tensor(rng, (64, 512), mx.BF16), tensor(rng, (4096,), mx.F32), tensor(rng, (4096,), mx.F32, 0.1)
+    want, want_p = torch.empty_like(x), p.clone()
+    mx.layernorm_fwd(x, want)
+    m, v = torch.zeros(4096, device="cuda"), torch.zeros(4096, device="cuda")
+    mx.adamw([{"p": want_p, "g": g, "m": m, "v": v}], **HYPER, step=1)
+    torch.cuda.synchronize()
+    for handle in (s, s.cuda_stream):
+        y, q = torch.empty_like(x), p.clone()
+        m, v = torch.zeros(4096, device="cuda"), torch.zeros(4096, device="cuda")
+        torch.cuda.synchronize()
+        mx.layernorm_fwd(x, y, stream=handle)
+        mx.adamw([{"p": q, "g": g, "m": m, "v": v}], **HYPER, step=1, stream=handle)
+        s.synchronize()
+        assert torch.equal(y, want) and torch.equal(q, want_p)
 
 
 @gpu
