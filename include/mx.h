@@ -888,7 +888,9 @@ int64_t mx_head_loss_work_bytes(int64_t M, int64_t V);
  *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
  *   p = p (1 - lr weight_decay)
  *       - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
- * in binary32, the factors formed in binary64.
+ * in binary32, the factors formed in binary64 and rounded once; m, v and sqrt(v)
+ * by one rounded operation after the other (beta1 m, (1 - beta1) g, their sum;
+ * beta2 v, ((1 - beta2) g) g, their sum; the root).
  *
  * The tensors are named once, in a table on the device: mx_adamw_table_size
  * gives its bytes and the number of chunks (of 2048 elements) in it,
@@ -910,7 +912,7 @@ int64_t mx_head_loss_work_bytes(int64_t M, int64_t V);
  *  States in 8 bits are rounded stochastically (the nearest code would never
  *  move: a step changes a mean by less than half a code).  With neighbours
  *  lo <= |x| / 2^X < hi in E4M3 and t = (|x| / 2^X - lo) / (hi - lo), the
- *  magnitude is hi iff r < floor(t 2^16); r is the low half (m) or the high half
+ *  magnitude is hi iff r + 1 < t 2^16; r is the low half (m) or the high half
  *  (v) of word i % 4 of Philox4x32-10 at counter (i/4 mod 2^32, i/4 div 2^32,
  *  tensor's place in `items`, t mod 2^32), key `seed` (low, high half), for
  *  element i: the same bits on every run, others on every step.  A block of 32

@@ -9,7 +9,9 @@
 // They are rounded stochastically: the nearest code would never move, as one
 // step changes a mean by 0.1% to 10% and half a step of E4M3 is 3% to 6%.
 // Everything else is binary32, and the update takes m and v before they are
-// rounded.
+// rounded.  m, v and sqrt(v) are formed by one rounded operation after the other,
+// without fused ones: which of two codes a value becomes hangs on its last bit,
+// and so it can be told from the formula alone.
 //
 // Bound by HBM: 16 bytes an element with bf16 gradients, 8-bit states and a bf16
 // copy (28 with binary32 states), each read and written once.  A thread takes
@@ -47,17 +49,17 @@ __global__ void adam_advance_kernel(AdamState* state, AdamHyper h, const float* 
 }
 
 // E4M3 code of x / 2^X given 2^-X (|x| <= 448 2^X), rounded by 16 random bits:
-// with neighbours lo <= |x| / 2^X < hi a step apart, hi iff r < floor(t 2^16),
-// t the share of the step above lo.  Exact: normal codes are the upper bits of
-// the binary32 pattern, below 2^-6 the steps are 2^-9.
+// with neighbours lo <= |x| / 2^X < hi a step apart, hi iff r + 1 < t 2^16, t the
+// share of the step above lo.  Exact: normal codes are the upper bits of the
+// binary32 pattern, below 2^-6 the steps are 2^-9.
 __device__ __forceinline__ uint32_t e4m3_sr_code(float x, float inv, uint32_t r) {
   const float a = __builtin_fabsf(x) * inv;
   const uint32_t b = __float_as_uint(a);
   const float u = a * 512.0f, low = __builtin_floorf(u);
   const bool normal = a >= 0x1p-6f;
   const uint32_t code = normal ? (b >> 20) - (120u << 3) : (uint32_t)low;
-  const uint32_t k = normal ? (b & 0xfffffu) >> 4 : (uint32_t)((u - low) * 65536.0f);
-  return code + (r < k ? 1u : 0u) + ((__float_as_uint(x) >> 24) & 0x80u);
+  const bool up = normal ? (b & 0xfffffu) > (r + 1u) << 4 : (u - low) * 65536.0f > (float)(r + 1u);
+  return code + (up ? 1u : 0u) + ((__float_as_uint(x) >> 24) & 0x80u);
 }
 
 // Eight values at element c of a tensor of n (zeros past its end), binary32 or
@@ -159,8 +161,8 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamParams all) {
   for (int e = 0; e < 8; ++e) {
     const bool in = c + e < n;
     const float x = g[e] * gs;
-    m[e] = in ? __builtin_fmaf(f.b1, m[e], f.g1 * x) : 0.0f;
-    v[e] = in ? __builtin_fmaf(f.b2, v[e], f.g2 * x * x) : 0.0f;
+    m[e] = in ? f.b1 * m[e] + f.g1 * x : 0.0f;
+    v[e] = in ? f.b2 * v[e] + f.g2 * x * x : 0.0f;
     root[e] = __builtin_sqrtf(v[e]);
     p[e] = __builtin_fmaf(-f.rate, m[e] / __builtin_fmaf(root[e], f.inv_root, f.eps), p[e] * f.decay);
   }

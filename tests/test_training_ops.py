@@ -994,9 +994,9 @@ def check_state8(packed, want, err, r16, n):
     ulp = 2.0 ** (np.maximum(ea - 1, -6) - 3)
     lo = np.floor(a / ulp)
     share = (a / ulp - lo) * 65536
-    code = (lo + (r16 < np.floor(share))) * ulp * s
+    code = (lo + (r16 + 1 < share)) * ulp * s
     got = np.abs(values8(packed, n))
-    unsure = np.abs(share - r16) <= 1 + 65536 * err / (ulp * s)
+    unsure = np.abs(share - (r16 + 1)) <= 65536 * err / (ulp * s)
     wrap = (share < 65536 * err / (ulp * s)) | (share > 65536 * (1 - err / (ulp * s)))
     assert ((got == code) | unsure | wrap).all()
     assert (np.abs(got - np.abs(want)) <= ulp * s * (1 + 1e-5)).all()
@@ -1033,6 +1033,39 @@ def test_adamw_8_bits(g_dtype, step, seed):
         words = philox64(np.arange((n + 3) // 4), i, step & 0xFFFFFFFF, seed).reshape(-1)[:n].astype(np.int64)
         check_state8(x["m"], wm, em, words & 0xFFFF, n)
         check_state8(x["v"], np.sqrt(wv), 4 * U * np.sqrt(wv), words >> 16, n)
+
+
+@gpu
+def test_adamw_states_bit_for_bit():
+    """m, v and the codes are what the operations one by one give in binary32 (numpy rounds each the same way)."""
+    rng = np.random.default_rng(77)
+    n, step, seed, f = 10000, 12, 99, np.float32
+    g = (rng.standard_normal(n) * 0.1).astype(f)
+    scale = f(0.75)
+    x = g * scale
+    b1, g1, b2, g2 = f(0.9), f(1 - 0.9), f(0.999), f(1 - 0.999)
+    m0, v0 = (rng.standard_normal(n) * 0.1).astype(f), (rng.standard_normal(n) * 0.1).astype(f) ** 2
+    d = lambda a: torch.from_numpy(a.copy()).cuda()  # noqa: E731
+    t = {"p": d(g), "g": d(g), "m": d(m0), "v": d(v0)}
+    gs = torch.full((1,), float(scale), device="cuda")
+    mx.adamw([t], **HYPER, step=step, grad_scale=gs)
+    assert np.array_equal(t["m"].cpu().numpy(), b1 * m0 + g1 * x)
+    assert np.array_equal(t["v"].cpu().numpy(), b2 * v0 + (g2 * x) * x)
+    t = {"p": d(g), "g": d(g), "m": state8_of(d(m0), n), "v": state8_of(d(np.sqrt(v0)), n)}
+    m0, u0 = values8(t["m"], n).astype(f), values8(t["v"], n).astype(f)
+    mx.adamw([t], **HYPER, step=step, seed=seed, grad_scale=gs)
+    words = philox64(np.arange(n // 4), 0, step, seed).reshape(-1).astype(np.int64)
+    for packed, want, r in ((t["m"], b1 * m0 + g1 * x, words & 0xFFFF),
+                            (t["v"], np.sqrt(b2 * (u0 * u0) + (g2 * x) * x), words >> 16)):
+        a = np.abs(np.pad(want.astype(np.float64), (0, -n % 32)).reshape(-1, 32))
+        mant, e = np.frexp(a.max(-1))
+        X = (e - 9 + (mant > 0.875))[:, None]
+        a = np.ldexp(a, -X)
+        ulp = 2.0 ** (np.maximum(np.frexp(a)[1] - 1, -6) - 3)
+        lo = np.floor(a / ulp)
+        up = np.pad(r, (0, -n % 32)).reshape(-1, 32) + 1 < (a / ulp - lo) * 65536
+        code = np.ldexp((lo + up) * ulp, X).reshape(-1)[:n]
+        assert np.array_equal(np.abs(values8(packed, n)), code)
 
 
 @gpu
