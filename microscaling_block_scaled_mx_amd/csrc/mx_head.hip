@@ -41,6 +41,17 @@ __device__ __forceinline__ float log2_hw(float x) {
 #endif
 }
 
+// a b, 0 where either is 0.
+__device__ __forceinline__ float zero_wins(float a, float b) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  float v;
+  asm("v_mul_legacy_f32 %0, %1, %2" : "=v"(v) : "v"(a), "v"(b));
+  return v;
+#else
+  return a * b;
+#endif
+}
+
 // Order of a wavefront's own LDS writes and reads across lanes (its LDS
 // instructions execute in order; the compiler must not move them).
 __device__ __forceinline__ void wave_lds_fence() {
@@ -283,38 +294,45 @@ struct HeadGradParams : GemmParams {
     const int64_t mw = m0 + wm * CF::kWM, nw = n0 + wn * CF::kWN;
     const int64_t packed_n = (N + 127) & ~(int64_t)127, packed_m = (M + 127) & ~(int64_t)127;
     float* const tile = reinterpret_cast<float*>(smem) + wave * 32 * kPitch;
-    const int limit = N - nw < CF::kWN ? (int)(N - nw) : CF::kWN;  // columns of this wavefront (may be <= 0)
+    const int limit = N - nw < CF::kWN ? (int)(N - nw) : CF::kWN;  // classes of this wavefront (may be <= 0)
     float top[CF::kMI], d[CF::kMI];
-    int at[CF::kMI], end[CF::kMI];  // the label's column; columns from `end` on are zeros
+    int at[CF::kMI];  // the label's column here, or -1
 #pragma unroll
     for (int i = 0; i < CF::kMI; ++i) {
       const int64_t m = mw + 32 * i + lrow;
       const int64_t mc = m < M ? m : M - 1;
       const int64_t y = labels[mc];
       const bool counts = m < M && y >= 0 && y < classes;
-      // (without a label everything is zeros, whatever the logits are)
-      end[i] = counts ? limit : 0;
       top[i] = -lse[mc] * kLog2e;
-      d[i] = dloss[mc * dloss_step];
+      d[i] = counts ? dloss[mc * dloss_step] : 0.0f;
       const int64_t c = y - first - nw;
       at[i] = counts && c >= 0 && c < CF::kWN ? (int)c : -1;
     }
 #pragma unroll
     for (int i = 0; i < CF::kMI; ++i) {
+      // G of the piece.  `plain`: no label and no end of the classes in it (most
+      // pieces).  A token without label has d = 0, whose products are 0 whatever
+      // the logits are (zero_wins).
+      const auto form = [&](auto plain) __attribute__((always_inline)) {
+        constexpr bool kPlain = decltype(plain)::value;
 #pragma unroll
-      for (int j = 0; j < CF::kNJ; ++j)
+        for (int j = 0; j < CF::kNJ; ++j)
 #pragma unroll
-        for (int e4 = 0; e4 < 4; ++e4) {
-          const int c = 32 * j + 8 * e4 + 4 * g;
-          float v[4];
+          for (int e4 = 0; e4 < 4; ++e4) {
+            const int c = 32 * j + 8 * e4 + 4 * g;
+            float v[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float p = exp2_hw(__builtin_fmaf(acc[i][j][4 * e4 + q], kLog2e, top[i]));
-            const float x = d[i] * (p - (at[i] == c + q ? 1.0f : 0.0f));
-            v[q] = c + q < end[i] ? x : 0.0f;
+            for (int q = 0; q < 4; ++q) {
+              float p = exp2_hw(__builtin_fmaf(acc[i][j][4 * e4 + q], kLog2e, top[i]));
+              if constexpr (!kPlain) p = at[i] == c + q ? p - 1.0f : p;
+              v[q] = zero_wins(d[i], p);
+              if constexpr (!kPlain) v[q] = c + q < limit ? v[q] : 0.0f;
+            }
+            *reinterpret_cast<float4*>(tile + lrow * kPitch + c) = make_float4(v[0], v[1], v[2], v[3]);
           }
-          *reinterpret_cast<float4*>(tile + lrow * kPitch + c) = make_float4(v[0], v[1], v[2], v[3]);
-        }
+      };
+      if (limit == CF::kWN && __builtin_amdgcn_ballot_w64(at[i] >= 0) == 0) form(std::true_type{});
+      else form(std::false_type{});
       wave_lds_fence();
       const int64_t m = mw + 32 * i + lrow, n = nw + 32 * g;
       if (q_row_codes != nullptr && m < M && n < packed_n) {

@@ -725,6 +725,15 @@ def linear_bwd_saved(M: int, N: int, K: int, dY, saved_x, Wc, fmt: int, scale_mo
 
 
 # ---------------------------------------------------------------- training operators
+def _floats(t, n: int, dev: int, what: str):
+    """Address of a contiguous float32 tensor of n elements, or 0."""
+    if t is None:
+        return 0
+    if t.dtype is torch.float32 and t.numel() == n and t.is_contiguous() and t.get_device() == dev >= 0:
+        return t.data_ptr()
+    return _matrix(t, 1, n, dev, what, (F32,))[0]  # (raises)
+
+
 def layernorm_fwd(x, y=None, gamma=None, beta=None, eps: float = 1e-5, mean=None, rstd=None, row=None, fmt: int = E4M3,
                   scale_mode: int = RCEIL, hadamard: bool = False, saved=None, stream=None):
     """mx_layernorm_fwd: y [M][C] = (x - mean) rstd gamma + beta (x, y each
@@ -741,8 +750,8 @@ def layernorm_fwd(x, y=None, gamma=None, beta=None, eps: float = 1e-5, mean=None
         w_dtype = b_dtype
     elif beta is not None and b_dtype != w_dtype:
         raise MXError(4, "layernorm_fwd: gamma and beta are of different types")
-    mp, _, _ = _matrix(mean, 1, M, dev, "layernorm_fwd mean", (F32,))
-    rp, _, _ = _matrix(rstd, 1, M, dev, "layernorm_fwd rstd", (F32,))
+    mp = _floats(mean, M, dev, "layernorm_fwd mean")
+    rp = _floats(rstd, M, dev, "layernorm_fwd rstd")
     args = _pack_layernorm_fwd(M, C, xp, ldx, gp, bp, yp, ldy, mp, rp, *_operand(row, M, C, fmt, dev, "layernorm_fwd row"),
                                *_operand(saved, M, C, E4M3, dev, "layernorm_fwd saved"), eps, x_dtype, y_dtype, w_dtype,
                                fmt, scale_mode, int(hadamard), 0)
@@ -768,11 +777,13 @@ def layernorm_bwd(dy, x, mean, rstd, dx=None, gamma=None, residual=None, dgamma=
     if residual is not None and dx is not None and r_dtype != dx_dtype:
         raise MXError(4, "layernorm_bwd: residual and dx are of different types")
     gp, _, w_dtype = _matrix(gamma, 1, C, dev, "layernorm_bwd gamma")
-    dgp, _, _ = _matrix(dgamma, 1, C, dev, "layernorm_bwd dgamma", (F32,))
-    dbp, _, _ = _matrix(dbeta, 1, C, dev, "layernorm_bwd dbeta", (F32,))
-    mp, _, _ = _matrix(mean, 1, M, dev, "layernorm_bwd mean", (F32,))
-    sp, _, _ = _matrix(rstd, 1, M, dev, "layernorm_bwd rstd", (F32,))
-    pp = _work(partials, 8 * C * lib().mx_layernorm_partial_rows(M, C), dev, "layernorm_bwd partials")
+    dgp = _floats(dgamma, C, dev, "layernorm_bwd dgamma")
+    dbp = _floats(dbeta, C, dev, "layernorm_bwd dbeta")
+    mp = _floats(mean, M, dev, "layernorm_bwd mean")
+    sp = _floats(rstd, M, dev, "layernorm_bwd rstd")
+    # (256 rows are enough for any number of tokens)
+    rows = 256 if partials is None or partials.nbytes >= 2048 * C else lib().mx_layernorm_partial_rows(M, C)
+    pp = _work(partials, 8 * C * rows, dev, "layernorm_bwd partials")
     args = _pack_layernorm_bwd(M, C, yp, lddy, xp, ldx, mp, sp, gp, rp, ldr, op, lddx, dgp, dbp, pp, dy_dtype, x_dtype,
                                dx_dtype, w_dtype, int(accumulate), 0)
     _check(lib().mx_layernorm_bwd(args, _handle(stream, here)), "mx_layernorm_bwd")
@@ -784,7 +795,8 @@ def _work(t, nbytes: int, dev: int, what: str):
         return 0
     if not t.is_contiguous():
         raise MXError(2, f"{what}: tensor argument is a strided view; pass a contiguous tensor")
-    _need(t, nbytes, what)
+    if t.nbytes < nbytes:
+        _need(t, nbytes, what)  # (raises)
     if t.get_device() != dev or dev < 0:
         _refuse_device(t, dev, what)
     return t.data_ptr()
@@ -808,11 +820,11 @@ def head_loss(a, b, M: int, V: int, K: int, fmt: int, labels, loss, lse, work, s
     labels int64 [M] (outside [0, V): none); work: any tensor of at least
     head_loss_work_bytes(M, V)."""
     dev, here = _current()
-    lp, _, _ = _matrix(loss, 1, M, dev, "head_loss loss", (F32,))
-    sp, _, _ = _matrix(lse, 1, M, dev, "head_loss lse", (F32,))
+    lp = _floats(loss, M, dev, "head_loss loss")
+    sp = _floats(lse, M, dev, "head_loss lse")
     args = _pack_head_loss(M, V, K, fmt, 0, *_operand(a, M, K, fmt, dev, "head_loss A"),
                            *_operand(b, V, K, fmt, dev, "head_loss B"), _labels(labels, M, dev, "head_loss"), lp, sp,
-                           _work(work, lib().mx_head_loss_work_bytes(M, V), dev, "head_loss work"))
+                           _work(work, 4 * ((V + 127) // 128 * 2 * M + M), dev, "head_loss work"))
     _check(lib().mx_head_loss(args, _handle(stream, here)), "mx_head_loss")
 
 
@@ -828,11 +840,11 @@ def head_loss_bwd(a, b, Wc, Xc, M: int, V: int, K: int, fmt: int, scale_mode: in
     dev, here = _current()
     xp, lddx, _ = _matrix(dX, M, K, dev, "head_loss_bwd dX", (BF16,))
     wp, lddw, dw_dtype = _matrix(dW, V, K, dev, "head_loss_bwd dW")
-    sp, _, _ = _matrix(lse, 1, M, dev, "head_loss_bwd lse", (F32,))
+    sp = _floats(lse, M, dev, "head_loss_bwd lse")
     n = dloss.numel()
     if n != M and n != 1:
         raise MXError(2, f"head_loss_bwd dloss: {n} values for {M} tokens")
-    dp, _, _ = _matrix(dloss, 1, n, dev, "head_loss_bwd dloss", (F32,))
+    dp = _floats(dloss, n, dev, "head_loss_bwd dloss")
     Mp, Vp, part = _rows32(M), _rows32(V), min(piece, V)
     args = _pack_head_loss_bwd(M, V, K, fmt, scale_mode, int(hadamard), int(accumulate),
                                *_operand(a, M, K, fmt, dev, "head_loss_bwd A"),
@@ -906,8 +918,7 @@ def adamw(items, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float
         raise MXError(7, f"adamw: the tensors are on cuda:{items.device}, the current device is cuda:{dev}")
     args = _pack_adamw(lr, beta1, beta2, eps, weight_decay, step, seed & 0xFFFFFFFFFFFFFFFF,
                        _work(state, ADAMW_STATE_BYTES, dev, "adamw state"),
-                       _matrix(lr_device, 1, 1, dev, "adamw lr_device", (F32,))[0],
-                       _matrix(grad_scale, 1, 1, dev, "adamw grad_scale", (F32,))[0])
+                       _floats(lr_device, 1, dev, "adamw lr_device"), _floats(grad_scale, 1, dev, "adamw grad_scale"))
     _check(lib().mx_adamw(items.address, items.n, items.chunks, args, _handle(stream, here)), "mx_adamw")
 
 

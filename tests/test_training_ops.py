@@ -224,6 +224,15 @@ def test_sizes_of_work_buffers():
     assert L.mx_head_loss_work_bytes(-1, 5) == L.mx_head_loss_work_bytes(5, 0) == 0
 
 
+def test_binding_refuses_short_buffers():
+    """Sizes are checked before a device is looked for."""
+    f = torch.zeros
+    with pytest.raises(mx.MXError, match="partials"):
+        mx._work(f(3, 2, 64), 8 * 64 * 4, 0, "layernorm_bwd partials")
+    for M, V in ((1, 1), (5, 128), (7, 129), (300, 50257)):
+        assert mx.head_loss_work_bytes(M, V) == 4 * ((V + 127) // 128 * 2 * M + M)
+
+
 def test_binding_refuses_host_tensors():
     x = torch.zeros(4, 64)
     with pytest.raises(mx.MXError):
