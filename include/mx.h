@@ -829,7 +829,7 @@ int64_t mx_layernorm_partial_rows(int64_t M, int64_t C);
  * (E2M1 and E2M3 under FLOOR, E4M3 under RCEIL; hadamard as mx_quantize), so
  * that only one piece of Q(G) is ever in memory.
  *
- *  dloss        binary32, the gradient of each token's loss: [M] with
+ *  dloss        binary32 (4-byte aligned), the gradient of each token's loss: [M] with
  *               dloss_step = 1, or one value for all with 0.
  *  Wc           fmt operand [K] x K = V rounded up to 32 (columns of W); for dX.
  *  Xc           fmt operand [K] x K = M rounded up to 32 (columns of X); for dW.
