@@ -748,7 +748,9 @@ int mx_linear_bwd_saved(const mx_linear_bwd_args* args, void* stream);
  *               with accumulate = 1.
  *  partials     binary32 [mx_layernorm_partial_rows(M, C)][2][C], needed for
  *               dgamma and dbeta: sums of groups of rows, added in order by a
- *               second launch.  Calls that share it must be ordered.
+ *               second launch.  Calls that share it must be ordered.  (Few rows
+ *               are summed beside dx without it, in another order, unless dx lies
+ *               over dy or x.)
  * M = 0 sets dgamma and dbeta to zero unless accumulating.
  */
 #define MX_LAYERNORM_MAX_C 16384

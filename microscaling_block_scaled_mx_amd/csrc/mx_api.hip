@@ -364,6 +364,16 @@ int validate_norm_rows(const void* t, int64_t M, int64_t C, int64_t ld) {
   return t && !rows_fit(M, ld) ? MX_ERR_INDEX_OVERFLOW : MX_OK;
 }
 
+// Whether the bytes from the first to the last element of two such tensors meet.
+bool norm_rows_meet(const void* s, int64_t lds, int s_dtype, const void* t, int64_t ldt, int t_dtype, int64_t M,
+                    int64_t C) {
+  if (!s || !t) return false;
+  const uintptr_t a = (uintptr_t)s, b = (uintptr_t)t;
+  const uintptr_t na = (uintptr_t)((M - 1) * lds + C) * (s_dtype == MX_F32 ? 4 : 2);
+  const uintptr_t nb = (uintptr_t)((M - 1) * ldt + C) * (t_dtype == MX_F32 ? 4 : 2);
+  return a < b + nb && b < a + na;
+}
+
 int validate_layernorm_fwd(const mx_layernorm_fwd_args& a) {
   if (!dtype_ok(a.x_dtype) || !dtype_ok(a.y_dtype) || !dtype_ok(a.w_dtype)) return MX_ERR_FORMAT;
   if (packed_ok(a.row) == packed_none(a.row) || packed_ok(a.saved) == packed_none(a.saved)) return MX_ERR_NULL;
@@ -1073,7 +1083,11 @@ int mx_layernorm_bwd(const mx_layernorm_bwd_args* args, void* stream) {
   if (st != MX_OK) return st;
   if ((st = check_device()) != MX_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
+  // in one launch x and dy are read by more workgroups than those that write dx
   const bool weights = a.dgamma || a.dbeta;
+  const bool one = a.M > 0 && mx::norm_one_launch(a.M, a.C) &&
+                   !norm_rows_meet(a.dx, a.lddx, a.dx_dtype, a.x, a.ldx, a.x_dtype, a.M, a.C) &&
+                   !norm_rows_meet(a.dx, a.lddx, a.dx_dtype, a.dy, a.lddy, a.dy_dtype, a.M, a.C);
   if (a.M > 0) {
     mx::NormBwdParams p;
     memset(&p, 0, sizeof p);
@@ -1088,7 +1102,12 @@ int mx_layernorm_bwd(const mx_layernorm_bwd_args* args, void* stream) {
     p.ldr = a.ldr;
     p.dx = a.dx;
     p.lddx = a.lddx;
-    p.partials = weights ? a.partials : nullptr;
+    p.partials = weights && !one ? a.partials : nullptr;
+    if (one) {
+      p.dgamma = a.dgamma;
+      p.dbeta = a.dbeta;
+      p.accumulate = a.accumulate;
+    }
     p.M = a.M;
     p.C = a.C;
     p.inv_c = (float)(1.0 / (double)a.C);
@@ -1097,7 +1116,7 @@ int mx_layernorm_bwd(const mx_layernorm_bwd_args* args, void* stream) {
     st = launched(mx::launch_norm_bwd(p, a.x_dtype == MX_F32, a.dy_dtype == MX_F32, s));
     if (st != MX_OK) return st;
   }
-  if (!weights || (a.M == 0 && a.accumulate)) return MX_OK;
+  if (!weights || one || (a.M == 0 && a.accumulate)) return MX_OK;
   return launched(mx::launch_norm_weights(a.partials, mx::norm_partial_rows(a.M, a.C), a.C, a.dgamma, a.dbeta,
                                           a.accumulate, s));
 }

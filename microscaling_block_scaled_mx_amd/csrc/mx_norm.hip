@@ -173,15 +173,81 @@ __global__ __launch_bounds__(MOST) void norm_fwd_kernel(NormFwdParams p, Split s
 // with 512 partial sums 56, and 2 more for adding them.
 constexpr int kBwdMost = 1024, kBwdSideC = 4096;  // rows stand side by side up to this width
 
+// The weights' gradients of 32 columns straight from x and dy, for few rows:
+// lane l of a wavefront holds eight columns (l % 4) of every so manieth row, the
+// sixteen lanes of a column and then the wavefronts are added in a fixed order.
+template <int X32, int D32>
+__device__ __forceinline__ void weight_columns(const NormBwdParams& p, int64_t c0, float (*red)[64]) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6, waves = blockDim.x >> 6;
+  const int64_t c = c0 + 8 * (lane & 3);
+  float dgamma[8], dbeta[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) dgamma[e] = dbeta[e] = 0.0f;
+  if (c < p.C) {
+#pragma unroll 4
+    for (int64_t r = t >> 2; r < p.M; r += blockDim.x >> 2) {
+      float x[8], d[8];
+      lane8_values<X32>(lane8_load<X32>(p.x, r * p.ldx + c), x);
+      lane8_values<D32>(lane8_load<D32>(p.dy, r * p.lddy + c), d);
+      const float mean = p.mean[r], rstd = p.rstd[r];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        dgamma[e] = __builtin_fmaf(d[e], (x[e] - mean) * rstd, dgamma[e]);
+        dbeta[e] = dbeta[e] + d[e];
+      }
+    }
+  }
+  const auto sum16 = [](float v) {  // over the lanes with this one's l % 4
+    v = v + dpp_float<kDppRor8>(v);
+    v = v + dpp_float<kDppRor4>(v);
+    const uint32_t b = __float_as_uint(v);
+    const auto x = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+    const uint32_t h = __float_as_uint(__uint_as_float(x[0]) + __uint_as_float(x[1]));
+    const auto y = __builtin_amdgcn_permlane32_swap(h, h, false, false);
+    return __uint_as_float(y[0]) + __uint_as_float(y[1]);
+  };
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    dgamma[e] = sum16(dgamma[e]);
+    dbeta[e] = sum16(dbeta[e]);
+  }
+  if (lane < 4) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      red[wave][8 * lane + e] = dgamma[e];
+      red[wave][32 + 8 * lane + e] = dbeta[e];
+    }
+  }
+  __syncthreads();
+  if (t >= 64 || c0 + (t & 31) >= p.C) return;
+  float total = red[0][t];
+  for (int w = 1; w < waves; ++w) total = total + red[w][t];
+  float* const out = t < 32 ? p.dgamma : p.dbeta;
+  if (out == nullptr) return;
+  float* const at = out + c0 + (t & 31);
+  *at = p.accumulate ? *at + total : total;
+#endif
+}
+
+// `row_groups` workgroups take rows; those past them, if any, 32 columns of the
+// weights' gradients each.
 template <int X32, int D32, int NV>
-__global__ __launch_bounds__(kBwdMost) void norm_bwd_kernel(NormBwdParams p, Split split) {
+__global__ __launch_bounds__(kBwdMost) void norm_bwd_kernel(NormBwdParams p, Split split, int row_groups) {
+  if constexpr (NV == 1) {
+    if ((int)blockIdx.x >= row_groups) {
+      __shared__ float sums[16][64];
+      weight_columns<X32, D32>(p, (int64_t)(blockIdx.x - row_groups) * 32, sums);
+      return;
+    }
+  }
   // two steps a thread leave no registers for the next row and gamma
   constexpr bool kAhead = NV == 1;
   __shared__ float red[2][16][2];
   __shared__ __attribute__((aligned(16))) float part[NV == 1 ? 2 * kBwdSideC : 4];
   const int wave = uniform(threadIdx.x >> 6), side = wave / split.waves, first = side * split.waves;
   const int tr = threadIdx.x - 64 * first, T = 64 * split.waves;
-  const int64_t step = (int64_t)gridDim.x * split.rows;
+  const int64_t step = (int64_t)row_groups * split.rows;
   Lane8<X32> next_x[NV];
   Lane8<D32> next_d[NV];
   float next_mean = 0.0f, next_rstd = 0.0f;
@@ -367,9 +433,14 @@ Split bwd_split(int64_t M, int64_t C) {
 template <int X32, int D32>
 hipError_t bwd(const NormBwdParams& p, hipStream_t stream) {
   const Split s = bwd_split(p.M, p.C);
-  const dim3 grid((unsigned)norm_partial_rows(p.M, p.C)), threads(64 * s.waves * s.rows);
-  if (p.C <= 512 * 16) hipLaunchKernelGGL((norm_bwd_kernel<X32, D32, 1>), grid, threads, 0, stream, p, s);
-  else hipLaunchKernelGGL((norm_bwd_kernel<X32, D32, 2>), grid, threads, 0, stream, p, s);
+  int rows = (int)norm_partial_rows(p.M, p.C), columns = 0;
+  if (p.dgamma != nullptr || p.dbeta != nullptr) {
+    columns = (int)((p.C + 31) / 32);
+    if (p.dx == nullptr) rows = 0;  // the columns alone (the same threads, so the same sums)
+  }
+  const dim3 grid((unsigned)(rows + columns)), threads(64 * s.waves * s.rows);
+  if (p.C <= 512 * 16) hipLaunchKernelGGL((norm_bwd_kernel<X32, D32, 1>), grid, threads, 0, stream, p, s, rows);
+  else hipLaunchKernelGGL((norm_bwd_kernel<X32, D32, 2>), grid, threads, 0, stream, p, s, rows);
   return hipGetLastError();
 }
 
@@ -378,6 +449,15 @@ hipError_t bwd(const NormBwdParams& p, hipStream_t stream) {
 hipError_t launch_norm_fwd(const NormFwdParams& p, int x_f32, hipStream_t stream) {
   if (x_f32) return p.w_f32 ? fwd_of<1, 1>(p, stream) : fwd_of<1, 0>(p, stream);
   return p.w_f32 ? fwd_of<0, 1>(p, stream) : fwd_of<0, 0>(p, stream);
+}
+
+// Few rows: x and dy are read a second time from the caches rather than a second
+// launch waited for (device us in bf16, one launch against two: 64 x 4096 3.4 / 7.6,
+// 256 x 8192 7.4 / 16.2, 512 x 512 6.3 / 6.4, 512 x 8192 14.1 / 17.9, 1003 x 2080
+// 9.1 / 11.1, 1003 x 4096 14.3 / 14.3 and in binary32 19.0 / 16.6, 1536 x 2080
+// 12.9 / 11.7).
+bool norm_one_launch(int64_t M, int64_t C) {
+  return C <= 512 * 16 && (M <= 512 || (M <= 1024 && M * C <= (1 << 21)));
 }
 
 int64_t norm_partial_rows(int64_t M, int64_t C) {

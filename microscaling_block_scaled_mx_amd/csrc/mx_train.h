@@ -46,12 +46,19 @@ struct NormBwdParams {
   void* dx;               // [M][lddx] or nullptr
   int64_t lddx;
   float* partials;        // [norm_partial_rows][2][C], or nullptr: no weight gradients
+  float* dgamma;          // [C] or nullptr; either given: both formed in this launch (norm_one_launch)
+  float* dbeta;
+  int accumulate;
   int64_t M, C;
   float inv_c;
   int w_f32, dx_f32;
 };
-// Rows of partial weight gradients that the backward pass of M x C writes.
+// Rows of partial weight gradients that the backward pass of M x C writes, where
+// norm_one_launch does not hold.
 int64_t norm_partial_rows(int64_t M, int64_t C);
+// Whether the weights' gradients may be summed beside dx, without partial sums
+// (where dx lies apart from x and dy).
+bool norm_one_launch(int64_t M, int64_t C);
 hipError_t launch_norm_bwd(const NormBwdParams& p, int x_f32, int dy_f32, hipStream_t stream);
 // dgamma, dbeta [C] (either nullptr) from `rows` partials, in order; added to
 // what they hold where `accumulate`.

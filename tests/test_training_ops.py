@@ -484,10 +484,26 @@ def test_layernorm_bwd_many_rows(M, C):
 
 
 @gpu
-def test_layernorm_bwd_parts():
+@pytest.mark.parametrize("M,C", [(512, 136), (513, 4104), (1003, 776), (1024, 2048), (1024, 2056), (1025, 64), (300, 8192), (300, 8200)])
+def test_layernorm_bwd_one_launch_or_two(M, C):
+    """The sizes on both sides of the rule, with gradients that are added to."""
+    rng = np.random.default_rng(M + C)
+    x, dy, gamma, mean, rstd = norm_bwd_inputs(rng, M, C, mx.F32, mx.BF16, mx.F32)
+    dx = torch.empty(M, C, device="cuda")
+    start = torch.randn(C, device="cuda"), torch.randn(C, device="cuda")
+    for accumulate in (False, True):
+        dgamma, dbeta = start[0].clone(), start[1].clone()
+        mx.layernorm_bwd(dy, x, mean, rstd, dx, gamma, None, dgamma, dbeta, partials_of(M, C), accumulate=accumulate)
+        before = (f64(start[0]), f64(start[1])) if accumulate else (0.0, 0.0)
+        check_norm_bwd(dy, x, mean, rstd, gamma, None, dx, dgamma, dbeta, before)
+
+
+@gpu
+@pytest.mark.parametrize("M", [45, 1300])
+def test_layernorm_bwd_parts(M):
     """Each output alone gives the bits it has beside the others; dx over dy, x and the residual; pitches."""
     rng = np.random.default_rng(8)
-    M, C = 45, 136
+    C = 136
     x, dy, gamma, mean, rstd = norm_bwd_inputs(rng, M, C, mx.F32, mx.F32, mx.F32)
     residual = tensor(rng, (M, C), mx.F32)
     new = lambda: torch.empty(C, device="cuda")  # noqa: E731
@@ -501,7 +517,13 @@ def test_layernorm_bwd_parts():
     for which in range(3):
         t = [dy.clone(), x.clone(), residual.clone()]
         mx.layernorm_bwd(t[0], t[1], mean, rstd, t[which], gamma, t[2], g1, b1, partials_of(M, C))
-        assert torch.equal(t[which], dx) and torch.equal(g1, dgamma) and torch.equal(b1, dbeta)
+        assert torch.equal(t[which], dx)  # (the weights' sums may be in another order)
+        check_norm_bwd(dy, x, mean, rstd, gamma, residual, t[which], g1, b1)
+    # dx in the same buffer as dy and x, row by row beside them
+    both = torch.cat((dy, x, torch.zeros_like(x)), 1)
+    mx.layernorm_bwd(both[:, :C], both[:, C:2 * C], mean, rstd, both[:, 2 * C:], gamma, residual, g1, b1, partials_of(M, C))
+    assert torch.equal(both[:, 2 * C:], dx) and torch.equal(both[:, :C], dy) and torch.equal(both[:, C:2 * C], x)
+    check_norm_bwd(dy, x, mean, rstd, gamma, residual, both[:, 2 * C:], g1, b1)
     wide = torch.full((M, 160), 5.0, device="cuda")
     view = wide[:, 8:8 + C]
     view.copy_(dy)
