@@ -424,8 +424,10 @@ Split bwd_split(int64_t M, int64_t C) {
   const int64_t width = C <= 512 * 16 ? 512 : 1024;
   Split s;
   s.waves = (int)((C + width - 1) / width);
-  // rows side by side: no more than leave every partial sum a workgroup
-  const int64_t fit = C <= kBwdSideC ? 16 / s.waves : 1, useful = (M + kMostPartials - 1) / kMostPartials;
+  // rows side by side: no more than leave every partial sum a workgroup; in one
+  // launch at least 512 threads, for the workgroups that sum columns
+  const int64_t fit = C <= kBwdSideC ? 16 / s.waves : 1;
+  const int64_t useful = norm_one_launch(M, C) ? 8 / s.waves : (M + kMostPartials - 1) / kMostPartials;
   s.rows = (int)(useful < 1 ? 1 : useful < fit ? useful : fit);
   return s;
 }
@@ -446,18 +448,19 @@ hipError_t bwd(const NormBwdParams& p, hipStream_t stream) {
 
 }  // namespace
 
+// Few rows: x and dy are read a second time rather than a second launch waited
+// for.  Device us, one launch against two, operands from HBM: bf16 64 x 4096 3.6 /
+// 7.6, 256 x 8192 9.8 / 17.2, 512 x 512 5.0 / 6.6, 512 x 8192 15.2 / 19.3, 1003 x
+// 2080 10.2 / 12.5; binary32 512 x 8192 19.9 / 20.6, 1003 x 776 10.7 / 10.8, 1003 x
+// 2080 12.0 / 14.3.  Past that a column's one workgroup takes too long: with half
+// the threads 1003 x 4096 in binary32 took 19.0 / 16.6, 1536 x 2080 17.6 / 13.5.
+bool norm_one_launch(int64_t M, int64_t C) {
+  return C <= 512 * 16 && (M <= 512 || (M <= 1024 && M * C <= (1 << 21)));
+}
+
 hipError_t launch_norm_fwd(const NormFwdParams& p, int x_f32, hipStream_t stream) {
   if (x_f32) return p.w_f32 ? fwd_of<1, 1>(p, stream) : fwd_of<1, 0>(p, stream);
   return p.w_f32 ? fwd_of<0, 1>(p, stream) : fwd_of<0, 0>(p, stream);
-}
-
-// Few rows: x and dy are read a second time from the caches rather than a second
-// launch waited for (device us in bf16, one launch against two: 64 x 4096 3.4 / 7.6,
-// 256 x 8192 7.4 / 16.2, 512 x 512 6.3 / 6.4, 512 x 8192 14.1 / 17.9, 1003 x 2080
-// 9.1 / 11.1, 1003 x 4096 14.3 / 14.3 and in binary32 19.0 / 16.6, 1536 x 2080
-// 12.9 / 11.7).
-bool norm_one_launch(int64_t M, int64_t C) {
-  return C <= 512 * 16 && (M <= 512 || (M <= 1024 && M * C <= (1 << 21)));
 }
 
 int64_t norm_partial_rows(int64_t M, int64_t C) {
