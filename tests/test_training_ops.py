@@ -1164,6 +1164,99 @@ def test_adamw_offsets_past_32_bits():
     assert not p[100:-100].any()
 
 
+@gpu
+def test_adamw_leaves_what_lies_between_tensors():
+    """Tensors in one buffer, any lengths: the elements between them stay as they are, and so do the states' next groups."""
+    rng = np.random.default_rng(31)
+    sizes = [1, 5, 129, 300, 2049, 77]
+    starts = np.cumsum([0] + [(n + 127) // 128 * 128 + 128 for n in sizes])
+    total = int(starts[-1])
+    flat = {k: torch.full((total,), 7.0, device="cuda") for k in ("p", "m32", "v32")}
+    copy = torch.full((total,), 7.0, dtype=torch.bfloat16, device="cuda")
+    codes = {k: (torch.full((total // 128, 1, 128), 0x55, dtype=torch.uint8, device="cuda"),
+                 torch.full((total // 128, 1, 4), 0x55, dtype=torch.uint8, device="cuda")) for k in "mv"}
+    g = tensor(rng, (total,), 1, 0.1)
+    inside, groups = torch.zeros(total, dtype=torch.bool, device="cuda"), torch.zeros(total // 128, dtype=torch.bool, device="cuda")
+    items = []
+    for i, (at, n) in enumerate(zip(starts, sizes)):
+        at = int(at)
+        inside[at:at + n] = True
+        groups[at // 128:(at + n + 127) // 128] = True
+        cut = lambda t: (t[0][at // 128:(at + n + 127) // 128], t[1][at // 128:(at + n + 127) // 128])  # noqa: E731
+        items.append({"p": flat["p"][at:at + n], "g": g[at:at + n], "copy": copy[at:at + n], "m": cut(codes["m"]), "v": cut(codes["v"])})
+        for t in (*items[-1]["m"], *items[-1]["v"]):
+            t.zero_()
+    mx.adamw(items, **HYPER, step=1)
+    assert (flat["p"][~inside] == 7).all() and (copy[~inside] == 7).all() and not (flat["p"][inside] == 7).any()
+    for k in "mv":
+        assert (codes[k][0][~groups] == 0x55).all() and (codes[k][1][~groups] == 0x55).all()
+    items = [{"p": it["p"], "g": it["g"], "m": flat["m32"][int(a):int(a) + n], "v": flat["v32"][int(a):int(a) + n]}
+             for it, a, n in zip(items, starts, sizes)]
+    mx.adamw(items, **HYPER, step=1)
+    assert (flat["m32"][~inside] == 7).all() and (flat["v32"][~inside] == 7).all() and (flat["p"][~inside] == 7).all()
+    assert not (flat["m32"][inside] == 7).any()
+
+
+@gpu
+@pytest.mark.parametrize("M,V,K,piece", [(1, 129, 32, 128), (130, 300, 96, 128), (257, 700, 160, 512), (64, 33000, 32, 16384)])
+@pytest.mark.parametrize("fmt,mode,had", FMTS)
+def test_head_writes_no_further_than_its_buffers(M, V, K, piece, fmt, mode, had):
+    """Every buffer at its stated size inside a larger one whose rest stays as it is."""
+    rng = np.random.default_rng(M + V)
+    guard = []
+
+    def bytes_of(n):
+        t = torch.full((n + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+        guard.append(t[n:])
+        return t[:n]
+
+    def floats(*shape):
+        n = int(np.prod(shape))
+        return bytes_of(4 * n).view(torch.float32).reshape(shape)
+
+    def pack(rows, k):
+        return (bytes_of(mx.lib().mx_codes_bytes(fmt, rows, k)), bytes_of(mx.lib().mx_scales_bytes(rows, k)))
+
+    a, b, _, _ = integer_operands(rng, M, V, K, fmt)
+    wc, _ = columns(rng, V, K, fmt, mode, had, 0.05)
+    xc, _ = columns(rng, M, K, fmt, mode, had, 1.0)
+    labels = labels_of(rng, M, V)
+    up = lambda n: (n + 31) // 32 * 32  # noqa: E731
+    part = min(piece, V)
+    loss, lse, work = floats(M), floats(M), bytes_of(mx.head_loss_work_bytes(M, V))
+    dX, dW = bytes_of(2 * M * K).view(torch.bfloat16).reshape(M, K), floats(V, K)
+    Gr, Gc, sums = pack(M, up(part)), pack(part, up(M)), floats(M, K)
+    mx.head_loss(a, b, M, V, K, fmt, labels, loss, lse, work)
+    mx.head_loss_bwd(a, b, wc, xc, M, V, K, fmt, mode, labels, lse, torch.ones(1, device="cuda"), dX=dX, dW=dW, Gr=Gr, Gc=Gc,
+                     piece=piece, sums=sums, hadamard=had)
+    assert torch.isfinite(dX).all() and torch.isfinite(dW).all() and torch.isfinite(loss).all()
+    assert all((t == 0x5A).all() for t in guard)
+
+
+@gpu
+@pytest.mark.parametrize("M,C", [(3, 40), (9, 1032), (700, 4096), (1500, 72), (40, 16384)])
+def test_layernorm_writes_no_further_than_its_buffers(M, C):
+    rng = np.random.default_rng(C)
+    guard = []
+
+    def bytes_of(n):
+        t = torch.full((n + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+        guard.append(t[n:])
+        return t[:n]
+
+    floats = lambda *s: bytes_of(4 * int(np.prod(s))).view(torch.float32).reshape(s)  # noqa: E731
+    x, dy = tensor(rng, (M, C), mx.BF16), tensor(rng, (M, C), mx.BF16)
+    y, mean, rstd, dx = floats(M, C), floats(M), floats(M), floats(M, C)
+    row = (bytes_of(mx.lib().mx_codes_bytes(mx.E2M3, M, C)), bytes_of(mx.lib().mx_scales_bytes(M, C))) if C % 32 == 0 else None
+    saved = (bytes_of(mx.lib().mx_codes_bytes(mx.E4M3, M, C)), bytes_of(mx.lib().mx_scales_bytes(M, C))) if C % 32 == 0 else None
+    mx.layernorm_fwd(x, y, mean=mean, rstd=rstd, row=row, fmt=mx.E2M3, scale_mode=mx.FLOOR, hadamard=True, saved=saved)
+    dgamma, dbeta, partials = floats(C), floats(C), floats(mx.layernorm_partial_rows(M, C), 2, C)
+    mx.layernorm_bwd(dy, x, mean, rstd, dx, None, None, dgamma, dbeta, partials)
+    check_norm(x, y, None, None, mean, rstd, 1e-5, mx.F32)
+    check_norm_bwd(dy, x, mean, rstd, None, None, dx, dgamma, dbeta)
+    assert all((t == 0x5A).all() for t in guard)
+
+
 # ---------------------------------------------------------------- graphs, streams, a step together
 class Step:
     """A norm, the projection onto V classes and its loss, all gradients, and the step over gamma, beta and W."""
