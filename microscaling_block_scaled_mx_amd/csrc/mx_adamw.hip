@@ -14,11 +14,12 @@
 // and so it can be told from the formula alone.
 //
 // Bound by HBM: 16 bytes an element with bf16 gradients, 8-bit states and a bf16
-// copy (28 with binary32 states), each read and written once: 198 M elements in 575
-// us, 5.5 TB/s (a large copy 5.1); 148 tensors of up to 12288 elements 5.6 us.  A thread takes
-// eight consecutive elements, four lanes a block of 32; a workgroup finds its tensor
-// by two loads from a table on the device, which is written once (by launches
-// whose arguments carry the items, so that nothing is copied from the host).
+// copy (28 with binary32 states), each read and written once: 198 M elements in 560
+// to 593 us, 5.3 to 5.7 TB/s (a large copy 5.1); 148 tensors of up to 12288
+// elements 5.6 us.  A thread takes eight consecutive elements, four lanes a block
+// of 32; a workgroup finds its tensor by two loads from a table on the device,
+// which is written once (by launches whose arguments carry the items, so that
+// nothing is copied from the host).
 #include <math.h>
 
 #include "mx_lanes.h"

@@ -9,8 +9,8 @@
 // flight while the current ones are reduced, and the backward pass keeps its
 // share of dgamma and dbeta in registers until its rows are done.  Sums are
 // binary32.  8191 x 8192 in bf16 with its MXFP8 pack takes 71 us, 4.75 TB/s where
-// a large copy reaches 5.1; backward 8191 x 4096 in bf16 with a residual 60 us in
-// two launches, 4.5 TB/s; one row of 4096 4.7 us.
+// a large copy reaches 5.1; backward 8191 x 4096 in bf16 with a residual 61 us in
+// two launches, 4.4 TB/s; one row of 4096 4.7 us.
 #include "mx_lanes.h"
 #include "mx_train.h"
 
