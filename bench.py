@@ -45,7 +45,7 @@ METRIC = "MX GEMM TFLOP/s and % of MXFP4/6/8 MFMA peak (Flux-12B shapes); quanti
 # sources are those the counters were taken with
 GEMM_TRAFFIC = {"bytes_per_launch": 236.8e6,
                 "sources": ("mx_gemm.hip", "mx_gemm_tile.h", "mx_device.h", "mx_kernels.h", "mx_tuned.inc"),
-                "sources_sha1": "5ace4c786f99c88f9ffe997fb32a148dccae4d68"}
+                "sources_sha1": "cc20fc70eb428425b8e834a7cad1b17489a3b256"}
 # VALU wavefront-instructions per launch of the fused pack (rocprofv3
 # SQ_INSTS_VALU), valid while the pack sources are those it was counted with
 PACK_VALU = {"instructions_per_launch": 1.028e7, "sources": ("mx_pack.hip", "mx_device.h", "mx_kernels.h"),

@@ -296,10 +296,18 @@ __device__ __forceinline__ v8i lds_operand(const uint8_t* rowp, int r, int ks, i
   return v;
 }
 
-// Dense tile order: XCD-contiguous ranges, then groups of 8 tile rows.
+// Dense tile order: XCD-contiguous ranges, then groups of 8 tile rows.  ANY: such
+// ranges for any number of tiles (the first T % 8 one longer), not multiples of
+// eight alone.
+template <bool ANY = false>
 __device__ __forceinline__ void dense_tile(int bid, int tiles_m, int tiles_n, int& tm, int& tn) {
   const int T = tiles_m * tiles_n;
-  if ((T & 7) == 0) bid = (bid & 7) * (T >> 3) + (bid >> 3);
+  if constexpr (ANY) {
+    const int xcd = bid & 7, more = T & 7;
+    bid = xcd * (T >> 3) + (xcd < more ? xcd : more) + (bid >> 3);
+  } else if ((T & 7) == 0) {
+    bid = (bid & 7) * (T >> 3) + (bid >> 3);
+  }
   const int GM = 8;
   const int per_group = GM * tiles_n;
   const int group = bid / per_group;
@@ -357,7 +365,7 @@ __device__ __forceinline__ void gemm_tile(const P& p, int bx, int by, int bz, ui
       split = bx / (tiles_m * tiles_n);
       local = bx - split * (tiles_m * tiles_n);
     }
-    dense_tile(local, tiles_m, tiles_n, tm, tn);
+    dense_tile<EPI == kEpiOwn>(local, tiles_m, tiles_n, tm, tn);
   } else if constexpr (MODE == kRaggedM) {
     // 1-D grid of (row tile, column tile) pairs, column tiles fastest.  Each
     // XCD takes a contiguous range, so the tiles of one row panel (and of
