@@ -414,23 +414,29 @@ hipError_t launch_tiles(const P& p, hipStream_t stream) {
 }
 
 // The output tile.  128 x 128, two a compute unit, where 256 x 256 would leave
-// units idle (rounds of the chip by area, as mx_gemm_act picks them; 333 tokens,
-// 50257 classes, K = 800 in E2M1 / E2M3 / E4M3: 21 / 25 / 32 us, 256 x 256 26 /
-// 27 / 39; gradient 30 / 41 / 44 against 38 / 47 / 48; 8192 x 16384 x 4096: 282 /
-// 368 / 471, 256 x 256 246 / 298 / 486; gradient 319 / 432 / 606 against 291 /
-// 381 / 520).  E2M1, whose products are over soonest, over several rounds: 256 x
-// 128, two a unit, so that one tile's exponentials and packs run beside
-// another's products (8192 x 16384 x 2048: 137 us, gradient 173; 256 x 256 142
-// and 186; E2M3 178 and 259 against 166 and 249).
+// units idle (rounds of the chip by area, 128 x 128 15% more, as mx_gemm_act picks
+// them; 333 tokens, 50257 classes, K = 800 in E2M1 / E2M3 / E4M3: 19 / 22 / 27 us,
+// 256 x 256 24 / 26 / 33; gradient 26 / 36 / 38 against 33 / 43 / 45; 8192 x 16384
+// x 4096: 282 / 368 / 471, 256 x 256 246 / 298 / 486; gradient 319 / 432 / 606
+// against 291 / 381 / 520).  E2M1, whose products are over soonest, over several
+// rounds: 256 x 128, two a unit, so that one tile's exponentials and packs run
+// beside another's products, at 5% less a round than 256 x 256 (8192 x 16384 x
+// 2048: 137 us, gradient 173; 256 x 256 142 and 186; 1003 x 50257 x 800 36 and 54,
+// 128 x 128 41 and 59, 256 x 256 44 and 64; the other way round at 640 x 50257 x
+// 1024: 30 and 42, 128 x 128 29 and 40; in one round 1003 x 16384 x 8192 67 and 72,
+// 256 x 256 65 and 71; E2M3 at 8192 x 16384 x 2048 178 and 259 against 166 and 249).
 enum Tile { kTile128, kTile256x128, kTile256 };
 Tile pick_tile(int fmt, int64_t M, int64_t N) {
   const int64_t cus = cu_count();
-  const int64_t t256 = ((M + 255) / 256) * ((N + 255) / 256), t128 = ((M + 127) / 128) * ((N + 127) / 128);
-  const int64_t rest = t128 % (2 * cus);  // a last round of at most one tile per unit takes 2/3 of a full one
-  const int64_t cost256 = (t256 + cus - 1) / cus * 65536;
-  const int64_t cost128 = (t128 / (2 * cus) * 32768 + (rest == 0 ? 0 : rest <= cus ? 22000 : 32768)) * 115 / 100;
-  if (cost256 > cost128) return kTile128;
-  return fmt == kE2M1 && t256 > cus ? kTile256x128 : kTile256;
+  const auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+  // two a unit: a last round of at most one tile per unit takes 2/3 of a full one
+  const auto pairs = [&](int64_t t, int64_t round) {
+    const int64_t rest = t % (2 * cus);
+    return t / (2 * cus) * round + (rest == 0 ? 0 : rest <= cus ? round * 2 / 3 : round);
+  };
+  const int64_t t256 = tiles(256, 256), cost128 = pairs(tiles(128, 128), 32768) * 115 / 100;
+  if (fmt == kE2M1 && t256 > cus) return pairs(tiles(256, 128), 65536) * 95 / 100 > cost128 ? kTile128 : kTile256x128;
+  return (t256 + cus - 1) / cus * 65536 > cost128 ? kTile128 : kTile256;
 }
 int tile_classes(Tile t) { return t == kTile256 ? 256 : 128; }
 
