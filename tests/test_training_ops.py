@@ -775,6 +775,16 @@ def test_head_loss_bwd(M, V, K, fmt, mode, had):
     assert (f64(dX)[~ok] == 0).all()
 
 
+# tiles of each size, in numbers that are no multiple of eight: 123 and 252 of 128 x 128, 249 of 256 x 256, 644 of 256 x 128
+# (E2M1 alone; the other formats take 1288 of 128 x 128 there); and tokens enough for the join of sixteen a workgroup
+@gpu
+@pytest.mark.parametrize("fmt,mode,had", FMTS)
+@pytest.mark.parametrize("M,V,K", [(333, 5200, 160), (750, 5300, 32), (700, 21000, 32), (1003, 20500, 32), (2100, 700, 160)])
+def test_head_tiles(M, V, K, fmt, mode, had):
+    test_head_loss(M, V, K, fmt)
+    test_head_loss_bwd(M, V, K, fmt, mode, had)
+
+
 @gpu
 @pytest.mark.parametrize("fmt,mode,had", FMTS)
 def test_head_loss_bwd_pieces(fmt, mode, had):
