@@ -751,7 +751,8 @@ int mx_linear_bwd_saved(const mx_linear_bwd_args* args, void* stream);
  *               second launch.  Calls that share it must be ordered.  (Few rows
  *               are summed beside dx without it, in another order, unless dx lies
  *               over dy or x.)
- * M = 0 sets dgamma and dbeta to zero unless accumulating.
+ * No other output may overlap an input or another output.  M = 0 sets dgamma and
+ * dbeta to zero unless accumulating.
  */
 #define MX_LAYERNORM_MAX_C 16384
 typedef struct {
